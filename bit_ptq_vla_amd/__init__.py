@@ -47,6 +47,7 @@ _TORCH_TO_QLIN = {torch.float16: QLIN_F16, torch.bfloat16: QLIN_BF16,
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
+_F32 = ctypes.c_float
 SIGNATURES = {
     "qlin_abi_version": [],
     "qlin_status_string": [_I32],
@@ -70,6 +71,8 @@ SIGNATURES = {
     "qlin_calibrate_composite": [_P, _I32, _I64, _I64, _P, _I32, _P, _P, _P, _I64, _P],
     "qlin_rotate_quant_act_composite": [_P, _I32, _I64, _I64, _I64, _P, _P, _P, _I32, _I32, _P, _P, _P, _P],
     "qlin_quantize_weights_composite": [_P, _I32, _I64, _I64, _P, _P, _P, _I32, _I32, _P, _P, _P, _P],
+    "qlin_add_rmsnorm_quant": [_P, _I32, _I64, _I64, _I64, _P, _I64, _P, _F32, _I32, _I32, _P, _P, _P, _P],
+    "qlin_add_rmsnorm": [_P, _I32, _I64, _I64, _I64, _P, _I64, _P, _F32, _P, _P, _P],
 }
 
 _lib = None
@@ -226,6 +229,87 @@ def _rows_arg(x: torch.Tensor, k: Optional[int]) -> int:
     if x.dim() != 2 or x.stride(1) != 1 or k > x.shape[1]:
         raise ValueError("x must be a row-major [m][>= k] tensor")
     return k
+
+
+def _on_device(fn, dev: torch.device, *args) -> int:
+    """fn(*args) with dev as the current device: launches go to the device
+    that holds the tensors, whatever the caller's current one is."""
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
+def _same_device(dev: torch.device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the call on {dev}")
+
+
+def _norm_args(x, weight, residual, residual_out):
+    """Checks shared by the residual + RMS norm calls; returns m, k, ldx, ldr
+    (a single row has no pitch of its own)."""
+    if x.dim() != 2 or x.stride(1) != 1:
+        raise ValueError("x must be a row-major [m][k] tensor")
+    _dev_tensor(x, "x")
+    m, k = x.shape
+    _same_device(x.device, weight=weight, residual=residual, residual_out=residual_out)
+    if weight.dtype != torch.float32 or weight.numel() != k or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous float32 [k] tensor")
+    ldx, ldr = (x.stride(0), 0) if m > 1 else (k, k)
+    for name, t in (("residual", residual), ("residual_out", residual_out)):
+        if t is None:
+            continue
+        if t.shape != x.shape or t.dtype != x.dtype or t.stride(1) != 1:
+            raise ValueError(f"{name} must be a row-major tensor of x's shape and type")
+        if m > 1:
+            if ldr and t.stride(0) != ldr:
+                raise ValueError("residual and residual_out need the same row pitch")
+            ldr = t.stride(0)
+    return m, k, ldx, ldr
+
+
+def qlin_add_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                           eps: float = 1e-6, had_block: int = 0, bits: int = 8,
+                           residual_out: Optional[torch.Tensor] = None,
+                           out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None
+                           ) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
+    """Codes and per-token scales of the RMS norm of r = x + residual (x, where
+    residual is None), after the block Hadamard; weight is float32 [k], the
+    norm's gamma times the next projection's inv_s.  r goes to residual_out
+    (which may be residual or x: in place); the third value returned is that
+    tensor, or None."""
+    m, k, ldx, ldr = _norm_args(x, weight, residual, residual_out)
+    if out is None:
+        xq = _codes(m, k, bits, x.device)
+        xs = torch.empty(m, dtype=torch.float32, device=x.device)
+    else:
+        xq, xs = out
+        _same_device(x.device, xq=xq, x_scale=xs)
+    _need(xq, m * code_row_bytes(k, bits), "xq")
+    _need(xs, m * 4, "x_scale")
+    st = _on_device(load().qlin_add_rmsnorm_quant, x.device, x.data_ptr(), _TORCH_TO_QLIN[x.dtype], m, k, ldx,
+                    _ptr(residual), ldr, weight.data_ptr(), eps, had_block, bits, _ptr(residual_out), xq.data_ptr(),
+                    xs.data_ptr(), _stream(x.device))
+    _check(st, "qlin_add_rmsnorm_quant")
+    return xq, xs, residual_out
+
+
+def qlin_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                     eps: float = 1e-6, residual_out: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """The RMS norm of r = x + residual in x's type, contiguous [m][k] (the
+    input of qlin_gemv_w4a16), and residual_out (or None)."""
+    m, k, ldx, ldr = _norm_args(x, weight, residual, residual_out)
+    y = out if out is not None else torch.empty((m, k), dtype=x.dtype, device=x.device)
+    if y.dtype != x.dtype:
+        raise ValueError("out must have x's type")
+    _same_device(x.device, out=y)
+    _need(y, m * k * y.element_size(), "out")
+    st = _on_device(load().qlin_add_rmsnorm, x.device, x.data_ptr(), _TORCH_TO_QLIN[x.dtype], m, k, ldx,
+                    _ptr(residual), ldr, weight.data_ptr(), eps, _ptr(residual_out), y.data_ptr(), _stream(x.device))
+    _check(st, "qlin_add_rmsnorm")
+    return y, residual_out
 
 
 def qlin_calibrate_step_scales(x: torch.Tensor, k: Optional[int] = None,

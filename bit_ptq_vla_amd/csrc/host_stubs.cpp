@@ -46,6 +46,11 @@ hipError_t launch_calibrate_fold(const void*, int, int64_t, int64_t, int64_t, bo
     return hipErrorNoBinaryForGpu;
 }
 
+hipError_t launch_add_rmsnorm(const void*, int, int64_t, int64_t, int64_t, const void*, int64_t, const float*, float,
+                              int, int, void*, void*, float*, hipStream_t) {
+    return hipErrorNoBinaryForGpu;
+}
+
 hipError_t launch_gemm(const GemmPlan&, const void*, const float*, const void*, const float*, int64_t, int64_t,
                        int64_t, bool, bool, void*, int, int32_t*, hipStream_t) {
     return hipErrorNoBinaryForGpu;

@@ -1,0 +1,286 @@
+// Residual addition -> RMS norm -> block Hadamard -> per-token quantization,
+// for gfx950: what stands between a layer's residual stream and its next
+// low-bit projection.
+//
+//   r = rne_T(x + res),   n_j = r_j w_j / sqrt(mean(r^2) + eps),
+//   v = n @ blockdiag(H_b / sqrt b),   x_scale = fp32(max|v| / qmax),
+//   code_j = rne(qmax v_j / max|v|)
+//
+// The codes do not depend on the row's norm or on 1/sqrt b: both cancel in
+// v_j / max|v|.  So one pass over the row serves: u = (r w) @ H (the +-1
+// transform) with its maximum and the sum of squares reduced together, codes
+// from u, and x_scale = max|u| / (qmax sqrt b rms).
+//
+// u is held in float64.  A 16-bit r times an fp32 w is exact there and the
+// transform's sums are off by a few 2^-53, so the codes are those of exact
+// arithmetic (ties to even) and equal a float64 reference's; the vector
+// float64 rate of this chip is its unpacked fp32 rate.  The sum of squares is
+// float64 too, so no fp32 row can overflow it.
+//
+// A row is held by g lanes (a power of two), lane t holding the 8 values from
+// 8 (c g + t) for chunk c.
+
+#include "code_pack.h"
+#include "device_common.h"
+#include "qlin_internal.h"
+
+namespace qlin {
+
+namespace {
+
+struct NormParams {
+    const void* x;
+    const void* res;     // or nullptr
+    void* res_out;       // r, or nullptr
+    const float* w;      // [k]
+    int64_t m, k, ldx, ldr;
+    float eps;
+    int g;               // lanes per row
+    int had_block;       // 0/1: none
+    int bits;            // 8, 4 or 6; 0: float output
+    void* q;             // codes, or y
+    float* scale;
+};
+
+// Lane (lane ^ D)'s double: its two halves by DPP where a pattern exists
+// (D = 1, 2, 8), else through the LDS crossbar.
+template <int D>
+__device__ __forceinline__ int lane_xor_i(int v) {
+    if constexpr (D == 1) return __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, false);
+    else if constexpr (D == 2) return __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, false);
+    else if constexpr (D == 8) return __builtin_amdgcn_mov_dpp(v, 0x128, 0xF, 0xF, false);   // row_ror:8
+    else if constexpr (D == 32) return __shfl_xor(v, 32, 64);
+    else return __builtin_amdgcn_ds_swizzle(v, (D << 10) | 0x1F);
+}
+template <int D>
+__device__ __forceinline__ double lane_xor_d(double v) {
+    return __hiloint2double(lane_xor_i<D>(__double2hiint(v)), lane_xor_i<D>(__double2loint(v)));
+}
+
+template <int D, int NCH>
+__device__ __forceinline__ void xlane_stage_d(double (&v)[NCH][8], int lane) {
+    const double sgn = (lane & D) ? -1.0 : 1.0;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[c][e] = fma(v[c][e], sgn, lane_xor_d<D>(v[c][e]));
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(void* p, const float f[8]) {
+    if constexpr (DT == F32) {
+        float4* o = static_cast<float4*>(p);
+        o[0] = make_float4(f[0], f[1], f[2], f[3]);
+        o[1] = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (DT == BF16)
+                w[i] = pk_bf16(f[2 * i], f[2 * i + 1]);
+            else
+                w[i] = f32_to_f16_bits(f[2 * i]) | (static_cast<uint32_t>(f32_to_f16_bits(f[2 * i + 1])) << 16);
+        }
+        *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ float round_to(float f) {
+    if constexpr (DT == BF16) return bf16_to_f32(f32_to_bf16_rne(f));
+    else if constexpr (DT == F16) return f16_bits_to_f32(f32_to_f16_bits(f));
+    else return f;
+}
+
+template <int DT, int NCH, int TPB, bool QUANT>
+__global__ __launch_bounds__(TPB) void add_rmsnorm_kernel(NormParams p) {
+    constexpr int ES = DT == F32 ? 4 : 2;
+    constexpr int NW = TPB / 64;
+    __shared__ double red[2][NW];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int g = p.g, t = tid & (g - 1);
+    const int b = p.had_block > 1 ? p.had_block : 1;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (TPB / g) + tid / g;
+    const bool row_ok = row < p.m;
+    const int64_t rr = row_ok ? row : p.m - 1;
+    const char* xrow = static_cast<const char*>(p.x) + rr * p.ldx * ES;
+    const char* rrow = static_cast<const char*>(p.res) + rr * p.ldr * ES;
+    char* orow = static_cast<char*>(p.res_out) + rr * p.ldr * ES;
+
+    bool ok[NCH];
+    int64_t col[NCH];
+    float r[NCH][8];
+    double ss = 0.0;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+        col[c] = (static_cast<int64_t>(c) * g + t) * 8;
+        ok[c] = col[c] < p.k;
+        if (!ok[c]) col[c] = 0;
+        load8<DT>(xrow + col[c] * ES, r[c]);
+        if (p.res) {
+            float a[8];
+            load8<DT>(rrow + col[c] * ES, a);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[c][e] = round_to<DT>(r[c][e] + a[e]);
+        }
+        if (!ok[c]) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[c][e] = 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fma(static_cast<double>(r[c][e]), static_cast<double>(r[c][e]), ss);
+    }
+    if (p.res_out && row_ok) {
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
+            if (ok[c]) store8<DT>(orow + col[c] * ES, r[c]);
+    }
+
+    double v[QUANT ? NCH : 1][8];
+    double top = 0.0;
+    if constexpr (QUANT) {
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) {
+            float w[8];
+            load8<F32>(p.w + col[c], w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[c][e] = static_cast<double>(r[c][e]) * static_cast<double>(w[e]);
+#pragma unroll
+            for (int h = 1; h < 8; h <<= 1) {
+                if (h < b) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        if ((e & h) == 0) {
+                            const double a0 = v[c][e], a1 = v[c][e + h];
+                            v[c][e] = a0 + a1;
+                            v[c][e + h] = a0 - a1;
+                        }
+                    }
+                }
+            }
+        }
+        if (b > 8) xlane_stage_d<1, NCH>(v, lane);
+        if (b > 16) xlane_stage_d<2, NCH>(v, lane);
+        if (b > 32) xlane_stage_d<4, NCH>(v, lane);
+        if (b > 64) xlane_stage_d<8, NCH>(v, lane);
+        if (b > 128) xlane_stage_d<16, NCH>(v, lane);
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmax(top, fabs(v[c][e]));
+    }
+
+    // the row's sum of squares and maximum: lanes (g >= 32), then waves
+    ss += lane_xor_d<1>(ss);
+    ss += lane_xor_d<2>(ss);
+    ss += lane_xor_d<4>(ss);
+    ss += lane_xor_d<8>(ss);
+    ss += lane_xor_d<16>(ss);
+    if (g > 32) ss += lane_xor_d<32>(ss);
+    if constexpr (QUANT) {
+        top = fmax(top, lane_xor_d<1>(top));
+        top = fmax(top, lane_xor_d<2>(top));
+        top = fmax(top, lane_xor_d<4>(top));
+        top = fmax(top, lane_xor_d<8>(top));
+        top = fmax(top, lane_xor_d<16>(top));
+        if (g > 32) top = fmax(top, lane_xor_d<32>(top));
+    }
+    if (g > 64) {
+        if (lane == 0) {
+            red[0][wave] = ss;
+            red[1][wave] = top;
+        }
+        __syncthreads();
+        const int wpr = g >> 6, first = (wave / wpr) * wpr;
+        ss = red[0][first];
+        top = red[1][first];
+        for (int i = 1; i < wpr; ++i) {
+            ss += red[0][first + i];
+            top = fmax(top, red[1][first + i]);
+        }
+    }
+    if (!row_ok) return;
+    const double rms = sqrt(ss / static_cast<double>(p.k) + static_cast<double>(p.eps));
+
+    if constexpr (QUANT) {
+        const double qmax = p.bits == 8 ? 127.0 : 7.0;
+        if (t == 0) {
+            const double root = sqrt(static_cast<double>(b));
+            // a row of zeros has scale 0 (also at eps = 0)
+            p.scale[row] = ss == 0.0 ? 0.f : static_cast<float>(top / (rms * root * qmax));
+        }
+        const double inv = top > 0.0 ? qmax / top : 0.0;
+        // fma(v, inv, M) with M = 1.5 * 2^52 rounds the product to an integer
+        // once, half to even, and leaves it in the low mantissa bits; |v| <= top
+        // keeps it on the grid.  inv and the product are off by 2^-45 at most
+        // for codes up to 127: a residual that close to a half (the window is
+        // far wider) is decided by the quotient itself.
+        constexpr double M = 6755399441055744.0;
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) {
+            uint32_t cb[8];
+            double worst = 0.0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const double qb = fma(v[c][e], inv, M);
+                worst = fmax(worst, fabs(fma(v[c][e], inv, M - qb)));
+                cb[e] = static_cast<uint32_t>(__double2loint(qb));
+            }
+            if (worst >= 0.5 - 1e-9) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    cb[e] = static_cast<uint32_t>(
+                        __double2loint((top > 0.0 ? rint(v[c][e] * qmax / top) : 0.0) + M));
+            }
+            if (ok[c]) store8_codes(p.bits, cb, p.q, row, p.k, col[c], lane);
+        }
+    } else {
+        const float inv = ss == 0.0 ? 0.f : static_cast<float>(1.0 / rms);
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) {
+            float w[8];
+            load8<F32>(p.w + col[c], w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[c][e] = r[c][e] * inv * w[e];
+            if (ok[c]) store8<DT>(static_cast<char*>(p.q) + (row * p.k + col[c]) * ES, r[c]);
+        }
+    }
+}
+
+template <int DT, int NCH, int TPB>
+hipError_t launch_tpb(const NormParams& p, hipStream_t st) {
+    const int64_t rpb = TPB / p.g;
+    const dim3 grid(static_cast<unsigned>((p.m + rpb - 1) / rpb));
+    if (p.bits)
+        add_rmsnorm_kernel<DT, NCH, TPB, true><<<grid, TPB, 0, st>>>(p);
+    else
+        add_rmsnorm_kernel<DT, NCH, TPB, false><<<grid, TPB, 0, st>>>(p);
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t launch_dt(NormParams p, hipStream_t st) {
+    int g = 32;
+    while (g < 1024 && g * 8 < p.k) g <<= 1;
+    p.g = g;
+    if (g <= 256) return launch_tpb<DT, 1, 256>(p, st);
+    if (g == 512) return launch_tpb<DT, 1, 512>(p, st);
+    if (p.k <= 8192) return launch_tpb<DT, 1, 1024>(p, st);
+    if (p.k <= 16384) return launch_tpb<DT, 2, 1024>(p, st);
+    return launch_tpb<DT, 4, 1024>(p, st);
+}
+
+}  // namespace
+
+hipError_t launch_add_rmsnorm(const void* x, int dtype, int64_t m, int64_t k, int64_t ldx, const void* res,
+                              int64_t ldr, const float* w, float eps, int had_block, int bits, void* res_out,
+                              void* q, float* scale, hipStream_t st) {
+    NormParams p{x, res, res_out, w, m, k, ldx, ldr, eps, 0, had_block, bits, q, scale};
+    switch (dtype) {
+        case F16: return launch_dt<F16>(p, st);
+        case BF16: return launch_dt<BF16>(p, st);
+        default: return launch_dt<F32>(p, st);
+    }
+}
+
+}  // namespace qlin

@@ -206,6 +206,41 @@ qlin_status composite_run(const void* x, qlin_dtype dt, int64_t rows, int64_t k,
                                                 as_stream(stream)));
 }
 
+// Checks and launch of the two residual + RMS norm entry points (bits 0: the
+// float output, no scale).
+qlin_status add_rmsnorm(const void* x, qlin_dtype dt, int64_t m, int64_t k, int64_t ldx, const void* res, int64_t ldr,
+                        const float* w, float eps, int32_t had_block, int32_t bits, void* res_out, void* q,
+                        float* scale, void* stream) {
+    if (m > 0 && (!x || !q || (bits && !scale))) return QLIN_ERR_NULL;
+    if (!w) return QLIN_ERR_NULL;
+    if (!is_float_in(dt)) return QLIN_ERR_DTYPE;
+    if (bits && !bits_ok(bits)) return QLIN_ERR_UNSUPPORTED;
+    if (!pow2_block_ok(had_block)) return QLIN_ERR_UNSUPPORTED;
+    if (!(eps >= 0.f) || eps > 3.402823466e38f) return QLIN_ERR_UNSUPPORTED;
+    if (m < 0 || m > 0x7FFFFFFF || k < 8 || (k % 8) != 0 || k > kMaxRowK) return QLIN_ERR_SHAPE;
+    if ((ldx % 8) != 0 || ldx < k) return QLIN_ERR_SHAPE;
+    if ((res || res_out) && ((ldr % 8) != 0 || ldr < k)) return QLIN_ERR_SHAPE;
+    if (!bits_k_ok(bits, k)) return QLIN_ERR_SHAPE;
+    if (had_block > 1 && (k % had_block) != 0) return QLIN_ERR_SHAPE;
+    if (!aligned16(x) || !aligned16(res) || !aligned16(res_out) || !aligned16(w) || !aligned16(q) || !aligned16(scale))
+        return QLIN_ERR_ALIGN;
+    const int64_t es = dtype_size(dt);
+    const int64_t xb = m > 0 ? ((m - 1) * ldx + k) * es : 0, rb = m > 0 ? ((m - 1) * ldr + k) * es : 0;
+    const Span outs[2] = {{q, bits ? code_bytes(m, k, bits) : m * k * es}, {scale, m * 4}};
+    const Span ins[4] = {{x, xb}, {res, rb}, {w, k * 4}, {res_out, rb}};
+    if (any_overlap(outs, 2, ins, 4)) return QLIN_ERR_ALIAS;
+    // r may replace the residual or x where it covers the same rows
+    const Span r = {res_out, rb};
+    if (overlap(r, ins[2])) return QLIN_ERR_ALIAS;
+    if (res_out != res && overlap(r, ins[1])) return QLIN_ERR_ALIAS;
+    if (!(res_out == x && ldx == ldr) && overlap(r, ins[0])) return QLIN_ERR_ALIAS;
+    if (m == 0) return QLIN_OK;
+    qlin_status st = check_device();
+    if (st != QLIN_OK) return st;
+    return map_err(qlin::launch_add_rmsnorm(x, dt, m, k, ldx, res, ldr, w, eps, had_block, bits, res_out, q, scale,
+                                            as_stream(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -297,6 +332,21 @@ qlin_status qlin_rotate_quant_act(const void* x, qlin_dtype x_dtype, int64_t m, 
     if (st != QLIN_OK) return st;
     return map_err(qlin::launch_rotate_quant(x, x_dtype, m, k, ldx, pre == QLIN_PRE_GEGLU, fold_inv_s,
                                              had_block, bits, xq, x_scale, as_stream(stream)));
+}
+
+qlin_status qlin_add_rmsnorm_quant(const void* x, qlin_dtype x_dtype, int64_t m, int64_t k, int64_t ldx,
+                                   const void* residual, int64_t ldr, const float* weight, float eps,
+                                   int32_t had_block, int32_t bits, void* residual_out, void* xq, float* x_scale,
+                                   void* stream) {
+    if (!bits_ok(bits)) return QLIN_ERR_UNSUPPORTED;
+    return add_rmsnorm(x, x_dtype, m, k, ldx, residual, ldr, weight, eps, had_block, bits, residual_out, xq, x_scale,
+                       stream);
+}
+
+qlin_status qlin_add_rmsnorm(const void* x, qlin_dtype x_dtype, int64_t m, int64_t k, int64_t ldx,
+                             const void* residual, int64_t ldr, const float* weight, float eps, void* residual_out,
+                             void* y, void* stream) {
+    return add_rmsnorm(x, x_dtype, m, k, ldx, residual, ldr, weight, eps, 0, 0, residual_out, y, nullptr, stream);
 }
 
 qlin_status qlin_calibrate_step_scales(const void* x, qlin_dtype x_dtype, int64_t m, int64_t k, int64_t ldx,

@@ -55,6 +55,12 @@ int64_t composite_calib_work_bytes(int64_t n, int64_t k, int b);
 hipError_t launch_calibrate_composite(const void* w, int dtype, int64_t n, int64_t k, const float* fold, int b,
                                       int32_t* perm, float* rot, void* work, hipStream_t st);
 
+// Residual addition, RMS norm and the next projection's quantizer (bits 8, 4
+// or 6), or the normalised row itself in x's type (bits 0, scale unused).
+hipError_t launch_add_rmsnorm(const void* x, int dtype, int64_t m, int64_t k, int64_t ldx, const void* res,
+                              int64_t ldr, const float* w, float eps, int had_block, int bits, void* res_out,
+                              void* q, float* scale, hipStream_t st);
+
 hipError_t launch_calibrate_fold(const void* x, int x_dtype, int64_t m, int64_t k, int64_t ldx,
                                  bool geglu, const void* w, int w_dtype, int64_t n, float* s,
                                  float* inv_s, hipStream_t st);

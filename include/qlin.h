@@ -162,6 +162,42 @@ qlin_status qlin_rotate_quant_act(const void* x, qlin_dtype x_dtype, int64_t m, 
                                   void* stream);
 
 /*
+ * Residual addition and root-mean-square norm in front of a projection: what
+ * leads from a layer's residual stream to the activation codes of the next
+ * integer GEMM (FoldQuantVLA abstract: dynamic per-token quantization of a
+ * projection's input), or to the 16-bit rows qlin_gemv_w4a16 reads.
+ *
+ *   r[m]    = round_T(x[m] + residual[m])         (x[m] when residual is NULL)
+ *   n[m][j] = r[m][j] * weight[j] / sqrt(mean_j(r[m][j]^2) + eps)
+ *
+ * qlin_add_rmsnorm_quant -- v = n @ blockdiag(H_b / sqrt(b)) row by row, then
+ *   x_scale[m] = fp32(max_j |v| / qmax), xq = rne(qmax * v / max_j |v|): the
+ *   codes are the rounded quotients of exact values (evaluated in float64,
+ *   ties to even), not of the rounded scale.  The channel fold of the next
+ *   projection goes into weight (gamma_j * inv_s_j).  A row whose v is zero
+ *   gives scale 0 and codes 0; a row that holds an infinity or a NaN gives a
+ *   NaN scale or codes without meaning, and leaves the other rows alone.
+ * qlin_add_rmsnorm -- y = round_T(n), contiguous [m][k] of x's type (fp32
+ *   arithmetic: two roundings before the last).
+ *
+ *   x         [m][ldx], x_dtype T F16/BF16/F32.
+ *   residual  [m][ldr] of the same type, or NULL.
+ *   residual_out  out [m][ldr]: r, or NULL.  May be residual itself, or x where
+ *             ldx == ldr: the update in place.  Any other overlap is an error.
+ *   weight    float[k].  eps >= 0, finite.
+ *   had_block, bits, xq, x_scale: as qlin_rotate_quant_act.
+ * Preconditions: m >= 0; 8 <= k <= 32768, k % 8 == 0 (k % 128 == 0 for E2M3);
+ * k % had_block == 0; ldx, ldr % 8 == 0 and >= k.  One launch; no workspace.
+ */
+qlin_status qlin_add_rmsnorm_quant(const void* x, qlin_dtype x_dtype, int64_t m, int64_t k, int64_t ldx,
+                                   const void* residual, int64_t ldr, const float* weight, float eps,
+                                   int32_t had_block, int32_t bits, void* residual_out, void* xq,
+                                   float* x_scale, void* stream);
+qlin_status qlin_add_rmsnorm(const void* x, qlin_dtype x_dtype, int64_t m, int64_t k, int64_t ldx,
+                             const void* residual, int64_t ldr, const float* weight, float eps,
+                             void* residual_out, void* y, void* stream);
+
+/*
  * Per-step static activation scales (Omega-QVLA technical summary,
  * Metodologia 2, "Scalatura delle Attivazioni DiT per Passo": a scale table
  * per denoising step, layer and channel, computed beforehand from

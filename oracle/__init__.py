@@ -25,6 +25,7 @@ Blocchi"; LoopQ abstract for plain RTN weights and the W4A16 weight-only form):
                   zigzag permutation of the input channels by weight norms,
                   per block R_j = U_j H_b / sqrt(b) with U_j the eigenvectors
                   of the block's weight Gram matrix
+  RMS norm        residual + norm + quantizer (layer_ref.py)
   per-step table  (Omega-QVLA "Scalatura delle Attivazioni DiT per Passo")
                   s_t[c] = max |rotated calibration activations| / qmax per
                   step; static codes v / s_t[c]; s_t folded into that step's
@@ -74,6 +75,10 @@ from .qlin_ref import (  # noqa: F401
     round_to_f16,
     round_output,
     qmax_of,
+)
+from .layer_ref import (  # noqa: F401
+    add_rmsnorm,
+    add_rmsnorm_quant,
 )
 from .compare import (  # noqa: F401
     compare_codes,
