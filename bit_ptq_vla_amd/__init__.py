@@ -72,6 +72,8 @@ SIGNATURES = {
     "qlin_rotate_quant_act_composite": [_P, _I32, _I64, _I64, _I64, _P, _P, _P, _I32, _I32, _P, _P, _P, _P],
     "qlin_quantize_weights_composite": [_P, _I32, _I64, _I64, _P, _P, _P, _I32, _I32, _P, _P, _P, _P],
     "qlin_add_rmsnorm_quant": [_P, _I32, _I64, _I64, _I64, _P, _I64, _P, _F32, _I32, _I32, _P, _P, _P, _P],
+    "qlin_rope_append_kv": [_P, _I32, _I64, _I64, _I32, _P, _I64, _I32, _I32, _P, _P, _P, _P, _I64, _P],
+    "qlin_rope_table": [_P, _I64, _I32, ctypes.c_double, ctypes.c_double, _P],
     "qlin_add_rmsnorm": [_P, _I32, _I64, _I64, _I64, _P, _I64, _P, _F32, _P, _P, _P],
 }
 
@@ -612,6 +614,138 @@ def qlin_gemv_w4a16(x: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor, gr
                              _stream(x.device))
     _check(st, "qlin_gemv_w4a16")
     return y
+
+
+class _KvCacheC(ctypes.Structure):
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("pages", _I64), ("page_size", _I32),
+                ("heads", _I32), ("head_dim", _I32)]
+
+
+class _KvBatchC(ctypes.Structure):
+    _fields_ = [("page_table", _P), ("table_ld", _I64), ("q_start", _P), ("kv_len", _P), ("prefix_len", _P),
+                ("batch", _I32), ("max_q", _I32), ("max_kv", _I32)]
+
+
+class KvCache:
+    """One layer's paged cache over tensors the caller owns (kept alive here):
+    k int8 [pages][heads][page][d], v int8 [pages][heads][d][page], k_scale and
+    v_scale float32 [pages][heads]."""
+
+    def __init__(self, k: torch.Tensor, k_scale: torch.Tensor, v: torch.Tensor, v_scale: torch.Tensor):
+        if k.dim() != 4 or v.dim() != 4 or v.shape != (k.shape[0], k.shape[1], k.shape[3], k.shape[2]):
+            raise ValueError("k must be [pages][heads][page][d] and v [pages][heads][d][page]")
+        for name, t, dt in (("k", k, torch.int8), ("v", v, torch.int8), ("k_scale", k_scale, torch.float32),
+                            ("v_scale", v_scale, torch.float32)):
+            if t.dtype != dt:
+                raise ValueError(f"{name} must be {dt}")
+            _need(t, 0, name)
+        _same_device(k.device, v=v, k_scale=k_scale, v_scale=v_scale)
+        if k_scale.shape != k.shape[:2] or v_scale.shape != k.shape[:2]:
+            raise ValueError("k_scale and v_scale must be [pages][heads]")
+        self.k, self.k_scale, self.v, self.v_scale = k, k_scale, v, v_scale
+        self.pages, self.heads, self.page_size, self.head_dim = k.shape
+        self.device = k.device
+        self._c = _KvCacheC(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), self.pages,
+                            self.page_size, self.heads, self.head_dim)
+        self._ref = ctypes.addressof(self._c)
+
+    @classmethod
+    def empty(cls, pages: int, page_size: int, heads: int, head_dim: int, device) -> "KvCache":
+        """A cache on new, uninitialised device memory (a page needs no clearing
+        before its first token)."""
+        i8 = dict(dtype=torch.int8, device=device)
+        f32 = dict(dtype=torch.float32, device=device)
+        return cls(torch.empty((pages, heads, page_size, head_dim), **i8), torch.empty((pages, heads), **f32),
+                   torch.empty((pages, heads, head_dim, page_size), **i8), torch.empty((pages, heads), **f32))
+
+
+class KvBatch:
+    """The sequences of one call, over int32 device tensors the caller owns
+    (kept alive here): page_table [batch][>= ceil(max_kv / page)], q_start
+    [batch + 1], kv_len [batch], prefix_len [batch] or None; max_q and max_kv
+    bound the new tokens and the length of any sequence."""
+
+    def __init__(self, page_table: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, max_q: int, max_kv: int,
+                 prefix_len: Optional[torch.Tensor] = None):
+        batch = kv_len.numel()
+        for name, t, n in (("page_table", page_table, 0), ("q_start", q_start, batch + 1), ("kv_len", kv_len, batch),
+                           ("prefix_len", prefix_len, batch)):
+            if t is None:
+                continue
+            _dev_tensor(t, name)
+            if t.dtype != torch.int32:
+                raise ValueError(f"{name} must be int32")
+            if n and (t.dim() != 1 or t.numel() != n or (n > 1 and t.stride(0) != 1)):
+                raise ValueError(f"{name} must hold {n} contiguous values")
+        if page_table.dim() != 2 or page_table.shape[0] != batch or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+            raise ValueError("page_table must be a row-major [batch][pages] tensor")
+        _same_device(kv_len.device, page_table=page_table, q_start=q_start, prefix_len=prefix_len)
+        self.page_table, self.q_start, self.kv_len, self.prefix_len = page_table, q_start, kv_len, prefix_len
+        self.batch, self.max_q, self.max_kv = batch, max_q, max_kv
+        self.device = kv_len.device
+        # what a row of the table holds, not its pitch, bounds max_kv
+        self.table_pages = page_table.shape[1]
+        self._c = _KvBatchC(page_table.data_ptr(), page_table.stride(0) if batch > 1 else self.table_pages,
+                            q_start.data_ptr(), kv_len.data_ptr(), _ptr(prefix_len), batch, max_q, max_kv)
+        self._ref = ctypes.addressof(self._c)
+
+    def check(self, cache: KvCache) -> None:
+        if self.device != cache.device:
+            raise ValueError(f"the batch is on {self.device}, the cache on {cache.device}")
+        if self.table_pages * cache.page_size < self.max_kv:
+            raise ValueError(f"page_table rows of {self.table_pages} pages do not hold max_kv = {self.max_kv} tokens")
+
+
+def _rows16(t: torch.Tensor, name: str, cols: int) -> int:
+    """Row pitch of a row-major [rows][cols] fp16 / bf16 tensor."""
+    if t.dim() != 2 or t.shape[1] != cols or t.stride(1) != 1:
+        raise ValueError(f"{name} must be a row-major [tokens][{cols}] tensor")
+    return t.stride(0) if t.shape[0] > 1 else -(-cols // 8) * 8
+
+
+def qlin_rope_table(positions: int, rot_dim: int, base: float = 10000.0, stretch: float = 1.0, device="cuda"
+                    ) -> torch.Tensor:
+    """float32 [positions][rot_dim]: the cosines, then the sines, of
+    p / stretch * base^(-2 i / rot_dim)."""
+    table = torch.empty((positions, rot_dim), dtype=torch.float32, device=device)
+    _dev_tensor(table, "device")
+    st = _on_device(load().qlin_rope_table, table.device, table.data_ptr(), positions, rot_dim, base, stretch,
+                    _stream(table.device))
+    _check(st, "qlin_rope_table")
+    return table
+
+
+def qlin_rope_append_kv(qkv: torch.Tensor, cache: KvCache, batch: KvBatch, heads_q: int,
+                        rope: Optional[torch.Tensor], interleaved: bool = False,
+                        positions: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None
+                        ) -> torch.Tensor:
+    """Turns q and k of qkv [tokens][(heads_q + 2 heads) d] by the rope table
+    [positions][rot_dim] (None: no rotation), appends k and v to the cache and
+    returns q [tokens][heads_q d].  positions: int32 [tokens] rows of the table
+    (default: the tokens' places in the cache)."""
+    d = cache.head_dim
+    ld = _rows16(qkv, "qkv", (heads_q + 2 * cache.heads) * d)
+    tokens = qkv.shape[0]
+    batch.check(cache)
+    if q_out is None:
+        q_out = torch.empty((tokens, heads_q * d), dtype=qkv.dtype, device=qkv.device)
+    ldq = _rows16(q_out, "q_out", heads_q * d)
+    if q_out.shape[0] != tokens or q_out.dtype != qkv.dtype:
+        raise ValueError("q_out must have qkv's rows and type")
+    rope_len = rot = 0
+    if rope is not None:
+        if rope.dim() != 2 or rope.dtype != torch.float32 or not rope.is_contiguous():
+            raise ValueError("rope must be a contiguous float32 [positions][rot_dim] tensor")
+        rope_len, rot = rope.shape
+    if positions is not None and (positions.dtype != torch.int32 or positions.numel() != tokens
+                                  or not positions.is_contiguous()):
+        raise ValueError("positions must be a contiguous int32 [tokens] tensor")
+    _same_device(cache.device, qkv=qkv, q_out=q_out, rope=rope, positions=positions)
+    st = _on_device(load().qlin_rope_append_kv, cache.device, qkv.data_ptr(), _TORCH_TO_QLIN.get(qkv.dtype, -1),
+                    tokens, ld, heads_q, _ptr(rope), rope_len, rot, int(interleaved), _ptr(positions), cache._ref,
+                    batch._ref, q_out.data_ptr(), ldq, _stream(cache.device))
+    _check(st, "qlin_rope_append_kv")
+    return q_out
 
 
 QLIN_STREAM_READ_SINK_WORDS = 4096

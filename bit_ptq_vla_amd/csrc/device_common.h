@@ -90,6 +90,26 @@ __device__ __forceinline__ void load8<F32>(const void* p, float f[8]) {
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
 
+// Eight floats rounded to the storage type, 16-byte aligned.
+template <int DT>
+__device__ __forceinline__ void store8(void* p, const float f[8]) {
+    if constexpr (DT == F32) {
+        float4* o = static_cast<float4*>(p);
+        o[0] = make_float4(f[0], f[1], f[2], f[3]);
+        o[1] = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (DT == BF16)
+                w[i] = pk_bf16(f[2 * i], f[2 * i + 1]);
+            else
+                w[i] = f32_to_f16_bits(f[2 * i]) | (static_cast<uint32_t>(f32_to_f16_bits(f[2 * i + 1])) << 16);
+        }
+        *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
 // fp32 product rounded on its own, never fused into a following add.  The
 // fold multiply feeds the first Hadamard butterfly; left to the compiler, it
 // becomes fma(x0, m0, x1 * m1) in some kernels and not in others, and

@@ -85,6 +85,16 @@ hipError_t launch_skinny_int(const void*, const float*, const void*, const float
     return hipErrorNoBinaryForGpu;
 }
 
+hipError_t launch_rope_append(const void*, int, int64_t, int, const float*, int64_t, int, int, const int32_t*,
+                              const KvIndex&, int8_t*, int8_t*, float*, float*, int, int, void*, int64_t,
+                              hipStream_t) {
+    return hipErrorNoBinaryForGpu;
+}
+
+hipError_t launch_rope_table(float*, int64_t, int, double, double, hipStream_t) {
+    return hipErrorNoBinaryForGpu;
+}
+
 hipError_t launch_stream_read(const void*, int64_t, uint32_t*, int64_t, hipStream_t) {
     return hipErrorNoBinaryForGpu;
 }

@@ -206,6 +206,40 @@ qlin_status composite_run(const void* x, qlin_dtype dt, int64_t rows, int64_t k,
                                                 as_stream(stream)));
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Shared checks of the calls on a paged cache.
+qlin_status kv_check(const qlin_kv_cache* c, const qlin_kv_batch* b, int64_t tokens, int32_t heads_q) {
+    if (!c || !b) return QLIN_ERR_NULL;
+    if (!c->k || !c->v || !c->k_scale || !c->v_scale) return QLIN_ERR_NULL;
+    if (b->batch > 0 && (!b->page_table || !b->q_start || !b->kv_len)) return QLIN_ERR_NULL;
+    if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64) return QLIN_ERR_UNSUPPORTED;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return QLIN_ERR_UNSUPPORTED;
+    if (c->pages < 1 || c->pages > 0x7FFFFFFF || c->heads < 1 || c->heads > 4096) return QLIN_ERR_SHAPE;
+    if (heads_q < 1 || heads_q > 65536 || heads_q % c->heads != 0) return QLIN_ERR_SHAPE;
+    if (tokens < 0 || tokens > 0x7FFFFFFF || b->batch < 0 || b->max_q < 0 || b->max_kv < 0) return QLIN_ERR_SHAPE;
+    if (b->table_ld < (static_cast<int64_t>(b->max_kv) + c->page_size - 1) / c->page_size) return QLIN_ERR_SHAPE;
+    if (b->table_ld > 0x7FFFFFFF) return QLIN_ERR_SHAPE;
+    if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_scale) || !aligned16(c->v_scale)) return QLIN_ERR_ALIGN;
+    if (!aligned4(b->page_table) || !aligned4(b->q_start) || !aligned4(b->kv_len) || !aligned4(b->prefix_len))
+        return QLIN_ERR_ALIGN;
+    return QLIN_OK;
+}
+
+// The call's index arrays as spans (4 of them).
+void kv_index_spans(const qlin_kv_cache* c, const qlin_kv_batch* b, Span* s) {
+    const int64_t n = b->batch, used = (static_cast<int64_t>(b->max_kv) + c->page_size - 1) / c->page_size;
+    s[0] = {b->page_table, n > 0 ? ((n - 1) * b->table_ld + used) * 4 : 0};
+    s[1] = {b->q_start, n > 0 ? (n + 1) * 4 : 0};
+    s[2] = {b->kv_len, n * 4};
+    s[3] = {b->prefix_len, n * 4};
+}
+
+qlin::KvIndex kv_index(const qlin_kv_cache* c, const qlin_kv_batch* b, int64_t tokens) {
+    return {b->page_table, b->table_ld, b->q_start, b->kv_len, b->prefix_len, tokens, c->pages, b->batch, b->max_q,
+            b->max_kv, c->page_size};
+}
+
 // Checks and launch of the two residual + RMS norm entry points (bits 0: the
 // float output, no scale).
 qlin_status add_rmsnorm(const void* x, qlin_dtype dt, int64_t m, int64_t k, int64_t ldx, const void* res, int64_t ldr,
@@ -550,6 +584,54 @@ qlin_status qlin_gemv_w4a16(const void* x, const void* wq, const void* w_scale, 
     qlin_status st = check_device();
     if (st != QLIN_OK) return st;
     return map_err(qlin::launch_gemv_w4a16(x, wq, w_scale, m, n, k, group, y, as_stream(stream)));
+}
+
+qlin_status qlin_rope_append_kv(const void* qkv, qlin_dtype dtype, int64_t tokens, int64_t ld, int32_t heads_q,
+                                const float* rope, int64_t rope_len, int32_t rot_dim, int32_t interleaved,
+                                const int32_t* positions, const qlin_kv_cache* cache, const qlin_kv_batch* batch,
+                                void* q_out, int64_t ldq, void* stream) {
+    qlin_status st = kv_check(cache, batch, tokens, heads_q);
+    if (st != QLIN_OK) return st;
+    if (tokens > 0 && (!qkv || !q_out)) return QLIN_ERR_NULL;
+    if (rot_dim > 0 && !rope) return QLIN_ERR_NULL;
+    if (dtype != QLIN_F16 && dtype != QLIN_BF16) return QLIN_ERR_DTYPE;
+    if (interleaved != 0 && interleaved != 1) return QLIN_ERR_UNSUPPORTED;
+    const int64_t d = cache->head_dim, wide = (static_cast<int64_t>(heads_q) + 2 * cache->heads) * d;
+    if (rot_dim < 0 || rot_dim > d || rot_dim % 16 != 0 || (rot_dim > 0 && rope_len < 1)) return QLIN_ERR_SHAPE;
+    if (ld % 8 != 0 || ld < wide || ldq % 8 != 0 || ldq < heads_q * d) return QLIN_ERR_SHAPE;
+    if (!aligned16(qkv) || !aligned16(q_out) || !aligned16(rope)) return QLIN_ERR_ALIGN;
+    if (!aligned4(positions)) return QLIN_ERR_ALIGN;
+    // one block per (page, head) of k and of v, then the q heads
+    const int64_t touched = qlin::kv_max_touched(batch->max_q, cache->page_size);
+    if (touched > 0 && static_cast<int64_t>(batch->batch) * cache->heads > (1LL << 30) / touched) return QLIN_ERR_SHAPE;
+    if (tokens * heads_q > (1LL << 33)) return QLIN_ERR_SHAPE;
+    const int64_t codes = cache->pages * cache->heads * cache->page_size * d, scales = cache->pages * cache->heads * 4;
+    const Span outs[5] = {{cache->k, codes}, {cache->v, codes}, {cache->k_scale, scales}, {cache->v_scale, scales},
+                          {q_out, tokens > 0 ? ((tokens - 1) * ldq + heads_q * d) * 2 : 0}};
+    Span ins[7] = {{qkv, tokens > 0 ? ((tokens - 1) * ld + wide) * 2 : 0}, {rope, rope_len * rot_dim * 4},
+                   {positions, tokens * 4}};
+    kv_index_spans(cache, batch, ins + 3);
+    if (any_overlap(outs, 5, ins, 7)) return QLIN_ERR_ALIAS;
+    if (tokens == 0 || batch->batch == 0 || batch->max_q == 0) return QLIN_OK;
+    st = check_device();
+    if (st != QLIN_OK) return st;
+    return map_err(qlin::launch_rope_append(qkv, dtype, ld, heads_q, rope, rope_len, rot_dim, interleaved, positions,
+                                            kv_index(cache, batch, tokens), cache->k, cache->v, cache->k_scale,
+                                            cache->v_scale, cache->heads, cache->head_dim, q_out, ldq,
+                                            as_stream(stream)));
+}
+
+qlin_status qlin_rope_table(float* table, int64_t positions, int32_t rot_dim, double base, double stretch,
+                            void* stream) {
+    if (!table) return QLIN_ERR_NULL;
+    if (!(base > 0.0) || !(base < 1e300) || !(stretch > 0.0) || !(stretch < 1e300)) return QLIN_ERR_UNSUPPORTED;
+    if (positions < 0 || positions > 0x7FFFFFFF || rot_dim < 2 || rot_dim % 2 != 0 || rot_dim > 1024)
+        return QLIN_ERR_SHAPE;
+    if (!aligned16(table)) return QLIN_ERR_ALIGN;
+    if (positions == 0) return QLIN_OK;
+    qlin_status st = check_device();
+    if (st != QLIN_OK) return st;
+    return map_err(qlin::launch_rope_table(table, positions, rot_dim, base, stretch, as_stream(stream)));
 }
 
 qlin_status qlin_stream_read(const void* src, int64_t bytes, uint32_t* sink, void* stream) {

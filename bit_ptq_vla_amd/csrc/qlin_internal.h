@@ -4,6 +4,8 @@
 #include <hip/hip_runtime_api.h>
 #include <stdint.h>
 
+#include "kv_index.h"
+
 namespace qlin {
 
 // Compute units of the current device (cached per device; 256 if unknown).
@@ -99,6 +101,13 @@ GemmPlan plan_gemm_f6(int64_t m, int64_t n, int64_t k, bool geglu);
 hipError_t launch_gemm_f6(const GemmPlan& plan, const void* xq, const float* x_scale, const void* wq,
                           const float* w_scale, int64_t m, int64_t n, int64_t k, void* y, int y_dtype, bool geglu,
                           hipStream_t st);
+
+// Rotary positions and the append to the paged cache; the rope table.
+hipError_t launch_rope_append(const void* qkv, int dtype, int64_t ld, int heads_q, const float* rope, int64_t rope_len,
+                              int rot, int interleaved, const int32_t* positions, const KvIndex& ix, int8_t* k,
+                              int8_t* v, float* ks, float* vs, int heads, int d, void* q_out, int64_t ldq,
+                              hipStream_t st);
+hipError_t launch_rope_table(float* table, int64_t positions, int rot, double base, double stretch, hipStream_t st);
 
 // Streaming read of bytes (a multiple of 16) at src; one word per block to sink.
 hipError_t launch_stream_read(const void* src, int64_t bytes, uint32_t* sink, int64_t sink_words, hipStream_t st);

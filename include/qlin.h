@@ -434,6 +434,86 @@ qlin_status qlin_gemv_w4a16(const void* x, const void* wq, const void* w_scale, 
                             int64_t n, int64_t k, int32_t group, void* y, void* stream);
 
 /*
+ * Paged key/value cache in 8 bits, and the attention over it: what stands
+ * between the q|k|v projection and the o projection of a layer.
+ *
+ * qlin_kv_cache -- one layer's cache.  A page holds page_size tokens of every
+ *   key/value head; each (page, head) of k and of v has one fp32 scale, and a
+ *   stored value is code * scale, codes int8 in [-127, 127].
+ *     k        int8 [pages][heads][page_size][head_dim]
+ *     v        int8 [pages][heads][head_dim][page_size]   (keys contiguous)
+ *     k_scale, v_scale  float [pages][heads]
+ *   page_size 16, 32 or 64; head_dim 64, 128 or 256.
+ * qlin_kv_batch -- the sequences of one call.  Sequence b's position j lies in
+ *   page page_table[b * table_ld + j / page_size] at j % page_size.  Its new
+ *   tokens are rows q_start[b] .. q_start[b + 1] - 1 of the call's token rows
+ *   and hold the last positions of its kv_len[b] (cached and new together).
+ *   The index arrays are int32 on the device, 4-byte aligned.
+ *   max_q, max_kv bound the new tokens and the length of any sequence (they
+ *   size the launch); table_ld >= ceil(max_kv / page_size).
+ *   prefix_len (or NULL): the query at position p sees the keys j < kv_len[b]
+ *   with j <= p or j < prefix_len[b]: causal without it, a prefix whose tokens
+ *   see each other with it, everything where it reaches kv_len.
+ *   What lies on the device cannot be refused: lengths are cut to their bounds
+ *   and a page number outside the pool counts as no page (its tokens are not
+ *   stored, its keys not seen).  A sequence may have no new tokens or no
+ *   tokens at all; rows of no sequence are left as they are.  Sequences may
+ *   share pages that they only read; a page that a call writes belongs to one.
+ */
+typedef struct {
+    int8_t* k;
+    int8_t* v;
+    float* k_scale;
+    float* v_scale;
+    int64_t pages;
+    int32_t page_size, heads, head_dim;
+} qlin_kv_cache;
+typedef struct {
+    const int32_t* page_table;
+    int64_t table_ld;
+    const int32_t* q_start;
+    const int32_t* kv_len;
+    const int32_t* prefix_len;
+    int32_t batch, max_q, max_kv;
+} qlin_kv_batch;
+
+/*
+ * qlin_rope_append_kv -- rotary positions on q and k, q out in its type, k and
+ * v into the cache.
+ *   qkv      [tokens][ld]: heads_q q heads, then cache->heads k heads, then as
+ *            many v heads, head_dim columns each; dtype F16 or BF16.
+ *   rope     float [rope_len][rot_dim]: row p holds rot_dim / 2 cosines, then
+ *            as many sines (qlin_rope_table, or any other scheme's table).
+ *            The first rot_dim values of a head turn, pair (a, b) with angle i:
+ *            (a cos - b sin, b cos + a sin); pairs (i, i + rot_dim / 2), or
+ *            (2i, 2i + 1) with interleaved = 1.  rot_dim 0: no rotation, rope
+ *            may be NULL; else a multiple of 16 up to head_dim.
+ *   positions int32 [tokens]: the rope row of each token; NULL: its place in
+ *            the cache.  Cut to 0 .. rope_len - 1.
+ *   q_out    out [tokens][ldq], heads_q * head_dim columns, dtype; fp32 products.
+ * Scales and codes, per (page, head), for k after its rotation and for v:
+ *   s = max(s_old, fp32(max |new values of the page| / 127)), s_old = 0 where
+ *   the call starts the page; new codes rne(x / s), codes already there
+ *   rne(c * s_old / s) where s > s_old.  All of it is evaluated in float64
+ *   from the stored inputs, so the codes are those of exact arithmetic.  An
+ *   infinity or a NaN does not enter the scale; they are stored as +-127 and 0.
+ *   Calling again with the same arguments changes nothing.
+ * Preconditions: tokens >= 0; heads_q a multiple of cache->heads; ld and ldq
+ * multiples of 8; outputs (q_out and the cache) overlap no input.  One launch.
+ *
+ * qlin_rope_table -- table[p][i] = cos(angle), table[p][rot_dim / 2 + i] =
+ * sin(angle), angle = p / stretch * base^(-2 i / rot_dim) in float64 (far
+ * positions keep their angle); stretch > 1 interpolates positions for a context
+ * that many times longer.  table: out float [positions][rot_dim]; rot_dim even.
+ */
+qlin_status qlin_rope_append_kv(const void* qkv, qlin_dtype dtype, int64_t tokens, int64_t ld, int32_t heads_q,
+                                const float* rope, int64_t rope_len, int32_t rot_dim, int32_t interleaved,
+                                const int32_t* positions, const qlin_kv_cache* cache, const qlin_kv_batch* batch,
+                                void* q_out, int64_t ldq, void* stream);
+qlin_status qlin_rope_table(float* table, int64_t positions, int32_t rot_dim, double base, double stretch,
+                            void* stream);
+
+/*
  * qlin_stream_read -- measurement aid, not a step of the projection: reads
  * `bytes` bytes at src once with 16-byte loads spread over the whole device
  * and writes the xor of the words a workgroup read to sink (one uint32 per

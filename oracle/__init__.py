@@ -79,6 +79,9 @@ from .qlin_ref import (  # noqa: F401
 from .layer_ref import (  # noqa: F401
     add_rmsnorm,
     add_rmsnorm_quant,
+    rope_table,
+    rope,
+    rope_append_kv,
 )
 from .compare import (  # noqa: F401
     compare_codes,

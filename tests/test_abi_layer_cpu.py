@@ -81,6 +81,166 @@ def test_add_rmsnorm_empty_is_ok(lib):
     assert norm(lib, m=0) == q.QLIN_OK
 
 
+# ---- paged cache descriptors
+
+I1, I2, I3, I4, R = 0x91000000, 0x92000000, 0x93000000, 0x94000000, 0x95000000   # index arrays, the rope table
+C1, C2, C3, C4 = 0x100000000, 0x200000000, 0x300000000, 0x300100000              # k, v, k_scale, v_scale
+
+
+def cache(k=C1, v=C2, ks=C3, vs=C4, pages=64, page=16, heads=2, d=64):
+    return q._KvCacheC(k, v, ks, vs, pages, page, heads, d)
+
+
+def batch(table=I1, ld=4, q_start=I2, kv_len=I3, prefix=None, n=3, max_q=7, max_kv=64):
+    return q._KvBatchC(table, ld, q_start, kv_len, prefix, n, max_q, max_kv)
+
+
+def refs(c, b):
+    return [None if x is None else q.ctypes.addressof(x) for x in (c, b)]
+
+
+KV_BAD = [
+    (dict(c=None), q.QLIN_ERR_NULL), (dict(b=None), q.QLIN_ERR_NULL),
+    (dict(c=cache(k=None)), q.QLIN_ERR_NULL), (dict(c=cache(vs=None)), q.QLIN_ERR_NULL),
+    (dict(b=batch(table=None)), q.QLIN_ERR_NULL), (dict(b=batch(q_start=None)), q.QLIN_ERR_NULL),
+    (dict(b=batch(kv_len=None)), q.QLIN_ERR_NULL),
+    (dict(c=cache(page=8)), q.QLIN_ERR_UNSUPPORTED), (dict(c=cache(page=48)), q.QLIN_ERR_UNSUPPORTED),
+    (dict(c=cache(d=96)), q.QLIN_ERR_UNSUPPORTED),
+    (dict(c=cache(pages=0)), q.QLIN_ERR_SHAPE), (dict(c=cache(heads=0)), q.QLIN_ERR_SHAPE),
+    (dict(hq=0), q.QLIN_ERR_SHAPE), (dict(hq=5), q.QLIN_ERR_SHAPE), (dict(tokens=-1), q.QLIN_ERR_SHAPE),
+    (dict(b=batch(n=-1)), q.QLIN_ERR_SHAPE), (dict(b=batch(max_q=-1)), q.QLIN_ERR_SHAPE),
+    (dict(b=batch(max_kv=-1)), q.QLIN_ERR_SHAPE), (dict(b=batch(ld=3)), q.QLIN_ERR_SHAPE),
+    (dict(b=batch(max_kv=65)), q.QLIN_ERR_SHAPE),
+    (dict(c=cache(k=C1 + 8)), q.QLIN_ERR_ALIGN), (dict(c=cache(vs=C4 + 4)), q.QLIN_ERR_ALIGN),
+    (dict(b=batch(kv_len=I3 + 2)), q.QLIN_ERR_ALIGN), (dict(b=batch(prefix=I4 + 1)), q.QLIN_ERR_ALIGN),
+    (dict(dt=2), q.QLIN_ERR_DTYPE), (dict(dt=3), q.QLIN_ERR_DTYPE), (dict(dt=-1), q.QLIN_ERR_DTYPE),
+]
+
+
+def append(lib, qkv=P, dt=1, tokens=20, ld=8 * 64, hq=4, rope=R, rope_len=64, rot=64, inter=0, pos=None, c=cache(),
+           b=batch(), out=P2, ldq=4 * 64):
+    return lib.qlin_rope_append_kv(qkv, dt, tokens, ld, hq, rope, rope_len, rot, inter, pos, *refs(c, b), out, ldq, None)
+
+
+@pytest.mark.parametrize("kw,status", KV_BAD + [
+    (dict(qkv=None), q.QLIN_ERR_NULL), (dict(out=None), q.QLIN_ERR_NULL), (dict(rope=None), q.QLIN_ERR_NULL),
+    (dict(inter=2), q.QLIN_ERR_UNSUPPORTED),
+    (dict(rot=-16), q.QLIN_ERR_SHAPE), (dict(rot=24), q.QLIN_ERR_SHAPE), (dict(rot=80), q.QLIN_ERR_SHAPE),
+    (dict(rope_len=0), q.QLIN_ERR_SHAPE), (dict(ld=504), q.QLIN_ERR_SHAPE), (dict(ld=516), q.QLIN_ERR_SHAPE),
+    (dict(ldq=248), q.QLIN_ERR_SHAPE), (dict(ldq=260), q.QLIN_ERR_SHAPE),
+    (dict(b=batch(n=1 << 30, max_q=1000)), q.QLIN_ERR_SHAPE),          # more blocks than a launch holds
+    (dict(qkv=P + 2), q.QLIN_ERR_ALIGN), (dict(out=P2 + 4), q.QLIN_ERR_ALIGN), (dict(rope=R + 4), q.QLIN_ERR_ALIGN),
+    (dict(pos=I4 + 2), q.QLIN_ERR_ALIGN),
+    (dict(out=P), q.QLIN_ERR_ALIAS), (dict(out=C1 + 4096), q.QLIN_ERR_ALIAS), (dict(pos=P2 + 64), q.QLIN_ERR_ALIAS),
+    (dict(c=cache(v=C1 + 64)), q.QLIN_ERR_ALIAS), (dict(c=cache(ks=C1)), q.QLIN_ERR_ALIAS),
+    (dict(b=batch(kv_len=C3)), q.QLIN_ERR_ALIAS), (dict(b=batch(table=C2 + 1024)), q.QLIN_ERR_ALIAS),
+])
+def test_rope_append_rejects(lib, kw, status):
+    assert append(lib, **kw) == status
+
+
+def test_rope_append_empty_is_ok(lib):
+    assert append(lib, tokens=0, qkv=None, out=None) == q.QLIN_OK
+    assert append(lib, b=batch(n=0, table=None, q_start=None, kv_len=None)) == q.QLIN_OK
+    assert append(lib, b=batch(max_q=0)) == q.QLIN_OK
+    assert append(lib, tokens=0, rot=0, rope=None, rope_len=0) == q.QLIN_OK
+
+
+@pytest.mark.parametrize("args,status", [
+    ((None, 8, 16, 1e4, 1.0), q.QLIN_ERR_NULL), ((R, -1, 16, 1e4, 1.0), q.QLIN_ERR_SHAPE),
+    ((R, 8, 15, 1e4, 1.0), q.QLIN_ERR_SHAPE), ((R, 8, 0, 1e4, 1.0), q.QLIN_ERR_SHAPE),
+    ((R, 8, 16, 0.0, 1.0), q.QLIN_ERR_UNSUPPORTED), ((R, 8, 16, 1e4, float("nan")), q.QLIN_ERR_UNSUPPORTED),
+    ((R, 8, 16, float("inf"), 1.0), q.QLIN_ERR_UNSUPPORTED), ((R, 8, 16, 1e4, -1.0), q.QLIN_ERR_UNSUPPORTED),
+    ((R + 8, 8, 16, 1e4, 1.0), q.QLIN_ERR_ALIGN), ((R, 0, 16, 1e4, 1.0), q.QLIN_OK),
+])
+def test_rope_table_checks(lib, args, status):
+    assert lib.qlin_rope_table(*args, None) == status
+
+
+# ---- the index arithmetic of the kernels, on the host
+
+INDEX_CHECK = r"""
+#include <cstdio>
+#include <cstdlib>
+#include <random>
+#include <vector>
+#include "kv_index.h"
+using namespace qlin;
+static void need(bool ok, const char* what) { if (!ok) { std::printf("broken: %s\n", what); std::exit(1); } }
+int main() {
+    std::mt19937 r(11);
+    auto any = [&](int lo, int hi) { return lo + static_cast<int>(r() % static_cast<unsigned>(hi - lo + 1)); };
+    for (int it = 0; it < 20000; ++it) {
+        KvIndex x{};
+        const bool damaged = it & 1;
+        x.page_size = 16 << any(0, 2);
+        x.batch = any(1, 5);
+        x.max_q = any(0, 90);
+        x.max_kv = any(0, 300);
+        const int cols = (x.max_kv + x.page_size - 1) / x.page_size;
+        x.table_ld = cols + any(0, 2);
+        x.pages = any(1, 40);
+        // exactly what the kernels may read: an index past it is an error under the sanitizer
+        std::vector<int32_t> table((x.batch - 1) * x.table_ld + cols), start(x.batch + 1), kv(x.batch), pre(x.batch);
+        int at = 0;
+        for (int b = 0; b <= x.batch; ++b) {
+            start[b] = at;
+            if (b < x.batch) { const int n = any(0, x.max_q < x.max_kv ? x.max_q : x.max_kv); at += n; kv[b] = any(n, x.max_kv); }
+        }
+        x.tokens = at + any(0, 3);
+        for (auto& p : table) p = any(0, static_cast<int>(x.pages) - 1);
+        for (auto& p : pre) p = any(-3, x.max_kv + 3);
+        if (damaged) {
+            const int32_t bad[] = {-1, INT32_MIN, INT32_MAX, 1 << 20, -77};
+            for (auto* v : {&table, &start, &kv, &pre})
+                for (auto& e : *v) if (any(0, 3) == 0) e = bad[any(0, 4)];
+        }
+        x.page_table = table.data(); x.q_start = start.data(); x.kv_len = kv.data();
+        x.prefix_len = any(0, 1) ? pre.data() : nullptr;
+        const int touched = kv_max_touched(x.max_q, x.page_size);
+        for (int b = 0; b < x.batch; ++b) {
+            const KvSeq s = kv_seq(x, b);
+            need(s.n >= 0 && s.n <= x.max_q && s.kv >= 0 && s.kv <= x.max_kv, "lengths");
+            need(s.row0 >= 0 && s.row0 + s.n <= x.tokens, "rows");
+            int covered = 0;
+            for (int i = 0; i < touched + 2; ++i) {
+                const KvSpan p = kv_touched(x, s, i);
+                if (p.hi <= p.lo || s.n == 0) continue;
+                need(i < touched, "pages touched past the grid");
+                need(p.idx >= 0 && p.idx < cols, "page column");
+                need(p.lo / x.page_size == p.idx && (p.hi - 1) / x.page_size == p.idx, "span in its page");
+                for (int j = p.lo; j < p.hi; ++j) need(j >= s.first && j - s.first < s.n, "token of a position");
+                const int page = kv_page(x, b, p.idx);
+                need(page == kNoPage || (page >= 0 && page < x.pages), "page");
+                covered += p.hi - p.lo;
+            }
+            need(covered == (s.n == 0 ? 0 : s.kv - (s.first < 0 ? 0 : s.first)), "every new token once");
+            for (int i = 0; i < s.n; ++i) {
+                const int v = kv_visible(x, s, b, s.first + i);
+                need(v >= 0 && v <= s.kv, "visible keys");
+                if (!damaged && !x.prefix_len) need(v == s.first + i + 1, "causal");
+            }
+        }
+    }
+    std::printf("index arithmetic holds\n");
+}
+"""
+
+
+def test_index_arithmetic_stays_in_bounds(tmp_path):
+    """Token ranges, page columns and page numbers over random and damaged
+    metadata, under the host sanitizers."""
+    src, exe = tmp_path / "index.cpp", tmp_path / "index"
+    src.write_text(INDEX_CHECK)
+    r = subprocess.run([hs.compiler(), "-std=c++17", "-O1", "-g", "-fsanitize=address,undefined",
+                        "-fno-sanitize-recover=undefined", "-D_GLIBCXX_ASSERTIONS", f"-I{hs.CSRC}", str(src), "-o", str(exe)],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-3000:]
+    env = {k: v for k, v in os.environ.items() if k != "LD_PRELOAD"}
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300, env=env)
+    assert r.returncode == 0 and "holds" in r.stdout, (r.stdout + r.stderr)[-3000:]
+
+
 # ---- the same calls under AddressSanitizer and UndefinedBehaviorSanitizer
 
 @pytest.mark.skipif("QLIN_LIB_PATH" in os.environ, reason="already the sanitizer build")

@@ -51,3 +51,74 @@ def test_norm_quant_is_the_unfused_chain():
     _, codes, scale = oracle.add_rmsnorm_quant(x, None, w, 1e-5, 32, 8, "f32")
     assert np.max(np.abs(codes - want)) <= 1 and np.mean(codes != want) < 1e-2   # the chain divides by the rounded scale
     assert np.allclose(scale, s_want, rtol=1e-7)
+
+
+# ---- rotary positions and the paged cache
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_is_a_complex_product_and_keeps_distances(interleaved):
+    d, rot = 16, 8
+    x, y = rng(7).standard_normal(d), rng(8).standard_normal(d)
+    t = oracle.rope_table(40, rot)
+    row = t[11].astype(np.float64)
+    a = np.arange(rot // 2) * 2 if interleaved else np.arange(rot // 2)
+    b = a + 1 if interleaved else a + rot // 2
+    z = (x[a] + 1j * x[b]) * (row[:rot // 2] + 1j * row[rot // 2:])
+    got = oracle.rope(x, t[11], rot, interleaved)
+    assert np.allclose(got[a], z.real, rtol=1e-14) and np.allclose(got[b], z.imag, rtol=1e-14)
+    assert np.array_equal(got[rot:], x[rot:])
+    # scores depend on the distance of two positions only
+    s = [oracle.rope(x, t[p + 3], rot, interleaved) @ oracle.rope(y, t[p], rot, interleaved) for p in (0, 9, 30)]
+    assert np.allclose(s, s[0], atol=1e-6)
+
+
+def test_rope_table_is_torchs_and_stretches():
+    t = oracle.rope_table(50, 12, base=500.0, stretch=2.0)
+    p = torch.arange(50, dtype=torch.float64)[:, None] / 2.0 / 500.0 ** (torch.arange(0, 12, 2, dtype=torch.float64) / 12)
+    assert np.allclose(t, torch.cat([p.cos(), p.sin()], 1).numpy(), atol=1e-7)
+    assert np.allclose(t[::2], oracle.rope_table(25, 12, base=500.0), atol=1e-7)
+
+
+def empty_cache(pages, heads, page, d):
+    return dict(k=np.full((pages, heads, page, d), 77, np.int8), v=np.full((pages, heads, d, page), 77, np.int8),
+                k_scale=np.full((pages, heads), 9.0, np.float32), v_scale=np.full((pages, heads), 9.0, np.float32))
+
+
+def test_append_by_hand():
+    # one head, d = 4, pages of 4 in the order 2, 0; q k v a token
+    c = empty_cache(3, 1, 4, 4)
+    x = np.zeros((5, 12))
+    x[:, 4] = [127.0, 254.0, 1.0, -3.0, 5.0]          # k: the page of the first four has scale 2
+    x[:, 8] = 1.27
+    q = oracle.rope_append_kv(x, c, [[2, 0]], [0, 5], [5], 1, None, 0, False)
+    assert c["k_scale"][2, 0] == 2.0 and c["k"][2, 0, :, 0].tolist() == [64, 127, 0, -2]   # 63.5 and 0.5, -1.5: to even
+    assert c["k_scale"][0, 0] == np.float32(5 / 127) and c["k"][0, 0, 0, 0] == 127 and c["k"][0, 0, 1, 0] == 77
+    assert c["v"][2, 0, 0].tolist() == [127] * 4 and c["v"][0, 0, 0].tolist() == [127, 77, 77, 77]
+    assert c["k_scale"][1, 0] == 9.0 and np.array_equal(q, x[:, :4])
+    # one more token, twice as large: the page's scale doubles and its code halves (63.5 -> 64)
+    x2 = np.zeros((1, 12))
+    x2[0, 4] = 10.0
+    oracle.rope_append_kv(x2, c, [[2, 0]], [0, 1], [6], 1, None, 0, False)
+    assert c["k_scale"][0, 0] == np.float32(10 / 127) and c["k"][0, 0, :2, 0].tolist() == [64, 127]
+    before = {n: a.copy() for n, a in c.items()}
+    oracle.rope_append_kv(x2, c, [[2, 0]], [0, 1], [6], 1, None, 0, False)
+    assert all(np.array_equal(before[n], c[n]) for n in c)
+
+
+def test_append_bounds_the_stored_error():
+    # a page filled at once: every stored value within half a step of its own
+    c = empty_cache(2, 2, 16, 8)
+    x = rng(9).standard_normal((16, 6 * 8))
+    oracle.rope_append_kv(x, c, [[1]], [0, 16], [16], 2, None, 0, False)
+    k = x.reshape(16, 6, 8)[:, 2:4].transpose(1, 0, 2)
+    v = x.reshape(16, 6, 8)[:, 4:].transpose(1, 2, 0)
+    for codes, scale, ref in ((c["k"][1], c["k_scale"][1], k), (c["v"][1], c["v_scale"][1], v)):
+        assert np.all(np.abs(codes * scale[:, None, None] - ref) <= 0.5000001 * scale[:, None, None])
+
+
+def test_append_keeps_damaged_values_out_of_the_scale():
+    c = empty_cache(1, 1, 16, 4)
+    x = np.zeros((2, 12))
+    x[0, 4:8] = [np.inf, -np.inf, np.nan, 127.0]
+    oracle.rope_append_kv(x, c, [[0]], [0, 2], [2], 1, None, 0, False)
+    assert c["k_scale"][0, 0] == 1.0 and c["k"][0, 0, 0].tolist() == [127, -127, 0, 127]
