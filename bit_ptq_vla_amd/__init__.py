@@ -73,6 +73,8 @@ SIGNATURES = {
     "qlin_quantize_weights_composite": [_P, _I32, _I64, _I64, _P, _P, _P, _I32, _I32, _P, _P, _P, _P],
     "qlin_add_rmsnorm_quant": [_P, _I32, _I64, _I64, _I64, _P, _I64, _P, _F32, _I32, _I32, _P, _P, _P, _P],
     "qlin_rope_append_kv": [_P, _I32, _I64, _I64, _I32, _P, _I64, _I32, _I32, _P, _P, _P, _P, _I64, _P],
+    "qlin_kv_attention": [_P, _I32, _I64, _I64, _I32, _P, _P, _F32, _F32, _P, _I64, _P, _I64, _P],
+    "qlin_kv_attention_workspace_bytes": [_I32, _P, _P],
     "qlin_rope_table": [_P, _I64, _I32, ctypes.c_double, ctypes.c_double, _P],
     "qlin_add_rmsnorm": [_P, _I32, _I64, _I64, _I64, _P, _I64, _P, _F32, _P, _P, _P],
 }
@@ -746,6 +748,46 @@ def qlin_rope_append_kv(qkv: torch.Tensor, cache: KvCache, batch: KvBatch, heads
                     batch._ref, q_out.data_ptr(), ldq, _stream(cache.device))
     _check(st, "qlin_rope_append_kv")
     return q_out
+
+
+def kv_attention_workspace_bytes(cache: KvCache, batch: KvBatch, heads_q: int) -> int:
+    """Bytes a qlin_kv_attention call on this batch takes to split a sequence's
+    keys over blocks (0: no split)."""
+    nbytes = _on_device(load().qlin_kv_attention_workspace_bytes, cache.device, heads_q, cache._ref, batch._ref)
+    if nbytes < 0:
+        raise QlinError(QLIN_ERR_SHAPE, "qlin_kv_attention_workspace_bytes")
+    return nbytes
+
+
+def kv_attention_workspace(cache: KvCache, batch: KvBatch, heads_q: int) -> Optional[torch.Tensor]:
+    """A device buffer for qlin_kv_attention (None when the call takes none)."""
+    nbytes = kv_attention_workspace_bytes(cache, batch, heads_q)
+    return torch.empty(nbytes, dtype=torch.uint8, device=cache.device) if nbytes else None
+
+
+def qlin_kv_attention(q: torch.Tensor, cache: KvCache, batch: KvBatch, heads_q: int, sm_scale: Optional[float] = None,
+                      softcap: float = 0.0, out: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of q [tokens][heads_q d] over the cache; sm_scale defaults to
+    d^-0.5, workspace (kv_attention_workspace) is allocated here when None."""
+    d = cache.head_dim
+    ldq = _rows16(q, "q", heads_q * d)
+    batch.check(cache)
+    if out is None:
+        out = torch.empty((q.shape[0], heads_q * d), dtype=q.dtype, device=q.device)
+    ldo = _rows16(out, "out", heads_q * d)
+    if out.shape[0] != q.shape[0] or out.dtype != q.dtype:
+        raise ValueError("out must have q's rows and type")
+    if workspace is None:
+        workspace = kv_attention_workspace(cache, batch, heads_q)
+    _need(workspace, 0, "workspace")
+    _same_device(cache.device, q=q, out=out, workspace=workspace)
+    st = _on_device(load().qlin_kv_attention, cache.device, q.data_ptr(), _TORCH_TO_QLIN.get(q.dtype, -1), q.shape[0],
+                    ldq, heads_q, cache._ref, batch._ref, d ** -0.5 if sm_scale is None else sm_scale, softcap,
+                    out.data_ptr(), ldo, _ptr(workspace),
+                    0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(cache.device))
+    _check(st, "qlin_kv_attention")
+    return out
 
 
 QLIN_STREAM_READ_SINK_WORDS = 4096

@@ -1,0 +1,362 @@
+// Attention over a paged int8 key/value cache with a scale per page and head,
+// for gfx950.
+//
+//   s_ij = sm_scale q_i . (ks_j ck_j)   (capped: c tanh(s / c)),
+//   out_i = sum_j exp(s_ij - m_i) vs_j cv_j / sum_j exp(s_ij - m_i)
+//
+// over the keys the query sees, in one pass with the running maximum m and sum.
+// Everything is computed transposed, so that no value ever changes lanes:
+//   S^T = K Q^T  (v_mfma_f32_16x16x32_f16: rows keys, columns queries) leaves a
+//   lane with scores of ONE query, and the same registers, rounded to fp16, are
+//   the B operand of O^T += V^T P^T, whose rows are head dimensions.  A lane's
+//   softmax statistics, rescaling and mask limit are its own scalars.
+// A step takes 64 keys, four granules of 16: lane group g = lane / 16 ends up
+// with the scores of granule g (key 16 g + 4 t + i in element i of tile t).
+// Rows of the K operand are permuted to make that so, and V, stored keys-first
+// in its page, is then one 16-byte load per lane and 16 dimensions.  A granule
+// lies in one page, so a lane needs one k scale and one v scale a step.
+//
+// Codes become fp16 exactly (|code| <= 127): byte + 128 under the exponent of
+// 1024, minus 1152.  bf16 queries become fp16 under a power of two per row that
+// brings the row's maximum to 2^13..2^14: exact but for elements 2^-27 below
+// that maximum.  Scores, statistics and sums are fp32.  The weights are rounded
+// to fp16 after multiplication by vs_j / vr, vr the largest v scale met so far
+// (<= 1, so they neither overflow nor lose the small pages): 2^-12 each, under
+// the output's own half step.
+
+#include "device_common.h"
+#include "kv_index.h"
+#include "qlin_internal.h"
+
+namespace qlin {
+
+namespace {
+
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+
+struct AttnParams {
+    KvIndex ix;
+    const void* q;
+    int64_t ldq;
+    const int8_t* k;
+    const int8_t* v;
+    const float* ks;
+    const float* vs;
+    void* out;
+    int64_t ldo;
+    int heads_q, heads, group;
+    float sm_scale, cap;
+    int row_tiles, splits, split_keys;
+    float* part_o;     // [splits][batch * max_q][heads_q][D]
+    float* part_ml;    // [splits][batch * max_q][heads_q][2]
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNegInf = -__builtin_inff();
+
+// Eight codes (two words) as fp16.
+__device__ __forceinline__ h8 codes_f16(uint32_t w0, uint32_t w1) {
+    const h2 off = {static_cast<_Float16>(-1152.f), static_cast<_Float16>(-1152.f)};
+    const uint32_t a = w0 ^ 0x80808080u, b = w1 ^ 0x80808080u;
+    const h2 r0 = __builtin_bit_cast(h2, __builtin_amdgcn_perm(0x64646464u, a, 0x04010400u)) + off;
+    const h2 r1 = __builtin_bit_cast(h2, __builtin_amdgcn_perm(0x64646464u, a, 0x04030402u)) + off;
+    const h2 r2 = __builtin_bit_cast(h2, __builtin_amdgcn_perm(0x64646464u, b, 0x04010400u)) + off;
+    const h2 r3 = __builtin_bit_cast(h2, __builtin_amdgcn_perm(0x64646464u, b, 0x04030402u)) + off;
+    return h8{r0[0], r0[1], r1[0], r1[1], r2[0], r2[1], r3[0], r3[1]};
+}
+
+// Maximum / sum over the four lane groups that share a query (lane ^ 16, ^ 32).
+__device__ __forceinline__ float groups_max(float v) {
+    v = fmaxf(v, lane_xor<16>(v));
+    return fmaxf(v, lane_xor<32>(v));
+}
+__device__ __forceinline__ float groups_sum(float v) {
+    v += lane_xor<16>(v);
+    return v + lane_xor<32>(v);
+}
+
+// A score in base-2 units from the raw product: capped where CAP.
+template <bool CAP>
+__device__ __forceinline__ float score(float raw, float mul, float cap_in, float cap_out) {
+    if constexpr (CAP) {
+        // c tanh(x / c) = c (1 - 2 / (1 + exp(2 x / c))): mul holds 2 / c * log2 e, cap_out c log2 e
+        const float e = __builtin_amdgcn_exp2f(raw * mul);
+        return cap_out - 2.f * cap_out * __builtin_amdgcn_rcpf(1.f + e);
+    } else {
+        return raw * mul;
+    }
+}
+
+// One query row of a block: column c holds row r0 + c of the (token, head of the group) rows.
+struct Row {
+    bool ok;
+    int64_t token;      // row of q and out
+    int64_t slot;       // row of the partials
+    int head;
+    int vis;            // keys it sees
+};
+
+__device__ __forceinline__ Row row_of(const AttnParams& p, const KvSeq& s, int b, int h, int r) {
+    Row x;
+    const int i = r / p.group;
+    x.ok = i < s.n;
+    const int ii = x.ok ? i : 0;
+    x.token = s.row0 + ii;
+    x.slot = static_cast<int64_t>(b) * p.ix.max_q + ii;
+    x.head = h * p.group + r % p.group;
+    x.vis = x.ok ? kv_visible(p.ix, s, b, s.first + i) : 0;
+    return x;
+}
+
+// Up to 16 query rows of one (sequence, kv head) against a range of its keys:
+// four waves take the range's 64-key steps in turn and join through LDS.
+template <int DT, int D, bool CAP>
+__global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
+    constexpr int NL = D / 64;     // 16-byte K loads per key row and lane
+    constexpr int ND = D / 16;     // 16-dimension tiles of the output
+    __shared__ float lo[4][16][D + 4];
+    __shared__ float lm[4][16], ll[4][16];
+    int64_t u = blockIdx.x;
+    const int sp = static_cast<int>(u % p.splits);
+    u /= p.splits;
+    const int rt = static_cast<int>(u % p.row_tiles);
+    u /= p.row_tiles;
+    const int h = static_cast<int>(u % p.heads);
+    const int b = static_cast<int>(u / p.heads);
+    const KvSeq s = kv_seq(p.ix, b);
+    const int rows = s.n * p.group, r0 = rt * 16;
+    if (r0 >= rows) return;
+    const int last = (r0 + 16 < rows ? r0 + 16 : rows) - 1;
+    const int vis_hi = row_of(p, s, b, h, last).vis, vis_lo = row_of(p, s, b, h, r0).vis;
+    const int k0 = sp * p.split_keys;
+    if (sp > 0 && k0 >= vis_hi) return;      // the join reads only the splits below the row's limit
+    const int k1 = k0 + p.split_keys < vis_hi ? k0 + p.split_keys : vis_hi;
+
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int c = lane & 15, g = lane >> 4;
+    const Row row = row_of(p, s, b, h, r0 + c < rows ? r0 + c : last);
+    const int vis = r0 + c < rows ? row.vis : 0;
+    const int ps = p.ix.page_size;
+
+    // the lane's part of its query: dimensions 64 j + 16 g .. + 15
+    h8 qf[2 * NL];
+    float qmul = p.sm_scale;
+    {
+        const char* src = static_cast<const char*>(p.q) + (row.token * p.ldq + static_cast<int64_t>(row.head) * D) * 2;
+        float f[2 * NL][8];
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+            load8<DT>(src + (64 * j + 16 * g) * 2, f[2 * j]);
+            load8<DT>(src + (64 * j + 16 * g + 8) * 2, f[2 * j + 1]);
+        }
+        int e = 0;
+        if constexpr (DT == BF16) {
+#pragma unroll
+            for (int j = 0; j < 2 * NL; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[j][i]));
+            top = groups_max(top);
+            if (top > 0.f && top < __builtin_inff()) e = 14 - __builtin_amdgcn_frexp_expf(top);
+            e = e > 120 ? 120 : e < -120 ? -120 : e;
+            qmul = __builtin_amdgcn_ldexpf(p.sm_scale, -e);
+        }
+#pragma unroll
+        for (int j = 0; j < 2 * NL; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                qf[j][i] = static_cast<_Float16>(DT == BF16 ? __builtin_amdgcn_ldexpf(f[j][i], e) : f[j][i]);
+    }
+    qmul *= CAP ? 2.f * kLog2e / p.cap : kLog2e;
+    const float cap_out = CAP ? p.cap * kLog2e : 0.f;
+
+    f4 o[ND];
+#pragma unroll
+    for (int t = 0; t < ND; ++t) o[t] = f4{0.f, 0.f, 0.f, 0.f};
+    float m = kNegInf, l = 0.f, vr = 0.f;
+    const int last_idx = s.kv > 0 ? (s.kv - 1) / ps : 0;
+    const int gk = c >> 2;                   // granule of the lane's K rows
+
+    for (int t0 = k0 + 64 * wave; t0 < k1; t0 += 256) {
+        // granules past the cache read its last page (their keys are masked)
+        int ik = (t0 + 16 * gk) / ps, iv = (t0 + 16 * g) / ps;
+        ik = ik < last_idx ? ik : last_idx;
+        iv = iv < last_idx ? iv : last_idx;
+        const int pk = kv_page(p.ix, b, ik), pv = kv_page(p.ix, b, iv);
+        const int64_t sk = static_cast<int64_t>(pk < 0 ? 0 : pk) * p.heads + h;
+        const int64_t sv = static_cast<int64_t>(pv < 0 ? 0 : pv) * p.heads + h;
+        const int8_t* kb = p.k + sk * ps * D + ((t0 + 16 * gk) % ps + (c & 3)) * D + 16 * g;
+        const int8_t* vb = p.v + sv * ps * D + static_cast<int64_t>(c) * ps + (t0 + 16 * g) % ps;
+        u4 kw[4][NL], vw[ND];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int j = 0; j < NL; ++j) kw[t][j] = *reinterpret_cast<const u4*>(kb + 4 * t * D + 64 * j);
+#pragma unroll
+        for (int t = 0; t < ND; ++t) vw[t] = *reinterpret_cast<const u4*>(vb + static_cast<int64_t>(16 * t) * ps);
+        const bool live = pv >= 0 && t0 + 16 * g < s.kv;
+        const float ksc = live ? p.ks[sv] : 0.f;
+        const float vsc = live ? p.vs[sv] : 0.f;
+
+        float x[16];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            f4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < NL; ++j) {
+                const u4 w = kw[t][j];
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16(w[0], w[1]), qf[2 * j], acc, 0, 0, 0);
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16(w[2], w[3]), qf[2 * j + 1], acc, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[4 * t + i] = acc[i];
+        }
+        const float mul = qmul * ksc;
+        const int lim = live ? vis - (t0 + 16 * g) : 0;      // keys of the granule that the query sees
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = i < lim ? score<CAP>(x[i], mul, 0.f, cap_out) : kNegInf;
+
+        float top = x[0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
+        top = groups_max(top);
+        const float vtop = groups_max(vsc);
+        const float mn = fmaxf(m, top), vn = fmaxf(vr, vtop);
+        const float base = mn > kNegInf ? mn : 0.f;          // nothing seen yet: all weights 0
+        const float alpha = m > kNegInf ? __builtin_amdgcn_exp2f(m - base) : 1.f;
+        if (__any(alpha != 1.f || vn != vr)) {
+            const float r = alpha * (vr > 0.f ? vr / vn : 1.f);
+#pragma unroll
+            for (int t = 0; t < ND; ++t) o[t] *= r;
+            l *= alpha;
+        }
+        m = mn;
+        vr = vn;
+        const float wv = vn > 0.f ? vsc / vn : 0.f;
+        h8 pf[2];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float w = __builtin_amdgcn_exp2f(x[i] - base);
+            l += w;
+            pf[i >> 3][i & 7] = static_cast<_Float16>(w * wv);
+        }
+#pragma unroll
+        for (int t = 0; t < ND; ++t) {
+            const u4 w = vw[t];
+            o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16(w[0], w[1]), pf[0], o[t], 0, 0, 0);
+            o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16(w[2], w[3]), pf[1], o[t], 0, 0, 0);
+        }
+    }
+
+    // join the waves: element i of tile t is dimension 16 t + 4 g + i of query c
+    l = groups_sum(l);
+#pragma unroll
+    for (int t = 0; t < ND; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lo[wave][c][16 * t + 4 * g + i] = o[t][i] * vr;
+    if (g == 0) {
+        lm[wave][c] = m;
+        ll[wave][c] = l;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < 16 * (D / 8); e += 256) {
+        const int r = e / (D / 8), d = e % (D / 8) * 8;
+        if (r0 + r >= rows) continue;
+        const Row x = row_of(p, s, b, h, r0 + r);
+        float mt = lm[0][r];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) mt = fmaxf(mt, lm[w][r]);
+        const float base = mt > kNegInf ? mt : 0.f;
+        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float a = __builtin_amdgcn_exp2f(lm[w][r] - base);
+            sum += a * ll[w][r];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] += a * lo[w][r][d + i];
+        }
+        if (p.splits == 1) {
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] *= inv;
+            store8<DT>(static_cast<char*>(p.out) + (x.token * p.ldo + static_cast<int64_t>(x.head) * D + d) * 2, f);
+        } else {
+            const int64_t at = ((static_cast<int64_t>(sp) * p.ix.batch * p.ix.max_q + x.slot) * p.heads_q + x.head);
+            store8<F32>(p.part_o + at * D + d, f);
+            if (d == 0) {
+                p.part_ml[2 * at] = mt;
+                p.part_ml[2 * at + 1] = sum;
+            }
+        }
+    }
+}
+
+// Joins the splits of every (token, head): D / 8 lanes each.
+template <int DT, int D>
+__global__ __launch_bounds__(256) void kv_attn_join_kernel(AttnParams p) {
+    const int64_t u = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / (D / 8);
+    const int d = threadIdx.x % (D / 8) * 8;
+    const int64_t slot = u / p.heads_q;
+    const int head = static_cast<int>(u % p.heads_q);
+    const int b = static_cast<int>(slot / p.ix.max_q), i = static_cast<int>(slot % p.ix.max_q);
+    if (b >= p.ix.batch) return;
+    const KvSeq s = kv_seq(p.ix, b);
+    if (i >= s.n) return;
+    const int vis = kv_visible(p.ix, s, b, s.first + i);
+    float m = kNegInf, sum = 0.f, f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int sp = 0; sp < p.splits && sp * p.split_keys < vis; ++sp) {
+        const int64_t at = (static_cast<int64_t>(sp) * p.ix.batch * p.ix.max_q + slot) * p.heads_q + head;
+        const float ms = p.part_ml[2 * at], ls = p.part_ml[2 * at + 1];
+        float v[8];
+        load8<F32>(p.part_o + at * D + d, v);
+        const float mn = fmaxf(m, ms), base = mn > kNegInf ? mn : 0.f;
+        const float a = __builtin_amdgcn_exp2f(m - base), c = __builtin_amdgcn_exp2f(ms - base);
+        sum = sum * a + ls * c;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = f[e] * a + v[e] * c;
+        m = mn;
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] *= inv;
+    store8<DT>(static_cast<char*>(p.out) + ((s.row0 + i) * p.ldo + static_cast<int64_t>(head) * D + d) * 2, f);
+}
+
+template <int DT, int D>
+hipError_t launch_d(const AttnParams& p, hipStream_t st) {
+    const int64_t blocks = static_cast<int64_t>(p.ix.batch) * p.heads * p.row_tiles * p.splits;
+    if (p.cap > 0.f)
+        kv_attn_rows16_kernel<DT, D, true><<<dim3(static_cast<unsigned>(blocks)), 256, 0, st>>>(p);
+    else
+        kv_attn_rows16_kernel<DT, D, false><<<dim3(static_cast<unsigned>(blocks)), 256, 0, st>>>(p);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.splits == 1) return e;
+    const int64_t lanes = static_cast<int64_t>(p.ix.batch) * p.ix.max_q * p.heads_q * (D / 8);
+    kv_attn_join_kernel<DT, D><<<dim3(static_cast<unsigned>((lanes + 255) / 256)), 256, 0, st>>>(p);
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t launch_dt(const AttnParams& p, int d, hipStream_t st) {
+    if (d == 64) return launch_d<DT, 64>(p, st);
+    if (d == 128) return launch_d<DT, 128>(p, st);
+    return launch_d<DT, 256>(p, st);
+}
+
+}  // namespace
+
+hipError_t launch_kv_attention(const KvAttnPlan& plan, const void* q, int dtype, int64_t ldq, int heads_q,
+                               const KvIndex& ix, const int8_t* k, const int8_t* v, const float* ks, const float* vs,
+                               int heads, int d, float sm_scale, float cap, void* out, int64_t ldo, void* ws,
+                               hipStream_t st) {
+    AttnParams p{ix, q, ldq, k, v, ks, vs, out, ldo, heads_q, heads, heads_q / heads, sm_scale, cap, plan.row_tiles,
+                 plan.splits, plan.split_keys, nullptr, nullptr};
+    if (plan.splits > 1) {
+        p.part_o = static_cast<float*>(ws);
+        p.part_ml = p.part_o + static_cast<int64_t>(plan.splits) * ix.batch * ix.max_q * heads_q * d;
+    }
+    return dtype == F16 ? launch_dt<F16>(p, d, st) : launch_dt<BF16>(p, d, st);
+}
+
+}  // namespace qlin

@@ -170,4 +170,26 @@ int64_t composite_calib_work_bytes(int64_t n, int64_t k, int b) {
     return (chunks * k + k + k * b) * 8;
 }
 
+KvAttnPlan plan_kv_attention(int64_t batch, int64_t max_q, int64_t max_kv, int heads_q, int heads, int d,
+                             bool allow_split) {
+    KvAttnPlan p;
+    const int64_t rows = max_q * (heads_q / heads);
+    p.row_tiles = static_cast<int>((rows + 15) / 16);
+    const int64_t units = batch * heads * p.row_tiles;
+    // few tiles: their keys are split until there are two blocks for each CU,
+    // 256 keys (a step of the block's four waves) at least to each
+    int64_t splits = 1;
+    if (allow_split && units > 0) {
+        const int64_t want = (2 * static_cast<int64_t>(device_cus()) + units - 1) / units, most = (max_kv + 255) / 256;
+        splits = want < most ? want : most;
+        splits = splits < 1 ? 1 : splits;
+    }
+    const int64_t keys = ((max_kv + splits - 1) / splits + 255) / 256 * 256;
+    p.split_keys = static_cast<int>(keys < 256 ? 256 : keys > 0x7FFFFF00 ? 0x7FFFFF00 : keys);
+    p.splits = splits == 1 ? 1 : static_cast<int>((max_kv + p.split_keys - 1) / p.split_keys);
+    p.blocks = units * p.splits;
+    p.ws_bytes = p.splits > 1 ? p.splits * batch * max_q * heads_q * (d + 2) * 4 : 0;
+    return p;
+}
+
 }  // namespace qlin

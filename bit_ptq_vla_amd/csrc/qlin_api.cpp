@@ -219,7 +219,9 @@ qlin_status kv_check(const qlin_kv_cache* c, const qlin_kv_batch* b, int64_t tok
     if (heads_q < 1 || heads_q > 65536 || heads_q % c->heads != 0) return QLIN_ERR_SHAPE;
     if (tokens < 0 || tokens > 0x7FFFFFFF || b->batch < 0 || b->max_q < 0 || b->max_kv < 0) return QLIN_ERR_SHAPE;
     if (b->table_ld < (static_cast<int64_t>(b->max_kv) + c->page_size - 1) / c->page_size) return QLIN_ERR_SHAPE;
-    if (b->table_ld > 0x7FFFFFFF) return QLIN_ERR_SHAPE;
+    // positions and (token, head) rows are 32-bit integers in the kernels
+    if (b->table_ld > 0x7FFFFFFF || b->max_kv > (1 << 30)) return QLIN_ERR_SHAPE;
+    if (static_cast<int64_t>(b->max_q) * (heads_q / c->heads) > (1LL << 30)) return QLIN_ERR_SHAPE;
     if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_scale) || !aligned16(c->v_scale)) return QLIN_ERR_ALIGN;
     if (!aligned4(b->page_table) || !aligned4(b->q_start) || !aligned4(b->kv_len) || !aligned4(b->prefix_len))
         return QLIN_ERR_ALIGN;
@@ -619,6 +621,46 @@ qlin_status qlin_rope_append_kv(const void* qkv, qlin_dtype dtype, int64_t token
                                             kv_index(cache, batch, tokens), cache->k, cache->v, cache->k_scale,
                                             cache->v_scale, cache->heads, cache->head_dim, q_out, ldq,
                                             as_stream(stream)));
+}
+
+int64_t qlin_kv_attention_workspace_bytes(int32_t heads_q, const qlin_kv_cache* cache, const qlin_kv_batch* batch) {
+    if (kv_check(cache, batch, 0, heads_q) != QLIN_OK) return -1;
+    const qlin::KvAttnPlan plan = qlin::plan_kv_attention(batch->batch, batch->max_q, batch->max_kv, heads_q,
+                                                          cache->heads, cache->head_dim, true);
+    return plan.blocks > 0x7FFFFFFF ? -1 : plan.ws_bytes;
+}
+
+qlin_status qlin_kv_attention(const void* q, qlin_dtype dtype, int64_t tokens, int64_t ldq, int32_t heads_q,
+                              const qlin_kv_cache* cache, const qlin_kv_batch* batch, float sm_scale, float softcap,
+                              void* out, int64_t ldo, void* workspace, int64_t workspace_bytes, void* stream) {
+    qlin_status st = kv_check(cache, batch, tokens, heads_q);
+    if (st != QLIN_OK) return st;
+    if (tokens > 0 && (!q || !out)) return QLIN_ERR_NULL;
+    if (dtype != QLIN_F16 && dtype != QLIN_BF16) return QLIN_ERR_DTYPE;
+    constexpr float kMax = 3.402823466e38f;
+    if (!(sm_scale >= -kMax && sm_scale <= kMax) || !(softcap >= 0.f && softcap <= kMax)) return QLIN_ERR_UNSUPPORTED;
+    const int64_t wide = static_cast<int64_t>(heads_q) * cache->head_dim;
+    if (ldq % 8 != 0 || ldq < wide || ldo % 8 != 0 || ldo < wide || workspace_bytes < 0) return QLIN_ERR_SHAPE;
+    if (!workspace && workspace_bytes > 0) return QLIN_ERR_NULL;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return QLIN_ERR_ALIGN;
+    const qlin::KvAttnPlan plan = qlin::plan_kv_attention(batch->batch, batch->max_q, batch->max_kv, heads_q,
+                                                          cache->heads, cache->head_dim, workspace != nullptr);
+    if (plan.blocks > 0x7FFFFFFF || static_cast<int64_t>(batch->batch) * batch->max_q * heads_q > (1LL << 33))
+        return QLIN_ERR_SHAPE;
+    if (workspace && workspace_bytes < plan.ws_bytes) return QLIN_ERR_WORKSPACE;
+    const int64_t codes = cache->pages * cache->heads * cache->page_size * cache->head_dim;
+    const int64_t scales = cache->pages * cache->heads * 4;
+    const Span outs[2] = {{out, tokens > 0 ? ((tokens - 1) * ldo + wide) * 2 : 0}, {workspace, workspace_bytes}};
+    Span ins[9] = {{q, tokens > 0 ? ((tokens - 1) * ldq + wide) * 2 : 0}, {cache->k, codes}, {cache->v, codes},
+                   {cache->k_scale, scales}, {cache->v_scale, scales}};
+    kv_index_spans(cache, batch, ins + 5);
+    if (any_overlap(outs, 2, ins, 9)) return QLIN_ERR_ALIAS;
+    if (tokens == 0 || batch->batch == 0 || batch->max_q == 0) return QLIN_OK;
+    st = check_device();
+    if (st != QLIN_OK) return st;
+    return map_err(qlin::launch_kv_attention(plan, q, dtype, ldq, heads_q, kv_index(cache, batch, tokens), cache->k,
+                                             cache->v, cache->k_scale, cache->v_scale, cache->heads, cache->head_dim,
+                                             sm_scale, softcap, out, ldo, workspace, as_stream(stream)));
 }
 
 qlin_status qlin_rope_table(float* table, int64_t positions, int32_t rot_dim, double base, double stretch,

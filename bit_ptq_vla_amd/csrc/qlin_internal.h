@@ -109,6 +109,20 @@ hipError_t launch_rope_append(const void* qkv, int dtype, int64_t ld, int heads_
                               hipStream_t st);
 hipError_t launch_rope_table(float* table, int64_t positions, int rot, double base, double stretch, hipStream_t st);
 
+// Attention over the paged cache.  The plan: query-row tiles, and how many
+// blocks share a tile's keys (split_keys each; their partials, ws_bytes, are
+// joined by a second kernel).
+struct KvAttnPlan {
+    int row_tiles, splits, split_keys;
+    int64_t blocks, ws_bytes;
+};
+KvAttnPlan plan_kv_attention(int64_t batch, int64_t max_q, int64_t max_kv, int heads_q, int heads, int d,
+                             bool allow_split);
+hipError_t launch_kv_attention(const KvAttnPlan& plan, const void* q, int dtype, int64_t ldq, int heads_q,
+                               const KvIndex& ix, const int8_t* k, const int8_t* v, const float* ks, const float* vs,
+                               int heads, int d, float sm_scale, float cap, void* out, int64_t ldo, void* ws,
+                               hipStream_t st);
+
 // Streaming read of bytes (a multiple of 16) at src; one word per block to sink.
 hipError_t launch_stream_read(const void* src, int64_t bytes, uint32_t* sink, int64_t sink_words, hipStream_t st);
 

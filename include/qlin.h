@@ -450,7 +450,8 @@ qlin_status qlin_gemv_w4a16(const void* x, const void* wq, const void* w_scale, 
  *   and hold the last positions of its kv_len[b] (cached and new together).
  *   The index arrays are int32 on the device, 4-byte aligned.
  *   max_q, max_kv bound the new tokens and the length of any sequence (they
- *   size the launch); table_ld >= ceil(max_kv / page_size).
+ *   size the launch); table_ld >= ceil(max_kv / page_size); max_kv and max_q
+ *   times the query heads of a kv head at most 2^30.
  *   prefix_len (or NULL): the query at position p sees the keys j < kv_len[b]
  *   with j <= p or j < prefix_len[b]: causal without it, a prefix whose tokens
  *   see each other with it, everything where it reaches kv_len.
@@ -512,6 +513,33 @@ qlin_status qlin_rope_append_kv(const void* qkv, qlin_dtype dtype, int64_t token
                                 void* q_out, int64_t ldq, void* stream);
 qlin_status qlin_rope_table(float* table, int64_t positions, int32_t rot_dim, double base, double stretch,
                             void* stream);
+
+/*
+ * qlin_kv_attention -- attention of each sequence's new tokens over its cache
+ * (their own keys and values appended before: qlin_rope_append_kv).
+ *   score(i, j) = sm_scale * q_i . k_j, or softcap * tanh(that / softcap) with
+ *   softcap > 0; out_i = sum_j softmax_j(score) v_j over the keys the query
+ *   sees (qlin_kv_batch).  Query head h reads kv head h / (heads_q / heads).
+ *   A query that sees no key gives zeros; rows of no sequence stay as they are.
+ *   q        [tokens][ldq], heads_q * head_dim columns, dtype F16 or BF16.
+ *   out      out [tokens][ldo], same columns and dtype.
+ *   workspace  device memory, 16-byte aligned, contents overwritten, of at least
+ *            qlin_kv_attention_workspace_bytes(heads_q, cache, batch) bytes (else
+ *            QLIN_ERR_WORKSPACE), or NULL with workspace_bytes 0: the keys of a
+ *            sequence are then not split over blocks, which is slower for few
+ *            rows.  Calls (and replays of captured calls) that can run at the
+ *            same time need different workspaces.
+ * fp32 scores, statistics and sums; weights are rounded to fp16 (2^-12 each)
+ * before their product with v.  The same call gives the same bits.
+ * qlin_kv_attention_workspace_bytes: 0 where the call takes no split, -1 for
+ * arguments the call would refuse.
+ * Preconditions: tokens >= 0; heads_q a multiple of cache->heads; ldq, ldo
+ * multiples of 8; sm_scale finite; softcap >= 0, finite; out overlaps no input.
+ */
+int64_t qlin_kv_attention_workspace_bytes(int32_t heads_q, const qlin_kv_cache* cache, const qlin_kv_batch* batch);
+qlin_status qlin_kv_attention(const void* q, qlin_dtype dtype, int64_t tokens, int64_t ldq, int32_t heads_q,
+                              const qlin_kv_cache* cache, const qlin_kv_batch* batch, float sm_scale, float softcap,
+                              void* out, int64_t ldo, void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
  * qlin_stream_read -- measurement aid, not a step of the projection: reads

@@ -82,6 +82,7 @@ from .layer_ref import (  # noqa: F401
     rope_table,
     rope,
     rope_append_kv,
+    kv_attention,
 )
 from .compare import (  # noqa: F401
     compare_codes,

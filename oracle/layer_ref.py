@@ -109,3 +109,36 @@ def rope_append_kv(qkv, cache, table, q_start, kv_len, heads_q: int, rope_rows, 
                     vs[at, h] = _store(v[at, h].T, vs[at, h], new, held)
             j = end
     return out.reshape(len(qkv), heads_q * d)
+
+
+def kv_attention(q, cache, table, q_start, kv_len, heads_q: int, sm_scale: float, softcap: float = 0.0,
+                 prefix_len=None):
+    """q float64 [tokens][hq d] over the cache (layout of rope_append_kv's), one
+    query at a time.  Returns float64 [tokens][hq d], rows of no sequence NaN."""
+    k, v, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
+    pages, heads, page, d = k.shape
+    x = np.asarray(q, dtype=np.float64).reshape(len(q), heads_q, d)
+    out = np.full(x.shape, np.nan)
+    for b in range(len(kv_len)):
+        n, kv = int(q_start[b + 1] - q_start[b]), int(kv_len[b])
+        j = np.arange(kv)
+        at = np.array([int(table[b][i // page]) for i in j], dtype=np.int64)
+        there = (at >= 0) & (at < pages)
+        at = np.where(there, at, 0)
+        for h in range(heads):
+            kh = k[at, h, j % page].astype(np.float64) * ks[at, h].astype(np.float64)[:, None]
+            vh = v[at, h, :, j % page].astype(np.float64) * vs[at, h].astype(np.float64)[:, None]
+            for i in range(n):
+                pos = kv - n + i
+                seen = there & ((j <= pos) | (j < (int(prefix_len[b]) if prefix_len is not None else 0)))
+                for g in range(heads_q // heads):
+                    head = h * (heads_q // heads) + g
+                    if not seen.any():
+                        out[q_start[b] + i, head] = 0.0
+                        continue
+                    s = kh[seen] @ x[q_start[b] + i, head] * sm_scale
+                    if softcap:
+                        s = softcap * np.tanh(s / softcap)
+                    w = np.exp(s - s.max())
+                    out[q_start[b] + i, head] = w @ vh[seen] / w.sum()
+    return out.reshape(len(q), heads_q * d)

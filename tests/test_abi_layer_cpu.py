@@ -111,6 +111,8 @@ KV_BAD = [
     (dict(b=batch(n=-1)), q.QLIN_ERR_SHAPE), (dict(b=batch(max_q=-1)), q.QLIN_ERR_SHAPE),
     (dict(b=batch(max_kv=-1)), q.QLIN_ERR_SHAPE), (dict(b=batch(ld=3)), q.QLIN_ERR_SHAPE),
     (dict(b=batch(max_kv=65)), q.QLIN_ERR_SHAPE),
+    (dict(b=batch(max_kv=(1 << 30) + 1, ld=1 << 30)), q.QLIN_ERR_SHAPE),
+    (dict(b=batch(max_q=1 << 30)), q.QLIN_ERR_SHAPE),                  # x 2 query heads of a kv head
     (dict(c=cache(k=C1 + 8)), q.QLIN_ERR_ALIGN), (dict(c=cache(vs=C4 + 4)), q.QLIN_ERR_ALIGN),
     (dict(b=batch(kv_len=I3 + 2)), q.QLIN_ERR_ALIGN), (dict(b=batch(prefix=I4 + 1)), q.QLIN_ERR_ALIGN),
     (dict(dt=2), q.QLIN_ERR_DTYPE), (dict(dt=3), q.QLIN_ERR_DTYPE), (dict(dt=-1), q.QLIN_ERR_DTYPE),
@@ -144,6 +146,44 @@ def test_rope_append_empty_is_ok(lib):
     assert append(lib, b=batch(n=0, table=None, q_start=None, kv_len=None)) == q.QLIN_OK
     assert append(lib, b=batch(max_q=0)) == q.QLIN_OK
     assert append(lib, tokens=0, rot=0, rope=None, rope_len=0) == q.QLIN_OK
+
+
+def attention(lib, x=P, dt=1, tokens=20, ldq=4 * 64, hq=4, c=cache(), b=batch(), scale=0.125, cap=0.0, out=P2,
+              ldo=4 * 64, ws=None, wsb=0):
+    return lib.qlin_kv_attention(x, dt, tokens, ldq, hq, *refs(c, b), scale, cap, out, ldo, ws, wsb, None)
+
+
+LONG = dict(ld=64, max_kv=1024, max_q=1)      # few rows over many keys: takes a split
+
+
+@pytest.mark.parametrize("kw,status", KV_BAD + [
+    (dict(x=None), q.QLIN_ERR_NULL), (dict(out=None), q.QLIN_ERR_NULL), (dict(wsb=64), q.QLIN_ERR_NULL),
+    (dict(scale=float("nan")), q.QLIN_ERR_UNSUPPORTED), (dict(scale=float("inf")), q.QLIN_ERR_UNSUPPORTED),
+    (dict(cap=-1.0), q.QLIN_ERR_UNSUPPORTED), (dict(cap=float("nan")), q.QLIN_ERR_UNSUPPORTED),
+    (dict(ldq=248), q.QLIN_ERR_SHAPE), (dict(ldq=260), q.QLIN_ERR_SHAPE), (dict(ldo=250), q.QLIN_ERR_SHAPE),
+    (dict(ws=P4, wsb=-16), q.QLIN_ERR_SHAPE),
+    (dict(x=P + 2), q.QLIN_ERR_ALIGN), (dict(out=P2 + 4), q.QLIN_ERR_ALIGN), (dict(ws=P4 + 8, wsb=64), q.QLIN_ERR_ALIGN),
+    (dict(b=batch(**LONG), ws=P4, wsb=1024), q.QLIN_ERR_WORKSPACE),
+    (dict(out=P), q.QLIN_ERR_ALIAS), (dict(out=C1 + 4096), q.QLIN_ERR_ALIAS), (dict(out=C3), q.QLIN_ERR_ALIAS),
+    (dict(b=batch(**LONG), ws=C2, wsb=1 << 24), q.QLIN_ERR_ALIAS),
+    (dict(b=batch(**LONG), ws=P2 - 4096, wsb=1 << 24), q.QLIN_ERR_ALIAS),     # over out
+    (dict(b=batch(prefix=P2 + 64)), q.QLIN_ERR_ALIAS),
+])
+def test_kv_attention_rejects(lib, kw, status):
+    assert attention(lib, **kw) == status
+
+
+def test_kv_attention_empty_is_ok_and_workspace_bytes(lib):
+    assert attention(lib, tokens=0, x=None, out=None) == q.QLIN_OK
+    assert attention(lib, b=batch(n=0, table=None, q_start=None, kv_len=None)) == q.QLIN_OK
+    assert attention(lib, b=batch(max_q=0)) == q.QLIN_OK
+    def need(hq, c, b):
+        return lib.qlin_kv_attention_workspace_bytes(hq, *refs(c, b))
+
+    assert need(4, cache(), batch(**LONG)) > 0 and need(4, cache(), batch(**LONG)) % 16 == 0
+    assert need(4, cache(), batch(max_kv=0)) == 0
+    assert need(5, cache(), batch()) == -1
+    assert need(4, None, None) == -1
 
 
 @pytest.mark.parametrize("args,status", [

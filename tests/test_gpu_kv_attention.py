@@ -1,0 +1,296 @@
+"""Attention over the paged int8 cache against the float64 oracle (GPU only).
+
+The tolerance of an output value, from the kernel's roundings, with
+A = sum_j p_j |v_j| (the oracle on |v|) and n keys:
+  scores    d products and sums in fp32 and a handful of fp32 roundings of the
+            score: delta <= (d + 8) 2^-24 B, B bounding |sm_scale| sum |q||k|
+            (and the capped score, whose tanh form adds 2^-21 of the cap);
+            a weight moves by the factor e^delta, numerator and sum by 2 delta;
+  weights   exp2 and their product with the scale ratio in fp32 (4 x 2^-24),
+            one rounding to fp16: 2^-11 / 2 = 2^-12 of the weight, or, below
+            fp16's normal range, 2^-25 of the largest weight times the largest
+            |v| each: n 2^-25 max |v|;
+  sums      n additions in fp32: n 2^-24;
+  bf16 q    elements 2^-27 below the row's largest lose bits: 2^-39 of it, within B's slack;
+  output    its half step.
+All but the fp16 rounding are bounded by worst cases, so the test allows them once.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import bit_ptq_vla_amd as q
+import oracle
+from bit_ptq_vla_amd import synth
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+SEED = 313
+DT = {"f16": torch.float16, "bf16": torch.bfloat16}
+HALF_STEP = {"f16": 2.0 ** -11, "bf16": 2.0 ** -8}
+
+
+def f64(t):
+    return t.detach().cpu().to(torch.float64).numpy()
+
+
+def i32(a):
+    return torch.tensor(np.asarray(a), dtype=torch.int32, device=DEV)
+
+
+class Cache:
+    def __init__(self, pages, page, heads, d, seed=5, spread=1.0):
+        g = np.random.default_rng(seed)
+        codes = lambda shape: np.clip(np.rint(40 * g.standard_normal(shape)), -127, 127).astype(np.int8)  # noqa: E731
+        scales = lambda: (0.025 * np.exp(spread * 0.3 * g.standard_normal((pages, heads)))).astype(np.float32)  # noqa: E731
+        self.host = dict(k=codes((pages, heads, page, d)), v=codes((pages, heads, d, page)), k_scale=scales(),
+                         v_scale=scales())
+        self.order = g.permutation(pages)
+        self.upload()
+
+    def upload(self):
+        dev = {n: torch.from_numpy(a.copy()).to(DEV) for n, a in self.host.items()}
+        self.cache = q.KvCache(dev["k"], dev["k_scale"], dev["v"], dev["v_scale"])
+
+    def table(self, batch, cols):
+        return self.order[:batch * cols].reshape(batch, cols).astype(np.int32)
+
+
+def queries(tokens, cols, dtype, tag):
+    return synth.normal_tensor(SEED, f"attn/{tag}/{tokens}/{cols}", (tokens, cols), dtype=dtype)
+
+
+def check(out, x, c, table, q_start, kv_len, hq, scale, cap, prefix, dtype, rows=None):
+    d = c.cache.head_dim
+    args = (table, q_start, kv_len, hq, scale, cap, prefix)
+    ref = oracle.kv_attention(f64(x), c.host, *args)
+    vabs = dict(c.host, v=np.abs(c.host["v"].astype(np.int16)).astype(np.int16))
+    a = oracle.kv_attention(f64(x), vabs, *args)
+    rows = np.arange(q_start[0], q_start[-1]) if rows is None else rows
+    n = max(1, int(np.max(kv_len)))
+    kmax = 127.0 * float(np.max(c.host["k_scale"][np.isfinite(c.host["k_scale"])]))
+    vmax = 127.0 * float(np.max(c.host["v_scale"][np.isfinite(c.host["v_scale"])]))
+    b = abs(scale) * kmax * np.abs(f64(x)[rows]).reshape(-1, hq, d).sum(2)
+    if cap:
+        b = np.minimum(b, cap)
+    delta = (d + 8) * 2.0 ** -24 * b + (2.0 ** -21 * cap if cap else 0.0)
+    rel = np.repeat(2 * delta + 2.0 ** -12 + (n + 8) * 2.0 ** -24, d, axis=1)
+    tiny = 2.0 ** -25 if dtype == "f16" else 0.0
+    tol = rel * a[rows] * (1 + 2.0 ** -6) + n * 2.0 ** -25 * vmax + HALF_STEP[dtype] * np.abs(ref[rows]) * (1 + 2.0 ** -6) + tiny
+    err = np.abs(f64(out)[rows] - ref[rows])
+    assert np.all(err <= tol), f"worst {np.max(err / tol):.3g} of the tolerance, error {np.max(err):.3g}"
+
+
+def batch_of(table, q_start, kv_len, page, prefix=None, max_kv=None):
+    n = np.diff(q_start)
+    return q.KvBatch(i32(table), i32(q_start), i32(kv_len), max_q=int(n.max()),
+                     max_kv=max_kv if max_kv is not None else table.shape[1] * page,
+                     prefix_len=None if prefix is None else i32(prefix))
+
+
+CASES = [
+    # dtype, hq, hkv, d, page, cap, (new, cached, prefix or None) of each sequence
+    ("f16", 2, 2, 128, 16, 0.0, [(1, 0, None)]),
+    ("f16", 4, 4, 128, 16, 0.0, [(1, 816, None)]),
+    ("bf16", 8, 2, 128, 32, 0.0, [(1, 100, None), (1, 31, None), (1, 64, None), (0, 9, None), (0, 0, None), (1, 0, None)]),
+    ("bf16", 4, 1, 256, 64, 50.0, [(1, 300, None), (1, 62, None)]),
+    ("f16", 6, 2, 64, 16, 0.0, [(5, 40, None), (1, 3, None), (17, 0, None)]),
+    ("bf16", 20, 1, 64, 32, 0.0, [(1, 77, None), (2, 0, None)]),
+    ("f16", 2, 2, 128, 32, 0.0, [(50, 81, 131), (50, 16, 66)]),
+    ("bf16", 2, 2, 256, 64, 30.0, [(70, 0, 50), (33, 5, 0), (64, 64, 200)]),
+    ("f16", 8, 1, 64, 64, 0.0, [(40, 0, None)]),
+    ("bf16", 3, 1, 128, 16, 5.0, [(130, 3, 7), (97, 0, -4), (128, 64, 1000)]),
+    ("f16", 2, 1, 128, 64, 0.0, [(200, 37, None), (129, 0, None), (1, 500, None)]),
+    ("bf16", 4, 2, 64, 16, 0.0, [(64, 0, 64), (65, 1, 0), (63, 129, 3)]),
+    ("f16", 1, 1, 256, 16, 0.0, [(150, 20, None)]),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: f"{c[0]}-{c[1]}-{c[2]}-{c[3]}-p{c[4]}-cap{c[5]}-{len(c[6])}")
+def test_attention(case):
+    dtype, hq, hkv, d, page, cap, seqs = case
+    new, kv = np.array([s[0] for s in seqs]), np.array([s[0] + s[1] for s in seqs])
+    prefix = [s[2] for s in seqs] if seqs[0][2] is not None else None
+    cols = max(1, -(-int(kv.max()) // page))
+    c = Cache(len(seqs) * cols + 2, page, hkv, d)
+    table = c.table(len(seqs), cols)
+    q_start = np.concatenate([[0], np.cumsum(new)])
+    x = queries(int(q_start[-1]), hq * d, dtype, str(case))
+    b = batch_of(table, q_start, kv, page, prefix)
+    out = q.qlin_kv_attention(x.to(DEV), c.cache, b, hq, softcap=cap)
+    again = q.qlin_kv_attention(x.to(DEV), c.cache, b, hq, softcap=cap)
+    torch.cuda.synchronize()
+    check(out, x, c, table, q_start, kv, hq, d ** -0.5, cap, prefix, dtype)
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16))
+
+
+@pytest.mark.parametrize("hq,hkv,d,kv,page", [(2, 2, 128, 5003, 64), (8, 1, 64, 4097, 16), (2, 1, 256, 2900, 32)])
+def test_split_keys(hq, hkv, d, kv, page):
+    cols = -(-kv // page)
+    c = Cache(cols + 1, page, hkv, d, seed=9)
+    table = c.table(1, cols)
+    x = queries(2, hq * d, "f16", f"long{kv}") * 3.0
+    b = batch_of(table, [0, 2], [kv], page)
+    assert q.kv_attention_workspace_bytes(c.cache, b, hq) > 0
+    out = q.qlin_kv_attention(x.to(DEV), c.cache, b, hq)
+    torch.cuda.synchronize()
+    check(out, x, c, table, [0, 2], [kv], hq, d ** -0.5, 0.0, None, "f16")
+    # without a workspace: unsplit
+    one = torch.empty_like(out)
+    st = q.load().qlin_kv_attention(x.to(DEV).data_ptr(), q.QLIN_F16, 2, hq * d, hq, c.cache._ref, b._ref, d ** -0.5, 0.0,
+                                    one.data_ptr(), hq * d, None, 0, torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == q.QLIN_OK
+    check(one, x, c, table, [0, 2], [kv], hq, d ** -0.5, 0.0, None, "f16")
+
+
+def test_few_keys_in_a_large_bound():
+    # a workspace and a launch for 4096 keys; most splits are empty, one sequence has no tokens
+    hq, hkv, d, page = 4, 2, 128, 32
+    c = Cache(3 * 128, page, hkv, d)
+    table = c.table(3, 128)
+    x = queries(2, hq * d, "bf16", "few")
+    b = batch_of(table, [0, 1, 1, 2], [3, 0, 300], page)
+    work = q.kv_attention_workspace(c.cache, b, hq)
+    work.fill_(255)                                   # NaN everywhere
+    out = q.qlin_kv_attention(x.to(DEV), c.cache, b, hq, workspace=work)
+    torch.cuda.synchronize()
+    check(out, x, c, table, [0, 1, 1, 2], [3, 0, 300], hq, d ** -0.5, 0.0, None, "bf16")
+
+
+def test_rows_that_see_nothing_and_damaged_pages():
+    # index arithmetic of the same cases: test_index_arithmetic_stays_in_bounds
+    hq, hkv, d, page = 2, 1, 64, 16
+    c = Cache(12, page, hkv, d)
+    table = c.table(4, 3)
+    table[0, 1] = 12            # behind the pool: keys 16 .. 31 unseen
+    table[1, :] = -5            # nothing to see
+    table[2, 2] = 1 << 30
+    q_start, kv = [0, 30, 34, 74, 79], [40, 4, 40, 3]
+    prefix = [0, 4, 48, 0]      # the last sequence: two of five queries stand in front of the cache
+    x = queries(79, hq * d, "f16", "bad")
+    out = torch.full((79, hq * d), 7.0, dtype=torch.float16, device=DEV)
+    q.qlin_kv_attention(x.to(DEV), c.cache, batch_of(table, q_start, kv, page, prefix), hq, out=out)
+    torch.cuda.synchronize()
+    check(out, x, c, table, q_start, kv, hq, d ** -0.5, 0.0, prefix, "f16")
+    assert not out[30:34].any() and not out[74:76].any()
+
+
+def test_what_lies_outside_the_cache_does_not_count():
+    # scales of unused pages, codes behind the last token and rows of no sequence
+    hq, hkv, d, page = 4, 2, 128, 32
+    c = Cache(6, page, hkv, d)
+    table = c.table(1, 3)
+    for other in set(range(6)) - set(table[0, :2].tolist()):
+        c.host["k_scale"][other] = np.nan
+        c.host["v_scale"][other] = np.inf
+    c.upload()
+    x = queries(6, hq * d, "bf16", "outside")
+    out = torch.full((6, hq * d + 8), 3.0, dtype=torch.bfloat16, device=DEV)
+    xp = torch.zeros((6, hq * d + 16), dtype=torch.bfloat16, device=DEV)
+    xp[:, :hq * d] = x.to(DEV)
+    b = q.KvBatch(i32(table), i32([1, 4]), i32([35]), max_q=3, max_kv=96)
+    q.qlin_kv_attention(xp[:, :hq * d], c.cache, b, hq, out=out[:, :hq * d])
+    torch.cuda.synchronize()
+    clean = dict(c.host)
+    clean["k_scale"], clean["v_scale"] = np.nan_to_num(c.host["k_scale"]), np.where(np.isfinite(c.host["v_scale"]), c.host["v_scale"], 0).astype(np.float32)
+    c.host = clean
+    check(out[:, :hq * d], x, c, table, [1, 4], [35], hq, d ** -0.5, 0.0, None, "bf16")
+    assert torch.all(out[0] == 3.0) and torch.all(out[4:] == 3.0) and torch.all(out[:, hq * d:] == 3.0)
+
+
+def test_queries_of_any_size():
+    # bf16 rows from 1e-30 to 1e30, a zero row, and damaged rows that stay alone
+    hq, hkv, d, page = 1, 1, 128, 16
+    c = Cache(4, page, hkv, d)
+    table = c.table(1, 4)
+    x = queries(7, d, "bf16", "sizes")
+    for i, f in enumerate([1e-30, 1e30, 1.0, 0.0, 1.0, 1.0, 30.0]):
+        x[i] = x[i] * f
+    x[4, 7] = float("nan")
+    x[5, 9] = float("inf")
+    out = q.qlin_kv_attention(x.to(DEV), c.cache, batch_of(table, [0, 7], [60], page), hq)
+    torch.cuda.synchronize()
+    for i in (0, 2, 3, 6):
+        with np.errstate(invalid="ignore"):
+            check(out, x, c, table, [0, 7], [60], hq, d ** -0.5, 0.0, None, "bf16", rows=np.array([i]))
+    assert torch.isfinite(out[1]).all() and not torch.isfinite(out[4]).any()
+
+
+def test_scales_of_very_different_pages():
+    # v scales over sixty octaves: small pages neither vanish from the fp16 weights nor overflow them
+    hq, hkv, d, page = 2, 1, 64, 16
+    c = Cache(20, page, hkv, d)
+    c.host["v_scale"] = np.exp2(np.linspace(-30, 30, 20)).astype(np.float32)[np.random.default_rng(1).permutation(20)][:, None].copy()
+    c.upload()
+    for first in range(0, 20, 4):                     # alone, and behind larger or smaller ones
+        order = np.argsort(c.host["v_scale"][:, 0])[::-1 if first % 8 else 1]
+        table = np.roll(order, first)[None, :].astype(np.int32)
+        x = queries(3, hq * d, "bf16", f"pages{first}") * 4.0
+        out = q.qlin_kv_attention(x.to(DEV), c.cache, batch_of(table, [0, 3], [320], page), hq)
+        torch.cuda.synchronize()
+        check(out, x, c, table, [0, 3], [320], hq, d ** -0.5, 0.0, None, "bf16")
+
+
+def test_cache_past_32_bit_offsets():
+    # 40000 pages x 8 heads x 64 x 128 = 2.6 GB each of k and v; the sequence lies at its end
+    hq, hkv, d, page, pages = 8, 8, 128, 64, 40000
+    big = q.KvCache.empty(pages, page, hkv, d, DEV)
+    small = Cache(4, page, hkv, d)
+    at = [39999, 33000, 39998, 20]
+    for i, p in enumerate(at):
+        big.k[p].copy_(small.cache.k[i])
+        big.v[p].copy_(small.cache.v[i])
+        big.k_scale[p].copy_(small.cache.k_scale[i])
+        big.v_scale[p].copy_(small.cache.v_scale[i])
+    x = queries(40, hq * d, "bf16", "big")
+    out = q.qlin_kv_attention(x.to(DEV), big, batch_of(np.array([at]), [0, 40], [250], page), hq)
+    torch.cuda.synchronize()
+    check(out, x, small, np.arange(4)[None, :], [0, 40], [250], hq, d ** -0.5, 0.0, None, "bf16")
+    del big
+
+
+def test_stream_and_replayed_graph():
+    hq, hkv, d, page = 4, 2, 128, 16
+    c = Cache(70, page, hkv, d)
+    table = c.table(2, 32)
+    x = queries(2, hq * d, "bf16", "g").to(DEV)
+    kv = i32([400, 7])
+    b = q.KvBatch(i32(table), i32([0, 1, 2]), kv, max_q=1, max_kv=512)
+    work = q.kv_attention_workspace(c.cache, b, hq)
+    out = torch.empty_like(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        q.qlin_kv_attention(x, c.cache, b, hq, out=out, workspace=work)
+    side.synchronize()
+    check(out, x, c, table, [0, 1, 2], [400, 7], hq, d ** -0.5, 0.0, None, "bf16")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        q.qlin_kv_attention(x, c.cache, b, hq, out=out, workspace=work)
+    for t, lens in enumerate([[1, 512], [300, 301], [0, 40]]):      # the graph reads the lengths
+        x.copy_(queries(2, hq * d, "bf16", f"g{t}"))
+        kv.copy_(torch.tensor(lens))
+        g.replay()
+        torch.cuda.synchronize()
+        check(out, x, c, table, [0, 1, 2], lens, hq, d ** -0.5, 0.0, None, "bf16")
+
+
+def test_refused_calls():
+    c = Cache(4, 16, 1, 64)
+    table = c.table(1, 2)
+    b = batch_of(table, [0, 2], [20], 16)
+    x = torch.zeros((2, 2 * 64), dtype=torch.float16, device=DEV)
+    with pytest.raises(ValueError):
+        q.qlin_kv_attention(x, c.cache, b, 1)
+    with pytest.raises(ValueError):
+        q.qlin_kv_attention(x, c.cache, b, 2, out=torch.empty_like(x).bfloat16())
+    with pytest.raises(ValueError):
+        q.qlin_kv_attention(x, c.cache, batch_of(table, [0, 2], [20], 16, max_kv=33), 2)
+    with pytest.raises(q.QlinError):
+        q.qlin_kv_attention(x.float(), c.cache, b, 2)
+    with pytest.raises(q.QlinError):
+        q.qlin_kv_attention(x, c.cache, b, 2, softcap=-1.0)
+    with pytest.raises(q.QlinError):
+        q.qlin_kv_attention(x, c.cache, b, 2, out=x)

@@ -122,3 +122,43 @@ def test_append_keeps_damaged_values_out_of_the_scale():
     x[0, 4:8] = [np.inf, -np.inf, np.nan, 127.0]
     oracle.rope_append_kv(x, c, [[0]], [0, 2], [2], 1, None, 0, False)
     assert c["k_scale"][0, 0] == 1.0 and c["k"][0, 0, 0].tolist() == [127, -127, 0, 127]
+
+
+# ---- attention over the paged cache
+
+def filled(pages, heads, page, d, seed=3):
+    g = np.random.default_rng(seed)
+    return dict(k=g.integers(-127, 128, (pages, heads, page, d), dtype=np.int8),
+                v=g.integers(-127, 128, (pages, heads, d, page), dtype=np.int8),
+                k_scale=g.uniform(0.005, 0.02, (pages, heads)).astype(np.float32),
+                v_scale=g.uniform(0.005, 0.02, (pages, heads)).astype(np.float32))
+
+
+@pytest.mark.parametrize("prefix", [None, 0, 6, 11])
+def test_attention_is_torchs(prefix):
+    heads, group, d, page, n, kv = 2, 2, 8, 4, 5, 11
+    c = filled(5, heads, page, d)
+    table = [[3, 0, 4]]
+    x = rng(10).standard_normal((n, heads * group * d))
+    got = oracle.kv_attention(x, c, table, [0, n], [kv], heads * group, 0.3, 0.0, None if prefix is None else [prefix])
+    k = np.concatenate([c["k"][p].astype(float) * c["k_scale"][p][:, None, None] for p in table[0]], 1)[:, :kv]
+    v = np.concatenate([(c["v"][p].astype(float) * c["v_scale"][p][:, None, None]).transpose(0, 2, 1) for p in table[0]], 1)[:, :kv]
+    mask = torch.ones(n, kv).tril(kv - n).bool()
+    mask[:, :prefix or 0] = True
+    q = torch.from_numpy(x.reshape(n, heads, group, d)).permute(1, 2, 0, 3)
+    ref = torch.nn.functional.scaled_dot_product_attention(
+        q, torch.from_numpy(k)[:, None].expand(-1, group, -1, -1), torch.from_numpy(v)[:, None].expand(-1, group, -1, -1),
+        attn_mask=mask, scale=0.3)
+    assert np.allclose(got, ref.permute(2, 0, 1, 3).reshape(n, -1).numpy(), rtol=1e-12)
+
+
+def test_attention_corner_rows():
+    c = filled(2, 1, 4, 8)
+    x = rng(11).standard_normal((3, 8))
+    # the first of three queries stands in front of the cache; a page outside the pool hides its keys
+    got = oracle.kv_attention(x, c, [[0]], [0, 3], [2], 1, 1.0)
+    assert not got[0].any() and np.allclose(got[1], c["v"][0, 0, :, 0] * np.float64(c["v_scale"][0, 0]), rtol=1e-12)
+    assert not oracle.kv_attention(x, c, [[9]], [0, 3], [3], 1, 1.0).any()
+    # a very small cap makes every score the same: the mean of the values
+    got = oracle.kv_attention(x[:1], c, [[1]], [0, 1], [4], 1, 1.0, softcap=1e-12)
+    assert np.allclose(got[0], c["v"][1, 0].astype(float).mean(1) * c["v_scale"][1, 0], rtol=1e-9)
