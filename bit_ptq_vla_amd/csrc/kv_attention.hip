@@ -21,7 +21,7 @@
 // brings the row's maximum to 2^13..2^14: exact but for elements 2^-27 below
 // that maximum.  Scores, statistics and sums are fp32.  The weights are rounded
 // to fp16 after multiplication by vs_j / vr, vr the largest v scale met so far
-// (<= 1, so they neither overflow nor lose the small pages): 2^-12 each, under
+// (<= 1, so they neither overflow nor lose the small pages): 2^-11 each at most, under
 // the output's own half step.
 
 #include "device_common.h"
@@ -292,6 +292,294 @@ __global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
     }
 }
 
+// ---- many query rows ---------------------------------------------------------
+
+// Byte offset of 16-byte chunk `c` of K row `row` in LDS: D fp16 a row, chunks
+// xor-swizzled so that eight lanes reading one chunk of eight rows meet eight
+// different bank groups.
+template <int D>
+__device__ __forceinline__ int k_off(int row, int c) {
+    constexpr int M = D / 8 < 16 ? D / 8 - 1 : 15;
+    return row * D * 2 + ((c ^ (row & M)) << 4);
+}
+// The same for V: 64 keys (8 chunks) a dimension.
+__device__ __forceinline__ int v_off(int d, int c) { return d * 128 + ((c ^ (d & 7)) << 4); }
+
+// The LDS row of key j (0..63) of a step.  The 32x32 product leaves lane half h
+// with rows 8 (i / 4) + 4 h + i % 4 in element i; with this order elements
+// 8 u .. 8 u + 7 of a lane are keys 16 u + 8 h + (0..7): B operand u of P^T as
+// it stands, against V in its stored order.
+__device__ __forceinline__ int key_row(int j) {
+    return (j & 48) | ((j & 4) << 1) | ((j & 8) >> 1) | (j & 3);
+}
+
+// 32 * NW query rows of one (sequence, kv head), 32 to a wave, against a range
+// of its keys.  The block turns each step's 64 keys into fp16 in LDS once (v
+// times its page's scale over the largest met) and every wave multiplies
+// v_mfma_f32_32x32x16_f16 tiles from there; the next step's codes are in
+// flight meanwhile, and two LDS buffers leave one barrier a step.
+template <int DT, int D, bool CAP, int NW>
+__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void kv_attn_tile_kernel(AttnParams p) {
+    constexpr int TPB = 64 * NW;
+    constexpr int NS = D / 16;            // k steps of S
+    constexpr int ND = D / 32;            // 32-dimension tiles of the output
+    constexpr int NC = D * 4 / TPB;       // 16-byte pieces of k (and of v) a thread stages per step
+    constexpr int KB = 64 * D * 2;        // bytes of one operand of a step in LDS
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    typedef float f16v __attribute__((ext_vector_type(16)));
+
+    int64_t u = blockIdx.x;
+    const int h = static_cast<int>(u % p.heads);
+    u /= p.heads;
+    const int sp = static_cast<int>(u % p.splits);
+    u /= p.splits;
+    const int b = static_cast<int>(u % p.ix.batch);
+    const int rt = p.row_tiles - 1 - static_cast<int>(u / p.ix.batch);   // the longest first
+    const KvSeq s = kv_seq(p.ix, b);
+    const int rows = s.n * p.group, r0 = rt * 32 * NW;
+    if (r0 >= rows) return;
+    const int last = (r0 + 32 * NW < rows ? r0 + 32 * NW : rows) - 1;
+    const int vis_hi = row_of(p, s, b, h, last).vis;
+    const int k0 = sp * p.split_keys;
+    if (sp > 0 && k0 >= vis_hi) return;
+    const int k1 = k0 + p.split_keys < vis_hi ? k0 + p.split_keys : vis_hi;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int c = lane & 31, hf = lane >> 5;
+    const int rw = r0 + 32 * wave;                       // the wave's first row
+    const Row row = row_of(p, s, b, h, rw + c < rows ? rw + c : last);
+    const int vis = rw + c < rows ? row.vis : 0;
+    // the wave's rows see at least / at most these keys
+    const int wave_lo = rw + 31 < rows ? row_of(p, s, b, h, rw).vis : 0;
+    const int wave_hi = rw < rows ? row_of(p, s, b, h, rw + 31 < rows ? rw + 31 : last).vis : 0;
+    const int ps = p.ix.page_size, psl = 31 - __builtin_clz(ps);
+    const int last_idx = s.kv > 0 ? (s.kv - 1) >> psl : 0;
+
+    // queries: dimensions 16 s + 8 hf .. + 7 of row c
+    h8 qf[NS];
+    float qmul = p.sm_scale;
+    {
+        const char* src = static_cast<const char*>(p.q) + (row.token * p.ldq + static_cast<int64_t>(row.head) * D) * 2;
+        int e = 0;
+        if constexpr (DT == BF16) {
+            float top = 0.f;
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+                float f[8];
+                load8<DT>(src + (16 * j + 8 * hf) * 2, f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
+            }
+            top = fmaxf(top, lane_xor<32>(top));
+            if (top > 0.f && top < __builtin_inff()) e = 14 - __builtin_amdgcn_frexp_expf(top);
+            e = e > 120 ? 120 : e < -120 ? -120 : e;
+            qmul = __builtin_amdgcn_ldexpf(p.sm_scale, -e);
+        }
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+            float f[8];
+            load8<DT>(src + (16 * j + 8 * hf) * 2, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                qf[j][i] = static_cast<_Float16>(DT == BF16 ? __builtin_amdgcn_ldexpf(f[i], e) : f[i]);
+        }
+    }
+    qmul *= CAP ? 2.f * kLog2e / p.cap : kLog2e;
+    const float cap_out = CAP ? p.cap * kLog2e : 0.f;
+
+    f16v o[ND];
+#pragma unroll
+    for (int t = 0; t < ND; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[t][i] = 0.f;
+    float m = kNegInf, l = 0.f, vr = 0.f;
+
+    // one step's codes on their way, and its granules' pages and scales
+    u4 kw[NC], vw[NC];
+    int pg[4];
+    float ksc[4], vsc[4];
+    auto fetch = [&](int t0) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            int idx = (t0 + 16 * x) >> psl;
+            idx = idx < last_idx ? idx : last_idx;
+            pg[x] = t0 + 16 * x < s.kv ? kv_page(p.ix, b, idx) : kNoPage;
+            const int64_t at = static_cast<int64_t>(pg[x] < 0 ? 0 : pg[x]) * p.heads + h;
+            ksc[x] = pg[x] < 0 ? 0.f : p.ks[at];
+            vsc[x] = pg[x] < 0 ? 0.f : p.vs[at];
+        }
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+            const int i = tid + n * TPB;
+            const int key = i / (D / 16), kc = i % (D / 16), vd = i >> 2, vg = i & 3;
+            const int gk = key >> 4;
+            const int pk = gk < 2 ? (gk == 0 ? pg[0] : pg[1]) : (gk == 2 ? pg[2] : pg[3]);
+            const int pv = vg < 2 ? (vg == 0 ? pg[0] : pg[1]) : (vg == 2 ? pg[2] : pg[3]);
+            const int64_t sk = static_cast<int64_t>(pk < 0 ? 0 : pk) * p.heads + h;
+            const int64_t sv = static_cast<int64_t>(pv < 0 ? 0 : pv) * p.heads + h;
+            kw[n] = *reinterpret_cast<const u4*>(p.k + sk * ps * D + ((t0 + key) & (ps - 1)) * D + 16 * kc);
+            vw[n] = *reinterpret_cast<const u4*>(p.v + sv * ps * D + vd * ps + ((t0 + 16 * vg) & (ps - 1)));
+        }
+    };
+    // the fetched step into buffer `buf`, and its granules' scales and flags
+    float mul[4], unit = 0.f, vlog[4], vinv[4];
+    int dead = 0;
+    auto stage = [&](int buf) {
+        char* kl = lds + buf * 2 * KB;
+        char* vl = kl + KB;
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+            const int i = tid + n * TPB;
+            const int key = i / (D / 16), kc = i % (D / 16), vd = i >> 2, vg = i & 3;
+            const int kr = key_row(key);
+            *reinterpret_cast<h8*>(kl + k_off<D>(kr, 2 * kc)) = codes_f16(kw[n][0], kw[n][1]);
+            *reinterpret_cast<h8*>(kl + k_off<D>(kr, 2 * kc + 1)) = codes_f16(kw[n][2], kw[n][3]);
+            *reinterpret_cast<h8*>(vl + v_off(vd, 2 * vg)) = codes_f16(vw[n][0], vw[n][1]);
+            *reinterpret_cast<h8*>(vl + v_off(vd, 2 * vg + 1)) = codes_f16(vw[n][2], vw[n][3]);
+        }
+        unit = fmaxf(unit, fmaxf(fmaxf(vsc[0], vsc[1]), fmaxf(vsc[2], vsc[3])));
+        dead = 0;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            mul[x] = ksc[x];
+            // a page 2^-30 below the largest keeps that ratio: its weights leave fp16 there anyway
+            vlog[x] = unit > 0.f ? fmaxf(__builtin_amdgcn_logf(vsc[x] / unit), -30.f) : 0.f;
+            vinv[x] = __builtin_amdgcn_exp2f(-vlog[x]);
+            dead |= (pg[x] < 0) << x;
+        }
+    };
+
+    int buf = 0;
+    if (k0 < k1) {
+        fetch(k0);
+        stage(0);
+    }
+    __syncthreads();
+    for (int t0 = k0; t0 < k1; t0 += 64, buf ^= 1) {
+        const bool more = t0 + 64 < k1;
+        if (more) fetch(t0 + 64);
+        if (t0 < wave_hi) {
+            const char* kl = lds + buf * 2 * KB;
+            const char* vl = kl + KB;
+            float x[32];
+#pragma unroll
+            for (int T = 0; T < 2; ++T) {
+                f16v acc;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+#pragma unroll
+                for (int j = 0; j < NS; ++j)
+                    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                        *reinterpret_cast<const h8*>(kl + k_off<D>(32 * T + c, 2 * j + hf)), qf[j], acc, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[16 * T + i] = acc[i];
+            }
+            // element 8 g + e is key 16 g + 8 hf + e of the step
+            if (CAP) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = score<CAP>(x[i], qmul * mul[i >> 3], 0.f, cap_out);
+            }
+            const bool whole = t0 + 64 <= wave_lo && dead == 0;
+            float top = kNegInf;
+            float sc[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                sc[g] = CAP ? 1.f : qmul * mul[g];
+                if (!whole) {
+                    const int lim = (dead >> g & 1) ? 0 : vis - (t0 + 16 * g + 8 * hf);
+                    // masked scores leave as the value that scales to -inf (a zero scale: all scores 0)
+                    const float out = sc[g] < 0.f ? -kNegInf : kNegInf;
+                    const bool zero = sc[g] == 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[8 * g + e] = e < lim ? (zero ? 0.f : x[8 * g + e]) : out;
+                    if (zero) sc[g] = 1.f;
+                }
+                float hi = x[8 * g];
+                if (!CAP && p.sm_scale < 0.f) {
+#pragma unroll
+                    for (int e = 1; e < 8; ++e) hi = fminf(hi, x[8 * g + e]);
+                } else {
+#pragma unroll
+                    for (int e = 1; e < 8; ++e) hi = fmaxf(hi, x[8 * g + e]);
+                }
+                top = fmaxf(top, hi * sc[g]);
+            }
+            top = fmaxf(top, lane_xor<32>(top));
+            // the reference follows the maximum once that is 2^8 past it: weights stay
+            // below 2^8, far inside fp16, and most steps rescale nothing
+            if (__any(top > m + 8.f || unit != vr)) {
+                const float mn = fmaxf(m, top);
+                const float r = m > kNegInf ? __builtin_amdgcn_exp2f(m - mn) : 1.f;
+                const float ro = r * (vr > 0.f ? vr / unit : 1.f);
+#pragma unroll
+                for (int t = 0; t < ND; ++t)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[t][i] *= ro;
+                l *= r;
+                m = mn;
+                vr = unit;
+            }
+            const float base = m > kNegInf ? m : 0.f;        // nothing seen yet: all weights 0
+            h8 pf[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                // weights times the page's v scale over the unit; the sum takes that out again
+                const float off = vlog[g] - base;
+                float sum = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float w = __builtin_amdgcn_exp2f(fmaf(x[8 * g + e], sc[g], off));
+                    sum += w;
+                    pf[g][e] = static_cast<_Float16>(w);
+                }
+                l = fmaf(sum, vinv[g], l);
+            }
+#pragma unroll
+            for (int t = 0; t < ND; ++t)
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    o[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                        *reinterpret_cast<const h8*>(vl + v_off(32 * t + c, 2 * g + hf)), pf[g], o[t], 0, 0, 0);
+        }
+        if (more) stage(buf ^ 1);
+        __syncthreads();
+    }
+
+    l += lane_xor<32>(l);
+    if (rw + c >= rows) return;
+    // element i of tile t is dimension 32 t + 8 (i / 4) + 4 hf + i % 4 of query c
+    if (p.splits == 1) {
+        const float inv = l > 0.f ? vr / l : 0.f;
+        char* dst = static_cast<char*>(p.out) + (row.token * p.ldo + static_cast<int64_t>(row.head) * D + 4 * hf) * 2;
+#pragma unroll
+        for (int t = 0; t < ND; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                uint2 w;
+                if constexpr (DT == BF16) {
+                    w.x = pk_bf16(o[t][i] * inv, o[t][i + 1] * inv);
+                    w.y = pk_bf16(o[t][i + 2] * inv, o[t][i + 3] * inv);
+                } else {
+                    w.x = f32_to_f16_bits(o[t][i] * inv) | static_cast<uint32_t>(f32_to_f16_bits(o[t][i + 1] * inv)) << 16;
+                    w.y = f32_to_f16_bits(o[t][i + 2] * inv) | static_cast<uint32_t>(f32_to_f16_bits(o[t][i + 3] * inv)) << 16;
+                }
+                *reinterpret_cast<uint2*>(dst + (32 * t + 2 * i) * 2) = w;
+            }
+    } else {
+        const int64_t at = ((static_cast<int64_t>(sp) * p.ix.batch * p.ix.max_q + row.slot) * p.heads_q + row.head);
+#pragma unroll
+        for (int t = 0; t < ND; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<float4*>(p.part_o + at * D + 32 * t + 2 * i + 4 * hf) =
+                    make_float4(o[t][i] * vr, o[t][i + 1] * vr, o[t][i + 2] * vr, o[t][i + 3] * vr);
+        if (hf == 0) {
+            p.part_ml[2 * at] = m;
+            p.part_ml[2 * at + 1] = l;
+        }
+    }
+}
+
 // Joins the splits of every (token, head): D / 8 lanes each.
 template <int DT, int D>
 __global__ __launch_bounds__(256) void kv_attn_join_kernel(AttnParams p) {
@@ -324,9 +612,18 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(AttnParams p) {
 }
 
 template <int DT, int D>
-hipError_t launch_d(const AttnParams& p, hipStream_t st) {
+hipError_t launch_d(const AttnParams& p, bool tile, hipStream_t st) {
     const int64_t blocks = static_cast<int64_t>(p.ix.batch) * p.heads * p.row_tiles * p.splits;
-    if (p.cap > 0.f)
+    if (tile) {
+        constexpr int bytes = 2 * 2 * 64 * D * 2;
+        auto kernel = p.cap > 0.f ? kv_attn_tile_kernel<DT, D, true, 4> : kv_attn_tile_kernel<DT, D, false, 4>;
+        if (bytes > 65536) {
+            const hipError_t a = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+            if (a != hipSuccess) return a;
+        }
+        kernel<<<dim3(static_cast<unsigned>(blocks)), 256, bytes, st>>>(p);
+    } else if (p.cap > 0.f)
         kv_attn_rows16_kernel<DT, D, true><<<dim3(static_cast<unsigned>(blocks)), 256, 0, st>>>(p);
     else
         kv_attn_rows16_kernel<DT, D, false><<<dim3(static_cast<unsigned>(blocks)), 256, 0, st>>>(p);
@@ -338,10 +635,10 @@ hipError_t launch_d(const AttnParams& p, hipStream_t st) {
 }
 
 template <int DT>
-hipError_t launch_dt(const AttnParams& p, int d, hipStream_t st) {
-    if (d == 64) return launch_d<DT, 64>(p, st);
-    if (d == 128) return launch_d<DT, 128>(p, st);
-    return launch_d<DT, 256>(p, st);
+hipError_t launch_dt(const AttnParams& p, int d, bool tile, hipStream_t st) {
+    if (d == 64) return launch_d<DT, 64>(p, tile, st);
+    if (d == 128) return launch_d<DT, 128>(p, tile, st);
+    return launch_d<DT, 256>(p, tile, st);
 }
 
 }  // namespace
@@ -356,7 +653,7 @@ hipError_t launch_kv_attention(const KvAttnPlan& plan, const void* q, int dtype,
         p.part_o = static_cast<float*>(ws);
         p.part_ml = p.part_o + static_cast<int64_t>(plan.splits) * ix.batch * ix.max_q * heads_q * d;
     }
-    return dtype == F16 ? launch_dt<F16>(p, d, st) : launch_dt<BF16>(p, d, st);
+    return dtype == F16 ? launch_dt<F16>(p, d, plan.tile, st) : launch_dt<BF16>(p, d, plan.tile, st);
 }
 
 }  // namespace qlin

@@ -174,7 +174,9 @@ KvAttnPlan plan_kv_attention(int64_t batch, int64_t max_q, int64_t max_kv, int h
                              bool allow_split) {
     KvAttnPlan p;
     const int64_t rows = max_q * (heads_q / heads);
-    p.row_tiles = static_cast<int>((rows + 15) / 16);
+    p.tile = rows > 64;
+    const int64_t per = p.tile ? 128 : 16;
+    p.row_tiles = static_cast<int>((rows + per - 1) / per);
     const int64_t units = batch * heads * p.row_tiles;
     // few tiles: their keys are split until there are two blocks for each CU,
     // 256 keys (a step of the block's four waves) at least to each

@@ -113,6 +113,7 @@ hipError_t launch_rope_table(float* table, int64_t positions, int rot, double ba
 // blocks share a tile's keys (split_keys each; their partials, ws_bytes, are
 // joined by a second kernel).
 struct KvAttnPlan {
+    bool tile;   // 128 rows to a block, else 16
     int row_tiles, splits, split_keys;
     int64_t blocks, ws_bytes;
 };

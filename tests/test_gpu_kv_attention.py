@@ -7,8 +7,8 @@ A = sum_j p_j |v_j| (the oracle on |v|) and n keys:
             (and the capped score, whose tanh form adds 2^-21 of the cap);
             a weight moves by the factor e^delta, numerator and sum by 2 delta;
   weights   exp2 and their product with the scale ratio in fp32 (4 x 2^-24),
-            one rounding to fp16: 2^-11 / 2 = 2^-12 of the weight, or, below
-            fp16's normal range, 2^-25 of the largest weight times the largest
+            one rounding to fp16: at most 2^-11 of the weight (half of a step
+            of eps 2^-10), or, below fp16's normal range, 2^-25 of the largest weight times the largest
             |v| each: n 2^-25 max |v|;
   sums      n additions in fp32: n 2^-24;
   bf16 q    elements 2^-27 below the row's largest lose bits: 2^-39 of it, within B's slack;
@@ -75,7 +75,7 @@ def check(out, x, c, table, q_start, kv_len, hq, scale, cap, prefix, dtype, rows
     if cap:
         b = np.minimum(b, cap)
     delta = (d + 8) * 2.0 ** -24 * b + (2.0 ** -21 * cap if cap else 0.0)
-    rel = np.repeat(2 * delta + 2.0 ** -12 + (n + 8) * 2.0 ** -24, d, axis=1)
+    rel = np.repeat(2 * delta + 2.0 ** -11 + (n + 8) * 2.0 ** -24, d, axis=1)
     tiny = 2.0 ** -25 if dtype == "f16" else 0.0
     tol = rel * a[rows] * (1 + 2.0 ** -6) + n * 2.0 ** -25 * vmax + HALF_STEP[dtype] * np.abs(ref[rows]) * (1 + 2.0 ** -6) + tiny
     err = np.abs(f64(out)[rows] - ref[rows])
@@ -224,13 +224,30 @@ def test_scales_of_very_different_pages():
     c = Cache(20, page, hkv, d)
     c.host["v_scale"] = np.exp2(np.linspace(-30, 30, 20)).astype(np.float32)[np.random.default_rng(1).permutation(20)][:, None].copy()
     c.upload()
-    for first in range(0, 20, 4):                     # alone, and behind larger or smaller ones
+    for first, rows in ((0, 3), (4, 3), (8, 70), (12, 3), (16, 70)):      # behind larger or smaller ones
         order = np.argsort(c.host["v_scale"][:, 0])[::-1 if first % 8 else 1]
         table = np.roll(order, first)[None, :].astype(np.int32)
-        x = queries(3, hq * d, "bf16", f"pages{first}") * 4.0
-        out = q.qlin_kv_attention(x.to(DEV), c.cache, batch_of(table, [0, 3], [320], page), hq)
+        x = queries(rows, hq * d, "bf16", f"pages{first}") * 4.0
+        out = q.qlin_kv_attention(x.to(DEV), c.cache, batch_of(table, [0, rows], [320], page), hq)
         torch.cuda.synchronize()
-        check(out, x, c, table, [0, 3], [320], hq, d ** -0.5, 0.0, None, "bf16")
+        check(out, x, c, table, [0, rows], [320], hq, d ** -0.5, 0.0, None, "bf16")
+
+
+@pytest.mark.parametrize("rows", [2, 140])
+@pytest.mark.parametrize("scale", [0.0, -0.2])
+def test_zero_scales_and_signs(rows, scale):
+    # pages whose scale is 0 (all their keys alike), masked keys among them; a zero and a negative sm_scale
+    hq, hkv, d, page = 1, 1, 128, 16
+    c = Cache(12, page, hkv, d)
+    c.host["k_scale"][c.order[[1, 8, 9]]] = 0.0
+    c.host["v_scale"][c.order[[2, 9]]] = 0.0
+    c.upload()
+    table = c.table(1, 10)
+    x = queries(rows, d, "bf16", f"zero{rows}")
+    for cap in (0.0, 20.0):
+        out = q.qlin_kv_attention(x.to(DEV), c.cache, batch_of(table, [0, rows], [155], page), hq, sm_scale=scale, softcap=cap)
+        torch.cuda.synchronize()
+        check(out, x, c, table, [0, rows], [155], hq, scale, cap, None, "bf16")
 
 
 def test_cache_past_32_bit_offsets():
