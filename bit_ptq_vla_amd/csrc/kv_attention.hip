@@ -21,8 +21,7 @@
 // brings the row's maximum to 2^13..2^14: exact but for elements 2^-27 below
 // that maximum.  Scores, statistics and sums are fp32.  The weights are rounded
 // to fp16 after multiplication by vs_j / vr, vr the largest v scale met so far
-// (<= 1, so they neither overflow nor lose the small pages): 2^-11 each at most, under
-// the output's own half step.
+// (in the exponent; no page overflows them): 2^-11 each at most.
 
 #include "device_common.h"
 #include "kv_index.h"
@@ -175,29 +174,42 @@ __global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
 #pragma unroll
     for (int t = 0; t < ND; ++t) o[t] = f4{0.f, 0.f, 0.f, 0.f};
     float m = kNegInf, l = 0.f, vr = 0.f;
-    const int last_idx = s.kv > 0 ? (s.kv - 1) / ps : 0;
+    const int psl = 31 - __builtin_clz(ps);
+    const int last_idx = s.kv > 0 ? (s.kv - 1) >> psl : 0;
     const int gk = c >> 2;                   // granule of the lane's K rows
+    const int32_t* table = p.ix.page_table + static_cast<int64_t>(b) * p.ix.table_ld;
+    const int64_t page_bytes = static_cast<int64_t>(ps) * D, pool_step = page_bytes * p.heads;
+    // t0 is a multiple of 64: a granule's place in its page does not depend on it
+    const int8_t* kh = p.k + h * page_bytes + (((16 * gk) & (ps - 1)) + (c & 3)) * D + 16 * g;
+    const int8_t* vh = p.v + h * page_bytes + c * ps + ((16 * g) & (ps - 1));
+    auto page_ahead = [&](int t0, int gran) {
+        const int idx = (t0 + 16 * gran) >> psl;
+        return table[idx < last_idx ? idx : last_idx];
+    };
+    // granules past the cache read its last page (their keys are masked)
+    int nk = 0, nv = 0;
+    if (k0 + 64 * wave < k1) {
+        nk = page_ahead(k0 + 64 * wave, gk);
+        nv = page_ahead(k0 + 64 * wave, g);
+    }
 
     for (int t0 = k0 + 64 * wave; t0 < k1; t0 += 256) {
-        // granules past the cache read its last page (their keys are masked)
-        int ik = (t0 + 16 * gk) / ps, iv = (t0 + 16 * g) / ps;
-        ik = ik < last_idx ? ik : last_idx;
-        iv = iv < last_idx ? iv : last_idx;
-        const int pk = kv_page(p.ix, b, ik), pv = kv_page(p.ix, b, iv);
-        const int64_t sk = static_cast<int64_t>(pk < 0 ? 0 : pk) * p.heads + h;
-        const int64_t sv = static_cast<int64_t>(pv < 0 ? 0 : pv) * p.heads + h;
-        const int8_t* kb = p.k + sk * ps * D + ((t0 + 16 * gk) % ps + (c & 3)) * D + 16 * g;
-        const int8_t* vb = p.v + sv * ps * D + static_cast<int64_t>(c) * ps + (t0 + 16 * g) % ps;
+        const bool live = nv >= 0 && nv < p.ix.pages && t0 + 16 * g < s.kv;
+        const int pk = nk >= 0 && nk < p.ix.pages ? nk : 0, pv = live ? nv : 0;
+        const int8_t* kb = kh + pk * pool_step;
+        const int8_t* vb = vh + pv * pool_step;
         u4 kw[4][NL], vw[ND];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int j = 0; j < NL; ++j) kw[t][j] = *reinterpret_cast<const u4*>(kb + 4 * t * D + 64 * j);
+        const int64_t sv = static_cast<int64_t>(pv) * p.heads + h;
+        float ksc = p.ks[sv], vsc = p.vs[sv];
 #pragma unroll
-        for (int t = 0; t < ND; ++t) vw[t] = *reinterpret_cast<const u4*>(vb + static_cast<int64_t>(16 * t) * ps);
-        const bool live = pv >= 0 && t0 + 16 * g < s.kv;
-        const float ksc = live ? p.ks[sv] : 0.f;
-        const float vsc = live ? p.vs[sv] : 0.f;
+        for (int t = 0; t < ND; ++t) vw[t] = *reinterpret_cast<const u4*>(vb + 16 * t * ps);
+        nk = page_ahead(t0 + 256, gk);
+        nv = page_ahead(t0 + 256, g);
+        if (!live) ksc = vsc = 0.f;
 
         float x[16];
 #pragma unroll
@@ -221,26 +233,33 @@ __global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
 #pragma unroll
         for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
         top = groups_max(top);
-        const float vtop = groups_max(vsc);
-        const float mn = fmaxf(m, top), vn = fmaxf(vr, vtop);
-        const float base = mn > kNegInf ? mn : 0.f;          // nothing seen yet: all weights 0
-        const float alpha = m > kNegInf ? __builtin_amdgcn_exp2f(m - base) : 1.f;
-        if (__any(alpha != 1.f || vn != vr)) {
-            const float r = alpha * (vr > 0.f ? vr / vn : 1.f);
+        const float vn = fmaxf(vr, groups_max(vsc));
+        // the reference follows the maximum once that is 2^8 past it (weights stay
+        // far inside fp16): most steps rescale nothing
+        if (__any(top > m + 8.f || vn != vr)) {
+            const float mn = fmaxf(m, top);
+            const float r = m > kNegInf ? __builtin_amdgcn_exp2f(m - mn) : 1.f;
+            const float ro = r * (vr > 0.f ? vr / vn : 1.f);
 #pragma unroll
-            for (int t = 0; t < ND; ++t) o[t] *= r;
-            l *= alpha;
+            for (int t = 0; t < ND; ++t) o[t] *= ro;
+            l *= r;
+            m = mn;
+            vr = vn;
         }
-        m = mn;
-        vr = vn;
-        const float wv = vn > 0.f ? vsc / vn : 0.f;
+        // weights times the page's v scale over the largest (at least 2^-30 of it:
+        // below, they leave fp16 anyway); the sum takes that out again
+        const float base = m > kNegInf ? m : 0.f;            // nothing seen yet: all weights 0
+        const float vlog = fmaxf(__builtin_amdgcn_logf(vsc) - __builtin_amdgcn_logf(vr), -30.f);
+        const float off = vlog - base;
         h8 pf[2];
+        float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const float w = __builtin_amdgcn_exp2f(x[i] - base);
-            l += w;
-            pf[i >> 3][i & 7] = static_cast<_Float16>(w * wv);
+            const float w = __builtin_amdgcn_exp2f(x[i] + off);
+            sum += w;
+            pf[i >> 3][i & 7] = static_cast<_Float16>(w);
         }
+        l = fmaf(sum, __builtin_amdgcn_exp2f(-vlog), l);
 #pragma unroll
         for (int t = 0; t < ND; ++t) {
             const u4 w = vw[t];
@@ -394,32 +413,48 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void kv_attn_tile_kernel
         for (int i = 0; i < 16; ++i) o[t][i] = 0.f;
     float m = kNegInf, l = 0.f, vr = 0.f;
 
-    // one step's codes on their way, and its granules' pages and scales
+    // A step's codes on their way.  Lane x of each four holds what belongs to the
+    // step's granule x: its page (read one step ahead of the codes), scales and
+    // whether it has keys; a piece of v lies in the granule of its own lane, a
+    // piece of k in one that the whole wave shares.
     u4 kw[NC], vw[NC];
-    int pg[4];
-    float ksc[4], vsc[4];
-    auto fetch = [&](int t0) {
+    const int x4 = lane & 3;
+    const int32_t* table = p.ix.page_table + static_cast<int64_t>(b) * p.ix.table_ld;
+    const int64_t page_bytes = static_cast<int64_t>(ps) * D, pool_step = page_bytes * p.heads;
+    const int8_t* kh = p.k + h * page_bytes;
+    const int8_t* vh = p.v + h * page_bytes;
+    int kat[NC], vat[NC], kg[NC], krow[NC];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            int idx = (t0 + 16 * x) >> psl;
-            idx = idx < last_idx ? idx : last_idx;
-            pg[x] = t0 + 16 * x < s.kv ? kv_page(p.ix, b, idx) : kNoPage;
-            const int64_t at = static_cast<int64_t>(pg[x] < 0 ? 0 : pg[x]) * p.heads + h;
-            ksc[x] = pg[x] < 0 ? 0.f : p.ks[at];
-            vsc[x] = pg[x] < 0 ? 0.f : p.vs[at];
-        }
+    for (int n = 0; n < NC; ++n) {
+        const int i = tid + n * TPB, key = i / (D / 16), kc = i % (D / 16), vd = i >> 2;
+        kat[n] = (key & (ps - 1)) * D + 16 * kc;
+        vat[n] = vd * ps + ((16 * x4) & (ps - 1));
+        kg[n] = __builtin_amdgcn_readfirstlane(key >> 4);
+        krow[n] = key_row(key);
+    }
+    auto page_ahead = [&](int t0) {
+        const int idx = (t0 + 16 * x4) >> psl;
+        return table[idx < last_idx ? idx : last_idx];
+    };
+    int ahead = 0, dead_next = 0;
+    float ks_next = 0.f, vs_next = 0.f;
+    auto fetch = [&](int t0) {
+        const bool live = ahead >= 0 && ahead < p.ix.pages && t0 + 16 * x4 < s.kv;
+        const int page = live ? ahead : 0;
+        dead_next = static_cast<int>(__ballot(!live)) & 15;
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
-            const int i = tid + n * TPB;
-            const int key = i / (D / 16), kc = i % (D / 16), vd = i >> 2, vg = i & 3;
-            const int gk = key >> 4;
-            const int pk = gk < 2 ? (gk == 0 ? pg[0] : pg[1]) : (gk == 2 ? pg[2] : pg[3]);
-            const int pv = vg < 2 ? (vg == 0 ? pg[0] : pg[1]) : (vg == 2 ? pg[2] : pg[3]);
-            const int64_t sk = static_cast<int64_t>(pk < 0 ? 0 : pk) * p.heads + h;
-            const int64_t sv = static_cast<int64_t>(pv < 0 ? 0 : pv) * p.heads + h;
-            kw[n] = *reinterpret_cast<const u4*>(p.k + sk * ps * D + ((t0 + key) & (ps - 1)) * D + 16 * kc);
-            vw[n] = *reinterpret_cast<const u4*>(p.v + sv * ps * D + vd * ps + ((t0 + 16 * vg) & (ps - 1)));
+            const int64_t pk = __builtin_amdgcn_readlane(page, kg[n]);
+            kw[n] = *reinterpret_cast<const u4*>(kh + pk * pool_step + kat[n]);
         }
+        const int8_t* vp = vh + page * pool_step;
+#pragma unroll
+        for (int n = 0; n < NC; ++n) vw[n] = *reinterpret_cast<const u4*>(vp + vat[n]);
+        const int64_t at = static_cast<int64_t>(page) * p.heads + h;
+        ks_next = p.ks[at];
+        vs_next = p.vs[at];
+        if (!live) ks_next = vs_next = 0.f;
+        ahead = page_ahead(t0 + 64);
     };
     // the fetched step into buffer `buf`, and its granules' scales and flags
     float mul[4], unit = 0.f, vlog[4], vinv[4];
@@ -430,27 +465,32 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void kv_attn_tile_kernel
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
             const int i = tid + n * TPB;
-            const int key = i / (D / 16), kc = i % (D / 16), vd = i >> 2, vg = i & 3;
-            const int kr = key_row(key);
-            *reinterpret_cast<h8*>(kl + k_off<D>(kr, 2 * kc)) = codes_f16(kw[n][0], kw[n][1]);
-            *reinterpret_cast<h8*>(kl + k_off<D>(kr, 2 * kc + 1)) = codes_f16(kw[n][2], kw[n][3]);
-            *reinterpret_cast<h8*>(vl + v_off(vd, 2 * vg)) = codes_f16(vw[n][0], vw[n][1]);
-            *reinterpret_cast<h8*>(vl + v_off(vd, 2 * vg + 1)) = codes_f16(vw[n][2], vw[n][3]);
+            const int kc = i % (D / 16), vd = i >> 2;
+            *reinterpret_cast<h8*>(kl + k_off<D>(krow[n], 2 * kc)) = codes_f16(kw[n][0], kw[n][1]);
+            *reinterpret_cast<h8*>(kl + k_off<D>(krow[n], 2 * kc + 1)) = codes_f16(kw[n][2], kw[n][3]);
+            *reinterpret_cast<h8*>(vl + v_off(vd, 2 * x4)) = codes_f16(vw[n][0], vw[n][1]);
+            *reinterpret_cast<h8*>(vl + v_off(vd, 2 * x4 + 1)) = codes_f16(vw[n][2], vw[n][3]);
         }
-        unit = fmaxf(unit, fmaxf(fmaxf(vsc[0], vsc[1]), fmaxf(vsc[2], vsc[3])));
-        dead = 0;
+        float top = fmaxf(vs_next, dpp_mov<0xB1>(vs_next));
+        top = fmaxf(top, dpp_mov<0x4E>(top));
+        unit = fmaxf(unit, top);
+        // a page 2^-30 below the largest keeps that ratio: its weights leave fp16
+        // there anyway (and a NaN, all scales 0, becomes it too)
+        const float lg = fmaxf(__builtin_amdgcn_logf(vs_next) - __builtin_amdgcn_logf(unit), -30.f);
+        const float li = __builtin_amdgcn_exp2f(-lg);
+        dead = dead_next;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            mul[x] = ksc[x];
-            // a page 2^-30 below the largest keeps that ratio: its weights leave fp16 there anyway
-            vlog[x] = unit > 0.f ? fmaxf(__builtin_amdgcn_logf(vsc[x] / unit), -30.f) : 0.f;
-            vinv[x] = __builtin_amdgcn_exp2f(-vlog[x]);
-            dead |= (pg[x] < 0) << x;
+            mul[x] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ks_next), x));
+            vlog[x] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lg), x));
+            vinv[x] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(li), x));
         }
+        unit = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(unit)));
     };
 
     int buf = 0;
     if (k0 < k1) {
+        ahead = page_ahead(k0);
         fetch(k0);
         stage(0);
     }
