@@ -118,7 +118,9 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream(dev: torch.device) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
+    # the raw handle of torch.cuda.current_stream(dev), without building the
+    # Stream object (2 us of a call that takes 6)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev.index is None else dev.index)
 
 
 def _check(status: int, where: str) -> None:
@@ -139,8 +141,8 @@ def _need(t, nbytes: int, name: str) -> None:
     _dev_tensor(t, name)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.numel() * t.element_size() < nbytes:
-        raise ValueError(f"{name} holds {t.numel() * t.element_size()} bytes, the call needs {nbytes}")
+    if t.nbytes < nbytes:
+        raise ValueError(f"{name} holds {t.nbytes} bytes, the call needs {nbytes}")
 
 
 def code_row_bytes(k: int, bits: int) -> int:
@@ -245,32 +247,34 @@ def _on_device(fn, dev: torch.device, *args) -> int:
 
 
 def _same_device(dev: torch.device, **tensors) -> None:
-    for name, t in tensors.items():
+    for t in tensors.values():
         if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the call on {dev}")
+            raise ValueError(f"{[n for n, x in tensors.items() if x is t][0]} is on {t.device}, the call on {dev}")
 
 
 def _norm_args(x, weight, residual, residual_out):
-    """Checks shared by the residual + RMS norm calls; returns m, k, ldx, ldr
-    (a single row has no pitch of its own)."""
-    if x.dim() != 2 or x.stride(1) != 1:
+    """Checks shared by the residual + RMS norm calls; returns the device, m, k,
+    ldx, ldr (a single row has no pitch of its own)."""
+    dev, shape = x.device, x.shape
+    if len(shape) != 2 or x.stride(1) != 1:
         raise ValueError("x must be a row-major [m][k] tensor")
     _dev_tensor(x, "x")
-    m, k = x.shape
-    _same_device(x.device, weight=weight, residual=residual, residual_out=residual_out)
+    m, k = shape
     if weight.dtype != torch.float32 or weight.numel() != k or not weight.is_contiguous():
         raise ValueError("weight must be a contiguous float32 [k] tensor")
+    if weight.device != dev:
+        raise ValueError(f"weight is on {weight.device}, the call on {dev}")
     ldx, ldr = (x.stride(0), 0) if m > 1 else (k, k)
-    for name, t in (("residual", residual), ("residual_out", residual_out)):
+    for t in (residual, residual_out):
         if t is None:
             continue
-        if t.shape != x.shape or t.dtype != x.dtype or t.stride(1) != 1:
-            raise ValueError(f"{name} must be a row-major tensor of x's shape and type")
+        if t.shape != shape or t.dtype != x.dtype or t.stride(1) != 1 or t.device != dev:
+            raise ValueError("residual and residual_out must be row-major tensors of x's shape and type on its device")
         if m > 1:
             if ldr and t.stride(0) != ldr:
                 raise ValueError("residual and residual_out need the same row pitch")
             ldr = t.stride(0)
-    return m, k, ldx, ldr
+    return dev, m, k, ldx, ldr
 
 
 def qlin_add_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
@@ -283,19 +287,20 @@ def qlin_add_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor, residual: Opti
     norm's gamma times the next projection's inv_s.  r goes to residual_out
     (which may be residual or x: in place); the third value returned is that
     tensor, or None."""
-    m, k, ldx, ldr = _norm_args(x, weight, residual, residual_out)
+    dev, m, k, ldx, ldr = _norm_args(x, weight, residual, residual_out)
     if out is None:
-        xq = _codes(m, k, bits, x.device)
-        xs = torch.empty(m, dtype=torch.float32, device=x.device)
+        xq = _codes(m, k, bits, dev)
+        xs = torch.empty(m, dtype=torch.float32, device=dev)
     else:
         xq, xs = out
-        _same_device(x.device, xq=xq, x_scale=xs)
-    _need(xq, m * code_row_bytes(k, bits), "xq")
-    _need(xs, m * 4, "x_scale")
-    st = _on_device(load().qlin_add_rmsnorm_quant, x.device, x.data_ptr(), _TORCH_TO_QLIN[x.dtype], m, k, ldx,
+        _same_device(dev, xq=xq, x_scale=xs)
+        _need(xq, m * code_row_bytes(k, bits), "xq")
+        _need(xs, m * 4, "x_scale")
+    st = _on_device(load().qlin_add_rmsnorm_quant, dev, x.data_ptr(), _TORCH_TO_QLIN[x.dtype], m, k, ldx,
                     _ptr(residual), ldr, weight.data_ptr(), eps, had_block, bits, _ptr(residual_out), xq.data_ptr(),
-                    xs.data_ptr(), _stream(x.device))
-    _check(st, "qlin_add_rmsnorm_quant")
+                    xs.data_ptr(), _stream(dev))
+    if st:
+        raise QlinError(st, "qlin_add_rmsnorm_quant")
     return xq, xs, residual_out
 
 
@@ -304,14 +309,14 @@ def qlin_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[t
                      out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """The RMS norm of r = x + residual in x's type, contiguous [m][k] (the
     input of qlin_gemv_w4a16), and residual_out (or None)."""
-    m, k, ldx, ldr = _norm_args(x, weight, residual, residual_out)
-    y = out if out is not None else torch.empty((m, k), dtype=x.dtype, device=x.device)
+    dev, m, k, ldx, ldr = _norm_args(x, weight, residual, residual_out)
+    y = out if out is not None else torch.empty((m, k), dtype=x.dtype, device=dev)
     if y.dtype != x.dtype:
         raise ValueError("out must have x's type")
-    _same_device(x.device, out=y)
+    _same_device(dev, out=y)
     _need(y, m * k * y.element_size(), "out")
-    st = _on_device(load().qlin_add_rmsnorm, x.device, x.data_ptr(), _TORCH_TO_QLIN[x.dtype], m, k, ldx,
-                    _ptr(residual), ldr, weight.data_ptr(), eps, _ptr(residual_out), y.data_ptr(), _stream(x.device))
+    st = _on_device(load().qlin_add_rmsnorm, dev, x.data_ptr(), _TORCH_TO_QLIN[x.dtype], m, k, ldx,
+                    _ptr(residual), ldr, weight.data_ptr(), eps, _ptr(residual_out), y.data_ptr(), _stream(dev))
     _check(st, "qlin_add_rmsnorm")
     return y, residual_out
 
@@ -700,9 +705,10 @@ class KvBatch:
 
 def _rows16(t: torch.Tensor, name: str, cols: int) -> int:
     """Row pitch of a row-major [rows][cols] fp16 / bf16 tensor."""
-    if t.dim() != 2 or t.shape[1] != cols or t.stride(1) != 1:
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols or t.stride(1) != 1:
         raise ValueError(f"{name} must be a row-major [tokens][{cols}] tensor")
-    return t.stride(0) if t.shape[0] > 1 else -(-cols // 8) * 8
+    return t.stride(0) if shape[0] > 1 else -(-cols // 8) * 8
 
 
 def qlin_rope_table(positions: int, rot_dim: int, base: float = 10000.0, stretch: float = 1.0, device="cuda"

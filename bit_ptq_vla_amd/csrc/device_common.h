@@ -60,6 +60,22 @@ __device__ __forceinline__ float f16_bits_to_f32(uint16_t b) {
 template <int DT>
 __device__ __forceinline__ void load8(const void* p, float f[8]);
 
+// Eight 16-bit values (F16 or BF16) of a 16-byte word, widened to fp32.
+template <int DT>
+__device__ __forceinline__ void unpack8(uint4 v, float f[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (DT == BF16) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        } else {
+            f[2 * i] = f16_bits_to_f32(static_cast<uint16_t>(w[i] & 0xFFFFu));
+            f[2 * i + 1] = f16_bits_to_f32(static_cast<uint16_t>(w[i] >> 16));
+        }
+    }
+}
+
 template <>
 __device__ __forceinline__ void load8<F16>(const void* p, float f[8]) {
     uint4 v = *reinterpret_cast<const uint4*>(p);

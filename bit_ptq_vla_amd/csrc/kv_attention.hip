@@ -109,13 +109,19 @@ __device__ __forceinline__ Row row_of(const AttnParams& p, const KvSeq& s, int b
 }
 
 // Up to 16 query rows of one (sequence, kv head) against a range of its keys:
-// four waves take the range's 64-key steps in turn and join through LDS.
+// four waves take the range's 64-key steps in turn, codes straight from memory
+// (the next step's are on their way as soon as this one's are used), and join
+// through LDS, [wave][row][D + 4] sums and then the statistics.
 template <int DT, int D, bool CAP>
 __global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
+    constexpr int NWV = 4;
     constexpr int NL = D / 64;     // 16-byte K loads per key row and lane
     constexpr int ND = D / 16;     // 16-dimension tiles of the output
-    __shared__ float lo[4][16][D + 4];
-    __shared__ float lm[4][16], ll[4][16];
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    const int rmax = p.ix.max_q * p.group < 16 ? p.ix.max_q * p.group : 16;
+    float* lo = reinterpret_cast<float*>(lds);
+    float* lm = lo + NWV * rmax * (D + 4);
+    float* ll = lm + NWV * rmax;
     int64_t u = blockIdx.x;
     const int sp = static_cast<int>(u % p.splits);
     u /= p.splits;
@@ -137,6 +143,51 @@ __global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
     const Row row = row_of(p, s, b, h, r0 + c < rows ? r0 + c : last);
     const int vis = r0 + c < rows ? row.vis : 0;
     const int ps = p.ix.page_size;
+
+    const int psl = 31 - __builtin_clz(ps);
+    const int last_idx = s.kv > 0 ? (s.kv - 1) >> psl : 0;
+    const int gk = c >> 2;                   // granule of the lane's K rows
+    const int32_t* table = p.ix.page_table + static_cast<int64_t>(b) * p.ix.table_ld;
+    const int64_t page_bytes = static_cast<int64_t>(ps) * D, pool_step = page_bytes * p.heads;
+    // t0 is a multiple of 64: a granule's place in its page does not depend on it
+    const int8_t* kh = p.k + h * page_bytes + (((16 * gk) & (ps - 1)) + (c & 3)) * D + 16 * g;
+    const int8_t* vh = p.v + h * page_bytes + c * ps + ((16 * g) & (ps - 1));
+    auto page_ahead = [&](int t0, int gran) {
+        const int idx = (t0 + 16 * gran) >> psl;
+        return table[idx < last_idx ? idx : last_idx];
+    };
+    // granules past the cache read its last page (their keys are masked)
+    const uint32_t pool = static_cast<uint32_t>(p.ix.pages);
+    u4 kw[4][NL], vw[ND];
+    float ksc = 0.f, vsc = 0.f;
+    int nk = 0, nv = 0;                      // table entries of the next step
+    bool live = false, live_next = false;
+    auto load_k = [&]() {
+        const int8_t* kb = kh + (static_cast<uint32_t>(nk) < pool ? nk : 0) * pool_step;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int j = 0; j < NL; ++j) kw[t][j] = *reinterpret_cast<const u4*>(kb + 4 * t * D + 64 * j);
+    };
+    auto load_v = [&](int t0) {
+        live_next = (static_cast<uint32_t>(nv) < pool) & (t0 + 16 * g < s.kv);
+        const int pv = live_next ? nv : 0;
+        const int8_t* vb = vh + pv * pool_step;
+        const int64_t sv = static_cast<int64_t>(pv) * p.heads + h;
+        ksc = p.ks[sv];
+        vsc = p.vs[sv];
+#pragma unroll
+        for (int t = 0; t < ND; ++t) vw[t] = *reinterpret_cast<const u4*>(vb + 16 * t * ps);
+    };
+    const int first = k0 + 64 * wave;
+    if (first < k1) {
+        nk = page_ahead(first, gk);
+        nv = page_ahead(first, g);
+        load_k();
+        load_v(first);
+        nk = page_ahead(first + 64 * NWV, gk);
+        nv = page_ahead(first + 64 * NWV, g);
+    }
 
     // the lane's part of its query: dimensions 64 j + 16 g .. + 15
     h8 qf[2 * NL];
@@ -174,42 +225,10 @@ __global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
 #pragma unroll
     for (int t = 0; t < ND; ++t) o[t] = f4{0.f, 0.f, 0.f, 0.f};
     float m = kNegInf, l = 0.f, vr = 0.f;
-    const int psl = 31 - __builtin_clz(ps);
-    const int last_idx = s.kv > 0 ? (s.kv - 1) >> psl : 0;
-    const int gk = c >> 2;                   // granule of the lane's K rows
-    const int32_t* table = p.ix.page_table + static_cast<int64_t>(b) * p.ix.table_ld;
-    const int64_t page_bytes = static_cast<int64_t>(ps) * D, pool_step = page_bytes * p.heads;
-    // t0 is a multiple of 64: a granule's place in its page does not depend on it
-    const int8_t* kh = p.k + h * page_bytes + (((16 * gk) & (ps - 1)) + (c & 3)) * D + 16 * g;
-    const int8_t* vh = p.v + h * page_bytes + c * ps + ((16 * g) & (ps - 1));
-    auto page_ahead = [&](int t0, int gran) {
-        const int idx = (t0 + 16 * gran) >> psl;
-        return table[idx < last_idx ? idx : last_idx];
-    };
-    // granules past the cache read its last page (their keys are masked)
-    int nk = 0, nv = 0;
-    if (k0 + 64 * wave < k1) {
-        nk = page_ahead(k0 + 64 * wave, gk);
-        nv = page_ahead(k0 + 64 * wave, g);
-    }
-
-    for (int t0 = k0 + 64 * wave; t0 < k1; t0 += 256) {
-        const bool live = nv >= 0 && nv < p.ix.pages && t0 + 16 * g < s.kv;
-        const int pk = nk >= 0 && nk < p.ix.pages ? nk : 0, pv = live ? nv : 0;
-        const int8_t* kb = kh + pk * pool_step;
-        const int8_t* vb = vh + pv * pool_step;
-        u4 kw[4][NL], vw[ND];
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int j = 0; j < NL; ++j) kw[t][j] = *reinterpret_cast<const u4*>(kb + 4 * t * D + 64 * j);
-        const int64_t sv = static_cast<int64_t>(pv) * p.heads + h;
-        float ksc = p.ks[sv], vsc = p.vs[sv];
-#pragma unroll
-        for (int t = 0; t < ND; ++t) vw[t] = *reinterpret_cast<const u4*>(vb + 16 * t * ps);
-        nk = page_ahead(t0 + 256, gk);
-        nv = page_ahead(t0 + 256, g);
-        if (!live) ksc = vsc = 0.f;
+    for (int t0 = first; t0 < k1; t0 += 64 * NWV) {
+        live = live_next;
+        const float ks_t = live ? ksc : 0.f, vs_t = live ? vsc : 0.f;
+        const bool more = t0 + 64 * NWV < k1;
 
         float x[16];
 #pragma unroll
@@ -224,7 +243,8 @@ __global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[4 * t + i] = acc[i];
         }
-        const float mul = qmul * ksc;
+        if (more) load_k();
+        const float mul = qmul * ks_t;
         const int lim = live ? vis - (t0 + 16 * g) : 0;      // keys of the granule that the query sees
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = i < lim ? score<CAP>(x[i], mul, 0.f, cap_out) : kNegInf;
@@ -233,7 +253,7 @@ __global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
 #pragma unroll
         for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
         top = groups_max(top);
-        const float vn = fmaxf(vr, groups_max(vsc));
+        const float vn = fmaxf(vr, groups_max(vs_t));
         // the reference follows the maximum once that is 2^8 past it (weights stay
         // far inside fp16): most steps rescale nothing
         if (__any(top > m + 8.f || vn != vr)) {
@@ -249,7 +269,7 @@ __global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
         // weights times the page's v scale over the largest (at least 2^-30 of it:
         // below, they leave fp16 anyway); the sum takes that out again
         const float base = m > kNegInf ? m : 0.f;            // nothing seen yet: all weights 0
-        const float vlog = fmaxf(__builtin_amdgcn_logf(vsc) - __builtin_amdgcn_logf(vr), -30.f);
+        const float vlog = fmaxf(__builtin_amdgcn_logf(vs_t) - __builtin_amdgcn_logf(vr), -30.f);
         const float off = vlog - base;
         h8 pf[2];
         float sum = 0.f;
@@ -266,34 +286,43 @@ __global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
             o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16(w[0], w[1]), pf[0], o[t], 0, 0, 0);
             o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16(w[2], w[3]), pf[1], o[t], 0, 0, 0);
         }
+        if (more) {
+            load_v(t0 + 64 * NWV);
+            nk = page_ahead(t0 + 128 * NWV, gk);
+            nv = page_ahead(t0 + 128 * NWV, g);
+        }
     }
 
     // join the waves: element i of tile t is dimension 16 t + 4 g + i of query c
     l = groups_sum(l);
+    if (c < rmax) {
 #pragma unroll
-    for (int t = 0; t < ND; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) lo[wave][c][16 * t + 4 * g + i] = o[t][i] * vr;
-    if (g == 0) {
-        lm[wave][c] = m;
-        ll[wave][c] = l;
+        for (int t = 0; t < ND; ++t)
+            *reinterpret_cast<float4*>(lo + (wave * rmax + c) * (D + 4) + 16 * t + 4 * g) =
+                make_float4(o[t][0] * vr, o[t][1] * vr, o[t][2] * vr, o[t][3] * vr);
+        if (g == 0) {
+            lm[wave * rmax + c] = m;
+            ll[wave * rmax + c] = l;
+        }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < 16 * (D / 8); e += 256) {
+    for (int e = threadIdx.x; e < rmax * (D / 8); e += 64 * NWV) {
         const int r = e / (D / 8), d = e % (D / 8) * 8;
         if (r0 + r >= rows) continue;
         const Row x = row_of(p, s, b, h, r0 + r);
-        float mt = lm[0][r];
+        float mt = lm[r];
 #pragma unroll
-        for (int w = 1; w < 4; ++w) mt = fmaxf(mt, lm[w][r]);
+        for (int w = 1; w < NWV; ++w) mt = fmaxf(mt, lm[w * rmax + r]);
         const float base = mt > kNegInf ? mt : 0.f;
         float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const float a = __builtin_amdgcn_exp2f(lm[w][r] - base);
-            sum += a * ll[w][r];
+        for (int w = 0; w < NWV; ++w) {
+            const float a = __builtin_amdgcn_exp2f(lm[w * rmax + r] - base);
+            sum += a * ll[w * rmax + r];
+            float v[8];
+            load8<F32>(lo + (w * rmax + r) * (D + 4) + d, v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] += a * lo[w][r][d + i];
+            for (int i = 0; i < 8; ++i) f[i] += a * v[i];
         }
         if (p.splits == 1) {
             const float inv = sum > 0.f ? 1.f / sum : 0.f;
@@ -313,16 +342,17 @@ __global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
 
 // ---- many query rows ---------------------------------------------------------
 
-// Byte offset of 16-byte chunk `c` of K row `row` in LDS: D fp16 a row, chunks
-// xor-swizzled so that eight lanes reading one chunk of eight rows meet eight
-// different bank groups.
+// Byte offset of 16-byte chunk `c` of K row `row` in LDS: D fp16 a row.  LDS has
+// 64 banks and serves a 16-byte access sixteen lanes at a time: the xor makes the
+// sixteen lanes that read one chunk of sixteen rows, or write every other chunk
+// of one or more rows, cover all 256 bytes.
 template <int D>
 __device__ __forceinline__ int k_off(int row, int c) {
-    constexpr int M = D / 8 < 16 ? D / 8 - 1 : 15;
-    return row * D * 2 + ((c ^ (row & M)) << 4);
+    const int x = D == 64 ? (row >> 1) & 7 : (row & 15) ^ (c >> 4);
+    return row * D * 2 + ((c ^ x) << 4);
 }
 // The same for V: 64 keys (8 chunks) a dimension.
-__device__ __forceinline__ int v_off(int d, int c) { return d * 128 + ((c ^ (d & 7)) << 4); }
+__device__ __forceinline__ int v_off(int d, int c) { return d * 128 + ((c ^ ((d >> 1) & 7)) << 4); }
 
 // The LDS row of key j (0..63) of a step.  The 32x32 product leaves lane half h
 // with rows 8 (i / 4) + 4 h + i % 4 in element i; with this order elements
@@ -332,17 +362,26 @@ __device__ __forceinline__ int key_row(int j) {
     return (j & 48) | ((j & 4) << 1) | ((j & 8) >> 1) | (j & 3);
 }
 
-// 32 * NW query rows of one (sequence, kv head), 32 to a wave, against a range
-// of its keys.  The block turns each step's 64 keys into fp16 in LDS once (v
-// times its page's scale over the largest met) and every wave multiplies
-// v_mfma_f32_32x32x16_f16 tiles from there; the next step's codes are in
-// flight meanwhile, and two LDS buffers leave one barrier a step.
-template <int DT, int D, bool CAP, int NW>
-__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void kv_attn_tile_kernel(AttnParams p) {
-    constexpr int TPB = 64 * NW;
+// 32 query rows to a wave, eight waves to a block; HV waves share 32 rows of a
+// 256-wide head and keep D / HV dimensions of their output each.  The waves run
+// in two groups, four (one to a SIMD) each, half a step apart: while one group
+// feeds the matrix units (the last step's P V, then this step's K Q) the other
+// does its softmax, so the two kinds of work overlap on every SIMD:
+//   phase      2t            2t + 1      2t + 2
+//   group 0    PV(t-1) QK(t) softmax(t)  PV(t) QK(t+1)
+//   group 1    softmax(t-1)  PV(t-1) QK(t)  softmax(t)
+// Each group stages its half of K(t + 1) and V(t) between the products of PV(t-1)
+// and QK(t): after the last use of K(t - 1) and V(t - 2), before the next of both.
+template <int DT, int D, bool CAP>
+__global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
+    constexpr int TPB = 512;
+    constexpr int HV = D == 256 ? 2 : 1;
+    constexpr int ROWS = 32 * 8 / HV;
     constexpr int NS = D / 16;            // k steps of S
-    constexpr int ND = D / 32;            // 32-dimension tiles of the output
-    constexpr int NC = D * 4 / TPB;       // 16-byte pieces of k (and of v) a thread stages per step
+    constexpr int ND = D / 32 / HV;       // 32-dimension tiles of the wave's output
+    constexpr int NC = D * 4 / TPB > 0 ? D * 4 / TPB : 1;   // 16-byte pieces of k (and of v) a thread stages
+    constexpr int AHEAD = D == 256 ? 3 : 6;
+    constexpr bool PART = D * 4 < TPB;    // only the first D * 4 threads stage
     constexpr int KB = 64 * D * 2;        // bytes of one operand of a step in LDS
     extern __shared__ __attribute__((aligned(16))) char lds[];
     typedef float f16v __attribute__((ext_vector_type(16)));
@@ -355,26 +394,87 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void kv_attn_tile_kernel
     const int b = static_cast<int>(u % p.ix.batch);
     const int rt = p.row_tiles - 1 - static_cast<int>(u / p.ix.batch);   // the longest first
     const KvSeq s = kv_seq(p.ix, b);
-    const int rows = s.n * p.group, r0 = rt * 32 * NW;
+    const int rows = s.n * p.group, r0 = rt * ROWS;
     if (r0 >= rows) return;
-    const int last = (r0 + 32 * NW < rows ? r0 + 32 * NW : rows) - 1;
+    const int last = (r0 + ROWS < rows ? r0 + ROWS : rows) - 1;
     const int vis_hi = row_of(p, s, b, h, last).vis;
     const int k0 = sp * p.split_keys;
     if (sp > 0 && k0 >= vis_hi) return;
     const int k1 = k0 + p.split_keys < vis_hi ? k0 + p.split_keys : vis_hi;
+    const int steps = k1 > k0 ? (k1 - k0 + 63) >> 6 : 0;
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int grp = wave >> 2, half = HV == 2 ? wave & 1 : 0;
     const int c = lane & 31, hf = lane >> 5;
-    const int rw = r0 + 32 * wave;                       // the wave's first row
+    const int rw = r0 + 32 * (wave / HV);                // the wave's first row
     const Row row = row_of(p, s, b, h, rw + c < rows ? rw + c : last);
     const int vis = rw + c < rows ? row.vis : 0;
-    // the wave's rows see at least / at most these keys
+    // the wave's rows see at least these keys
     const int wave_lo = rw + 31 < rows ? row_of(p, s, b, h, rw).vis : 0;
-    const int wave_hi = rw < rows ? row_of(p, s, b, h, rw + 31 < rows ? rw + 31 : last).vis : 0;
     const int ps = p.ix.page_size, psl = 31 - __builtin_clz(ps);
     const int last_idx = s.kv > 0 ? (s.kv - 1) >> psl : 0;
 
-    // queries: dimensions 16 s + 8 hf .. + 7 of row c
+    // Lane x of each four holds what belongs to granule x of a step: its page,
+    // scales and whether it has keys; a piece of v lies in the granule of its own
+    // lane, a piece of k in one that the whole wave shares.
+    const int x4 = lane & 3;
+    const int32_t* table = p.ix.page_table + static_cast<int64_t>(b) * p.ix.table_ld;
+    const int64_t page_bytes = static_cast<int64_t>(ps) * D, pool_step = page_bytes * p.heads;
+    const int8_t* kh = p.k + h * page_bytes;
+    const int8_t* vh = p.v + h * page_bytes;
+    const float* ksh = p.ks + h;
+    const float* vsh = p.vs + h;
+    // entry of the page table for the lane's granule of step t, and the page it
+    // stands for (asked for only when it is used: nothing waits for the load)
+    auto entry_of = [&](int t) {
+        const int idx = (k0 + 64 * t + 16 * x4) >> psl;
+        return table[idx < last_idx ? idx : last_idx];
+    };
+    const uint32_t pool = static_cast<uint32_t>(p.ix.pages);
+    auto page_of = [&](int entry, int t) {
+        const bool in = static_cast<uint32_t>(entry) < pool, short_of = k0 + 64 * t + 16 * x4 < s.kv;
+        return (in & short_of) ? entry : kNoPage;
+    };
+    int en0 = 0, en1 = 0, en2 = 0;           // entries of steps t, t + 1, t + 2
+    if (steps > 0) {
+        en0 = entry_of(0);
+        en1 = entry_of(1);
+        en2 = entry_of(2);
+    }
+    u4 kw[NC], vw[NC];
+    const bool stages = !PART || tid < D * 4;
+    auto fetch_k = [&](int page) {
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+            const int i = tid + n * TPB, key = i / (D / 16), kc = i % (D / 16);
+            const int pk = __builtin_amdgcn_readlane(page, __builtin_amdgcn_readfirstlane(key >> 4) & 3);
+            if (stages)
+                kw[n] = *reinterpret_cast<const u4*>(kh + (pk < 0 ? 0 : pk) * pool_step + (key & (ps - 1)) * D + 16 * kc);
+        }
+    };
+    auto fetch_v = [&](int page) {
+        const int8_t* vp = vh + (page < 0 ? 0 : page) * pool_step + ((16 * x4) & (ps - 1));
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+            if (stages) vw[n] = *reinterpret_cast<const u4*>(vp + ((tid + n * TPB) >> 2) * ps);
+    };
+    // part i of staging: half (8 codes) of piece i / 2 of k, then of v
+    auto stage_part = [&](int i, int tk, int tv) {
+        const int n = (i >> 1) % NC, e = (i & 1) * 2, at = tid + n * TPB;
+        if (i < 2 * NC) {
+            const h8 w = codes_f16(kw[n][e], kw[n][e + 1]);
+            char* dst = lds + (tk & 1) * KB + k_off<D>(key_row(at / (D / 16)), 2 * (at % (D / 16)) + (i & 1));
+            if (stages) *reinterpret_cast<h8*>(dst) = w;
+        } else {
+            const h8 w = codes_f16(vw[n][e], vw[n][e + 1]);
+            char* dst = lds + 2 * KB + (tv & 1) * KB + v_off(at >> 2, 2 * x4 + (i & 1));
+            if (stages) *reinterpret_cast<h8*>(dst) = w;
+        }
+    };
+    if (steps > 0) fetch_k(page_of(en0, 0));
+
+    // queries: dimensions 16 j + 8 hf .. + 7 of row c
     h8 qf[NS];
     float qmul = p.sm_scale;
     {
@@ -412,219 +512,231 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void kv_attn_tile_kernel
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[t][i] = 0.f;
     float m = kNegInf, l = 0.f, vr = 0.f;
+    float x[32];
+    h8 pf[4];
+    float ks_t = 0.f, vs_t = 0.f;            // scales of the lane's granule of step t
+    float sc[4], vlog[4], vinv[4], unit = 0.f;
+    int dead_t = 0;
 
-    // A step's codes on their way.  Lane x of each four holds what belongs to the
-    // step's granule x: its page (read one step ahead of the codes), scales and
-    // whether it has keys; a piece of v lies in the granule of its own lane, a
-    // piece of k in one that the whole wave shares.
-    u4 kw[NC], vw[NC];
-    const int x4 = lane & 3;
-    const int32_t* table = p.ix.page_table + static_cast<int64_t>(b) * p.ix.table_ld;
-    const int64_t page_bytes = static_cast<int64_t>(ps) * D, pool_step = page_bytes * p.heads;
-    const int8_t* kh = p.k + h * page_bytes;
-    const int8_t* vh = p.v + h * page_bytes;
-    int kat[NC], vat[NC], kg[NC], krow[NC];
+    // The products of PV(t - 1), then of QK(t): A operands are read AHEAD products
+    // before their use.  A matrix instruction that waits for its unit keeps the
+    // other group's vector instructions from issuing, so each is followed by about
+    // as much other issue as it runs: its read, and staging or a pause (measured
+    // with one wave of each kind on a SIMD: 32.6 cycles a product and nothing
+    // beside it without the pause; 34.5, and the other wave at 4/5 of its rate, with).
+    constexpr int NP = 4 * ND + 2 * NS;
+    auto products = [&](int t, bool first, bool second) {
+        const char* vl = lds + 2 * KB + ((t - 1) & 1) * KB;
+        const char* kl = lds + (t & 1) * KB;
+        auto operand = [&](int i) {
+            if (i < 4 * ND)
+                return *reinterpret_cast<const h8*>(vl + v_off(32 * (half * ND + i / 4) + c, 2 * (i % 4) + hf));
+            const int j = i - 4 * ND;
+            return *reinterpret_cast<const h8*>(kl + k_off<D>(32 * (j & 1) + c, 2 * (j >> 1) + hf));
+        };
+        f16v a0, a1;
 #pragma unroll
-    for (int n = 0; n < NC; ++n) {
-        const int i = tid + n * TPB, key = i / (D / 16), kc = i % (D / 16), vd = i >> 2;
-        kat[n] = (key & (ps - 1)) * D + 16 * kc;
-        vat[n] = vd * ps + ((16 * x4) & (ps - 1));
-        kg[n] = __builtin_amdgcn_readfirstlane(key >> 4);
-        krow[n] = key_row(key);
-    }
-    auto page_ahead = [&](int t0) {
-        const int idx = (t0 + 16 * x4) >> psl;
-        return table[idx < last_idx ? idx : last_idx];
-    };
-    int ahead = 0, dead_next = 0;
-    float ks_next = 0.f, vs_next = 0.f;
-    auto fetch = [&](int t0) {
-        const bool live = ahead >= 0 && ahead < p.ix.pages && t0 + 16 * x4 < s.kv;
-        const int page = live ? ahead : 0;
-        dead_next = static_cast<int>(__ballot(!live)) & 15;
+        for (int i = 0; i < 16; ++i) a0[i] = a1[i] = 0.f;
+        const int from = first ? 0 : 4 * ND, to = second ? NP : 4 * ND;
+        h8 fr[AHEAD];
 #pragma unroll
-        for (int n = 0; n < NC; ++n) {
-            const int64_t pk = __builtin_amdgcn_readlane(page, kg[n]);
-            kw[n] = *reinterpret_cast<const u4*>(kh + pk * pool_step + kat[n]);
+        for (int i = 0; i < AHEAD; ++i) fr[i] = operand(from + i);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = from; i < to; ++i) {
+            const h8 w = fr[(i - from) % AHEAD];
+            if (i < 4 * ND) o[i / 4] = __builtin_amdgcn_mfma_f32_32x32x16_f16(w, pf[i % 4], o[i / 4], 0, 0, 0);
+            else if ((i - 4 * ND) & 1) a1 = __builtin_amdgcn_mfma_f32_32x32x16_f16(w, qf[(i - 4 * ND) >> 1], a1, 0, 0, 0);
+            else a0 = __builtin_amdgcn_mfma_f32_32x32x16_f16(w, qf[(i - 4 * ND) >> 1], a0, 0, 0, 0);
+            if (i + AHEAD < to) fr[(i - from) % AHEAD] = operand(i + AHEAD);
+            const int part = second && i >= 4 && (i & 1) == 0 ? (i - 4) / 2 : 4 * NC;
+            if (part < 4 * NC) stage_part(part, t + 1, t);
+            else asm volatile("s_nop 4");
+            __builtin_amdgcn_sched_barrier(0);
         }
-        const int8_t* vp = vh + page * pool_step;
+        if (second) {
 #pragma unroll
-        for (int n = 0; n < NC; ++n) vw[n] = *reinterpret_cast<const u4*>(vp + vat[n]);
-        const int64_t at = static_cast<int64_t>(page) * p.heads + h;
-        ks_next = p.ks[at];
-        vs_next = p.vs[at];
-        if (!live) ks_next = vs_next = 0.f;
-        ahead = page_ahead(t0 + 64);
-    };
-    // the fetched step into buffer `buf`, and its granules' scales and flags
-    float mul[4], unit = 0.f, vlog[4], vinv[4];
-    int dead = 0;
-    auto stage = [&](int buf) {
-        char* kl = lds + buf * 2 * KB;
-        char* vl = kl + KB;
-#pragma unroll
-        for (int n = 0; n < NC; ++n) {
-            const int i = tid + n * TPB;
-            const int kc = i % (D / 16), vd = i >> 2;
-            *reinterpret_cast<h8*>(kl + k_off<D>(krow[n], 2 * kc)) = codes_f16(kw[n][0], kw[n][1]);
-            *reinterpret_cast<h8*>(kl + k_off<D>(krow[n], 2 * kc + 1)) = codes_f16(kw[n][2], kw[n][3]);
-            *reinterpret_cast<h8*>(vl + v_off(vd, 2 * x4)) = codes_f16(vw[n][0], vw[n][1]);
-            *reinterpret_cast<h8*>(vl + v_off(vd, 2 * x4 + 1)) = codes_f16(vw[n][2], vw[n][3]);
+            for (int i = 0; i < 16; ++i) {
+                x[i] = a0[i];
+                x[16 + i] = a1[i];
+            }
         }
-        float top = fmaxf(vs_next, dpp_mov<0xB1>(vs_next));
-        top = fmaxf(top, dpp_mov<0x4E>(top));
-        unit = fmaxf(unit, top);
+    };
+    // step t's scales, uniform over the wave
+    auto scales = [&](int t) {
+        const bool none = page_of(en0, t) == kNoPage;
+        dead_t = static_cast<int>(__ballot(none)) & 15;
+        const float ks = none ? 0.f : ks_t, vs = none ? 0.f : vs_t;
+        float vtop = fmaxf(vs, dpp_mov<0xB1>(vs));
+        vtop = fmaxf(vtop, dpp_mov<0x4E>(vtop));
+        unit = fmaxf(vr, vtop);
         // a page 2^-30 below the largest keeps that ratio: its weights leave fp16
         // there anyway (and a NaN, all scales 0, becomes it too)
-        const float lg = fmaxf(__builtin_amdgcn_logf(vs_next) - __builtin_amdgcn_logf(unit), -30.f);
+        const float lg = fmaxf(__builtin_amdgcn_logf(vs) - __builtin_amdgcn_logf(unit), -30.f);
         const float li = __builtin_amdgcn_exp2f(-lg);
-        dead = dead_next;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            mul[x] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ks_next), x));
-            vlog[x] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lg), x));
-            vinv[x] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(li), x));
+        for (int g = 0; g < 4; ++g) {
+            sc[g] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ks), g));
+            vlog[g] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lg), g));
+            vinv[g] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(li), g));
         }
-        unit = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(unit)));
+    };
+    // x -> pf, with the row statistics
+    auto softmax = [&](int t) {
+        const int t0 = k0 + 64 * t;
+        float sc_[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) sc_[g] = qmul * sc[g];
+        if (CAP) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = score<CAP>(x[i], sc_[i >> 3], 0.f, cap_out);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) sc_[g] = 1.f;
+        }
+        // element 8 g + e is key 16 g + 8 hf + e of the step
+        if (!(t0 + 64 <= wave_lo && dead_t == 0)) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int lim = (dead_t >> g & 1) ? 0 : vis - (t0 + 16 * g + 8 * hf);
+                // masked scores leave as the value that scales to -inf (a zero scale: all scores 0)
+                const float out = sc_[g] < 0.f ? -kNegInf : kNegInf;
+                const bool zero = sc_[g] == 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[8 * g + e] = e < lim ? (zero ? 0.f : x[8 * g + e]) : out;
+                if (zero) sc_[g] = 1.f;
+            }
+        }
+        float top = kNegInf;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            float hi = x[8 * g];
+            if (!CAP && p.sm_scale < 0.f) {
+#pragma unroll
+                for (int e = 1; e < 8; ++e) hi = fminf(hi, x[8 * g + e]);
+            } else {
+#pragma unroll
+                for (int e = 1; e < 8; ++e) hi = fmaxf(hi, x[8 * g + e]);
+            }
+            top = fmaxf(top, hi * sc_[g]);
+        }
+        top = fmaxf(top, lane_xor<32>(top));
+        // the reference follows the maximum once that is 2^8 past it: weights stay
+        // below 2^8, far inside fp16, and most steps rescale nothing
+        if (__any(top > m + 8.f || unit != vr)) {
+            const float mn = fmaxf(m, top);
+            const float r = m > kNegInf ? __builtin_amdgcn_exp2f(m - mn) : 1.f;
+            const float ro = r * (vr > 0.f ? vr / unit : 1.f);
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[d][i] *= ro;
+            l *= r;
+            m = mn;
+            vr = unit;
+        }
+        const float base = m > kNegInf ? m : 0.f;        // nothing seen yet: all weights 0
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            // weights times the page's v scale over the unit; the sum takes that out again
+            const float off = vlog[g] - base;
+            float sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float w = __builtin_amdgcn_exp2f(fmaf(x[8 * g + e], sc_[g], off));
+                sum += w;
+                pf[g][e] = static_cast<_Float16>(w);
+            }
+            l = fmaf(sum, vinv[g], l);
+        }
+    };
+    // what step t + 1's phases need, on its way during softmax(t)
+    // (past the last step: some page's codes, staged and never read)
+    auto ahead = [&](int t) {
+        fetch_k(page_of(en2, t + 2));
+        const int page = page_of(en1, t + 1);
+        fetch_v(page);
+        const int64_t at = static_cast<int64_t>(page < 0 ? 0 : page) * p.heads;
+        ks_t = ksh[at];
+        vs_t = vsh[at];
+        en0 = en1;
+        en1 = en2;
+        en2 = entry_of(t + 3);
     };
 
-    int buf = 0;
-    if (k0 < k1) {
-        ahead = page_ahead(k0);
-        fetch(k0);
-        stage(0);
+    if (steps > 0) {
+#pragma unroll
+        for (int i = 0; i < 2 * NC; ++i) stage_part(i, 0, 0);
+        // the first product with V meets weights of 0: its buffer must hold numbers
+#pragma unroll
+        for (int n = 0; n < (4 * D + TPB - 1) / TPB * 2; ++n)
+            if (tid + n * TPB < 8 * D)
+                *reinterpret_cast<u4*>(lds + 3 * KB + 16 * (tid + n * TPB)) = u4{0, 0, 0, 0};
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) pf[g][i] = static_cast<_Float16>(0.f);
+        en2 = en1;
+        en1 = en0;
+        ahead(-1);
     }
     __syncthreads();
-    for (int t0 = k0; t0 < k1; t0 += 64, buf ^= 1) {
-        const bool more = t0 + 64 < k1;
-        if (more) fetch(t0 + 64);
-        if (t0 < wave_hi) {
-            const char* kl = lds + buf * 2 * KB;
-            const char* vl = kl + KB;
-            float x[32];
-#pragma unroll
-            for (int T = 0; T < 2; ++T) {
-                f16v acc;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-#pragma unroll
-                for (int j = 0; j < NS; ++j)
-                    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                        *reinterpret_cast<const h8*>(kl + k_off<D>(32 * T + c, 2 * j + hf)), qf[j], acc, 0, 0, 0);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[16 * T + i] = acc[i];
-            }
-            // element 8 g + e is key 16 g + 8 hf + e of the step
-            if (CAP) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = score<CAP>(x[i], qmul * mul[i >> 3], 0.f, cap_out);
-            }
-            const bool whole = t0 + 64 <= wave_lo && dead == 0;
-            float top = kNegInf;
-            float sc[4];
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                sc[g] = CAP ? 1.f : qmul * mul[g];
-                if (!whole) {
-                    const int lim = (dead >> g & 1) ? 0 : vis - (t0 + 16 * g + 8 * hf);
-                    // masked scores leave as the value that scales to -inf (a zero scale: all scores 0)
-                    const float out = sc[g] < 0.f ? -kNegInf : kNegInf;
-                    const bool zero = sc[g] == 0.f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[8 * g + e] = e < lim ? (zero ? 0.f : x[8 * g + e]) : out;
-                    if (zero) sc[g] = 1.f;
-                }
-                float hi = x[8 * g];
-                if (!CAP && p.sm_scale < 0.f) {
-#pragma unroll
-                    for (int e = 1; e < 8; ++e) hi = fminf(hi, x[8 * g + e]);
-                } else {
-#pragma unroll
-                    for (int e = 1; e < 8; ++e) hi = fmaxf(hi, x[8 * g + e]);
-                }
-                top = fmaxf(top, hi * sc[g]);
-            }
-            top = fmaxf(top, lane_xor<32>(top));
-            // the reference follows the maximum once that is 2^8 past it: weights stay
-            // below 2^8, far inside fp16, and most steps rescale nothing
-            if (__any(top > m + 8.f || unit != vr)) {
-                const float mn = fmaxf(m, top);
-                const float r = m > kNegInf ? __builtin_amdgcn_exp2f(m - mn) : 1.f;
-                const float ro = r * (vr > 0.f ? vr / unit : 1.f);
-#pragma unroll
-                for (int t = 0; t < ND; ++t)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[t][i] *= ro;
-                l *= r;
-                m = mn;
-                vr = unit;
-            }
-            const float base = m > kNegInf ? m : 0.f;        // nothing seen yet: all weights 0
-            h8 pf[4];
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                // weights times the page's v scale over the unit; the sum takes that out again
-                const float off = vlog[g] - base;
-                float sum = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float w = __builtin_amdgcn_exp2f(fmaf(x[8 * g + e], sc[g], off));
-                    sum += w;
-                    pf[g][e] = static_cast<_Float16>(w);
-                }
-                l = fmaf(sum, vinv[g], l);
-            }
-#pragma unroll
-            for (int t = 0; t < ND; ++t)
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    o[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                        *reinterpret_cast<const h8*>(vl + v_off(32 * t + c, 2 * g + hf)), pf[g], o[t], 0, 0, 0);
-        }
-        if (more) stage(buf ^ 1);
+    if (grp) __syncthreads();
+    for (int t = 0; t < steps; ++t) {
+        products(t, true, true);
+        scales(t);
+        __syncthreads();
+        ahead(t);
+        softmax(t);
         __syncthreads();
     }
+    if (steps > 0) products(steps, true, false);
+    if (!grp) __syncthreads();
 
     l += lane_xor<32>(l);
     if (rw + c >= rows) return;
-    // element i of tile t is dimension 32 t + 8 (i / 4) + 4 hf + i % 4 of query c
+    // element i of tile d is dimension 32 (half ND + d) + 8 (i / 4) + 4 hf + i % 4 of query c
+    const int d0 = 32 * ND * half + 4 * hf;
     if (p.splits == 1) {
         const float inv = l > 0.f ? vr / l : 0.f;
-        char* dst = static_cast<char*>(p.out) + (row.token * p.ldo + static_cast<int64_t>(row.head) * D + 4 * hf) * 2;
+        char* dst = static_cast<char*>(p.out) + (row.token * p.ldo + static_cast<int64_t>(row.head) * D + d0) * 2;
 #pragma unroll
-        for (int t = 0; t < ND; ++t)
+        for (int d = 0; d < ND; ++d)
 #pragma unroll
             for (int i = 0; i < 16; i += 4) {
                 uint2 w;
                 if constexpr (DT == BF16) {
-                    w.x = pk_bf16(o[t][i] * inv, o[t][i + 1] * inv);
-                    w.y = pk_bf16(o[t][i + 2] * inv, o[t][i + 3] * inv);
+                    w.x = pk_bf16(o[d][i] * inv, o[d][i + 1] * inv);
+                    w.y = pk_bf16(o[d][i + 2] * inv, o[d][i + 3] * inv);
                 } else {
-                    w.x = f32_to_f16_bits(o[t][i] * inv) | static_cast<uint32_t>(f32_to_f16_bits(o[t][i + 1] * inv)) << 16;
-                    w.y = f32_to_f16_bits(o[t][i + 2] * inv) | static_cast<uint32_t>(f32_to_f16_bits(o[t][i + 3] * inv)) << 16;
+                    w.x = f32_to_f16_bits(o[d][i] * inv) | static_cast<uint32_t>(f32_to_f16_bits(o[d][i + 1] * inv)) << 16;
+                    w.y = f32_to_f16_bits(o[d][i + 2] * inv) | static_cast<uint32_t>(f32_to_f16_bits(o[d][i + 3] * inv)) << 16;
                 }
-                *reinterpret_cast<uint2*>(dst + (32 * t + 2 * i) * 2) = w;
+                *reinterpret_cast<uint2*>(dst + (32 * d + 2 * i) * 2) = w;
             }
     } else {
         const int64_t at = ((static_cast<int64_t>(sp) * p.ix.batch * p.ix.max_q + row.slot) * p.heads_q + row.head);
 #pragma unroll
-        for (int t = 0; t < ND; ++t)
+        for (int d = 0; d < ND; ++d)
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<float4*>(p.part_o + at * D + 32 * t + 2 * i + 4 * hf) =
-                    make_float4(o[t][i] * vr, o[t][i + 1] * vr, o[t][i + 2] * vr, o[t][i + 3] * vr);
-        if (hf == 0) {
+                *reinterpret_cast<float4*>(p.part_o + at * D + 32 * d + 2 * i + d0) =
+                    make_float4(o[d][i] * vr, o[d][i + 1] * vr, o[d][i + 2] * vr, o[d][i + 3] * vr);
+        if (hf == 0 && half == 0) {
             p.part_ml[2 * at] = m;
             p.part_ml[2 * at + 1] = l;
         }
     }
 }
 
-// Joins the splits of every (token, head): D / 8 lanes each.
-template <int DT, int D>
+// Joins the splits of each (token, head).  GROUPS == 1: D / 8 lanes to each, the
+// splits in turn (few of them: their loads go out together).  Else a block to
+// each, its lanes in GROUPS groups that share the splits and meet in LDS (64
+// splits of one token's 32 heads: 5.5 us, one group 23 us; 4 splits: 5.6 and 3.4).
+template <int DT, int D, int GROUPS>
 __global__ __launch_bounds__(256) void kv_attn_join_kernel(AttnParams p) {
-    const int64_t u = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / (D / 8);
-    const int d = threadIdx.x % (D / 8) * 8;
+    constexpr int LANES = D / 8;
+    __shared__ float lo[GROUPS][D + 8], lm[GROUPS], ll[GROUPS];
+    const int64_t u = GROUPS > 1 ? blockIdx.x : (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / LANES;
     const int64_t slot = u / p.heads_q;
     const int head = static_cast<int>(u % p.heads_q);
     const int b = static_cast<int>(slot / p.ix.max_q), i = static_cast<int>(slot % p.ix.max_q);
@@ -632,18 +744,39 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(AttnParams p) {
     const KvSeq s = kv_seq(p.ix, b);
     if (i >= s.n) return;
     const int vis = kv_visible(p.ix, s, b, s.first + i);
+    const int grp = GROUPS > 1 ? threadIdx.x / LANES : 0, d = threadIdx.x % LANES * 8;
+    const int used = vis > 0 ? (vis - 1) / p.split_keys + 1 : 0;
     float m = kNegInf, sum = 0.f, f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int sp = 0; sp < p.splits && sp * p.split_keys < vis; ++sp) {
-        const int64_t at = (static_cast<int64_t>(sp) * p.ix.batch * p.ix.max_q + slot) * p.heads_q + head;
-        const float ms = p.part_ml[2 * at], ls = p.part_ml[2 * at + 1];
-        float v[8];
-        load8<F32>(p.part_o + at * D + d, v);
+    auto add = [&](float ms, float ls, const float* v) {
         const float mn = fmaxf(m, ms), base = mn > kNegInf ? mn : 0.f;
         const float a = __builtin_amdgcn_exp2f(m - base), c = __builtin_amdgcn_exp2f(ms - base);
         sum = sum * a + ls * c;
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = f[e] * a + v[e] * c;
         m = mn;
+    };
+#pragma unroll 4
+    for (int sp = grp; sp < used; sp += GROUPS) {
+        const int64_t at = (static_cast<int64_t>(sp) * p.ix.batch * p.ix.max_q + slot) * p.heads_q + head;
+        const float ms = p.part_ml[2 * at], ls = p.part_ml[2 * at + 1];
+        float v[8];
+        load8<F32>(p.part_o + at * D + d, v);
+        add(ms, ls, v);
+    }
+    if (GROUPS > 1) {                         // groups past `used` hold nothing
+        store8<F32>(&lo[grp][d], f);
+        if (d == 0) {
+            lm[grp] = m;
+            ll[grp] = sum;
+        }
+        __syncthreads();
+        if (grp > 0) return;
+        const int groups = used < GROUPS ? used : GROUPS;
+        for (int g = 1; g < groups; ++g) {
+            float v[8];
+            load8<F32>(&lo[g][d], v);
+            add(lm[g], ll[g], v);
+        }
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
@@ -651,34 +784,34 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(AttnParams p) {
     store8<DT>(static_cast<char*>(p.out) + ((s.row0 + i) * p.ldo + static_cast<int64_t>(head) * D + d) * 2, f);
 }
 
-template <int DT, int D>
-hipError_t launch_d(const AttnParams& p, bool tile, hipStream_t st) {
-    const int64_t blocks = static_cast<int64_t>(p.ix.batch) * p.heads * p.row_tiles * p.splits;
-    if (tile) {
-        constexpr int bytes = 2 * 2 * 64 * D * 2;
-        auto kernel = p.cap > 0.f ? kv_attn_tile_kernel<DT, D, true, 4> : kv_attn_tile_kernel<DT, D, false, 4>;
-        if (bytes > 65536) {
-            const hipError_t a = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-            if (a != hipSuccess) return a;
-        }
-        kernel<<<dim3(static_cast<unsigned>(blocks)), 256, bytes, st>>>(p);
-    } else if (p.cap > 0.f)
-        kv_attn_rows16_kernel<DT, D, true><<<dim3(static_cast<unsigned>(blocks)), 256, 0, st>>>(p);
+void launch_lds(void (*kernel)(AttnParams), int64_t blocks, int threads, int lds, const AttnParams& p, hipStream_t st) {
+    if (lds > 65536)     // a launch's default limit
+        (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    kernel<<<dim3(static_cast<unsigned>(blocks)), threads, lds, st>>>(p);
+}
+
+template <int DT, int D, bool CAP>
+hipError_t launch_cap(const AttnParams& p, const KvAttnPlan& plan, hipStream_t st) {
+    if (plan.many)
+        launch_lds(kv_attn_phase_kernel<DT, D, CAP>, plan.blocks, 512, 2 * 2 * 64 * D * 2, p, st);
     else
-        kv_attn_rows16_kernel<DT, D, false><<<dim3(static_cast<unsigned>(blocks)), 256, 0, st>>>(p);
-    hipError_t e = hipGetLastError();
+        launch_lds(kv_attn_rows16_kernel<DT, D, CAP>, plan.blocks, 256, plan.lds_bytes, p, st);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
-    const int64_t lanes = static_cast<int64_t>(p.ix.batch) * p.ix.max_q * p.heads_q * (D / 8);
-    kv_attn_join_kernel<DT, D><<<dim3(static_cast<unsigned>((lanes + 255) / 256)), 256, 0, st>>>(p);
+    const int64_t rows = static_cast<int64_t>(p.ix.batch) * p.ix.max_q * p.heads_q;
+    if (p.splits > 8)
+        kv_attn_join_kernel<DT, D, 2048 / D><<<dim3(static_cast<unsigned>(rows)), 256, 0, st>>>(p);
+    else
+        kv_attn_join_kernel<DT, D, 1><<<dim3(static_cast<unsigned>((rows * (D / 8) + 255) / 256)), 256, 0, st>>>(p);
     return hipGetLastError();
 }
 
 template <int DT>
-hipError_t launch_dt(const AttnParams& p, int d, bool tile, hipStream_t st) {
-    if (d == 64) return launch_d<DT, 64>(p, tile, st);
-    if (d == 128) return launch_d<DT, 128>(p, tile, st);
-    return launch_d<DT, 256>(p, tile, st);
+hipError_t launch_dt(const AttnParams& p, const KvAttnPlan& plan, int d, hipStream_t st) {
+    const bool cap = p.cap > 0.f;
+    if (d == 64) return cap ? launch_cap<DT, 64, true>(p, plan, st) : launch_cap<DT, 64, false>(p, plan, st);
+    if (d == 128) return cap ? launch_cap<DT, 128, true>(p, plan, st) : launch_cap<DT, 128, false>(p, plan, st);
+    return cap ? launch_cap<DT, 256, true>(p, plan, st) : launch_cap<DT, 256, false>(p, plan, st);
 }
 
 }  // namespace
@@ -693,7 +826,7 @@ hipError_t launch_kv_attention(const KvAttnPlan& plan, const void* q, int dtype,
         p.part_o = static_cast<float*>(ws);
         p.part_ml = p.part_o + static_cast<int64_t>(plan.splits) * ix.batch * ix.max_q * heads_q * d;
     }
-    return dtype == F16 ? launch_dt<F16>(p, d, plan.tile, st) : launch_dt<BF16>(p, d, plan.tile, st);
+    return dtype == F16 ? launch_dt<F16>(p, plan, d, st) : launch_dt<BF16>(p, plan, d, st);
 }
 
 }  // namespace qlin

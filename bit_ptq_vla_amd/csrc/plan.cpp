@@ -173,21 +173,23 @@ int64_t composite_calib_work_bytes(int64_t n, int64_t k, int b) {
 KvAttnPlan plan_kv_attention(int64_t batch, int64_t max_q, int64_t max_kv, int heads_q, int heads, int d,
                              bool allow_split) {
     KvAttnPlan p;
-    const int64_t rows = max_q * (heads_q / heads);
-    p.tile = rows > 64;
-    const int64_t per = p.tile ? 128 : 16;
+    const int64_t rows = max_q * (heads_q / heads), cus = device_cus();
+    p.many = rows > 64;
+    const int64_t per = !p.many ? 16 : d == 256 ? 128 : 256;
     p.row_tiles = static_cast<int>((rows + per - 1) / per);
     const int64_t units = batch * heads * p.row_tiles;
-    // few tiles: their keys are split until there are two blocks for each CU,
-    // 256 keys (a step of the block's four waves) at least to each
+    p.lds_bytes = static_cast<int>(4 * (rows < 16 ? rows : 16) * (d + 6) * 4);
+    // Few tiles: their keys are split until there are two blocks of 16 rows for
+    // each CU, or one of many rows (which fill a CU each), 256 keys at least to a
+    // block.
     int64_t splits = 1;
     if (allow_split && units > 0) {
-        const int64_t want = (2 * static_cast<int64_t>(device_cus()) + units - 1) / units, most = (max_kv + 255) / 256;
+        const int64_t want = p.many ? cus / units : (2 * cus + units - 1) / units, most = (max_kv + 255) / 256;
         splits = want < most ? want : most;
         splits = splits < 1 ? 1 : splits;
     }
     const int64_t keys = ((max_kv + splits - 1) / splits + 255) / 256 * 256;
-    p.split_keys = static_cast<int>(keys < 256 ? 256 : keys > 0x7FFFFF00 ? 0x7FFFFF00 : keys);
+    p.split_keys = static_cast<int>(keys < 256 ? 256 : keys);
     p.splits = splits == 1 ? 1 : static_cast<int>((max_kv + p.split_keys - 1) / p.split_keys);
     p.blocks = units * p.splits;
     p.ws_bytes = p.splits > 1 ? p.splits * batch * max_q * heads_q * (d + 2) * 4 : 0;

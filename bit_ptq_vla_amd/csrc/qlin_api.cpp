@@ -605,8 +605,9 @@ qlin_status qlin_rope_append_kv(const void* qkv, qlin_dtype dtype, int64_t token
     if (!aligned4(positions)) return QLIN_ERR_ALIGN;
     // one block per (page, head) of k and of v, then the q heads
     const int64_t touched = qlin::kv_max_touched(batch->max_q, cache->page_size);
-    if (touched > 0 && static_cast<int64_t>(batch->batch) * cache->heads > (1LL << 30) / touched) return QLIN_ERR_SHAPE;
-    if (tokens * heads_q > (1LL << 33)) return QLIN_ERR_SHAPE;
+    if (touched > 0 && static_cast<int64_t>(batch->batch) * cache->heads > (1LL << 29) / touched) return QLIN_ERR_SHAPE;
+    const int64_t q_tasks = static_cast<int64_t>(batch->max_q) * heads_q * (d / 16);
+    if (q_tasks > (1LL << 31) || batch->batch * (q_tasks / 64 + 1) > (1LL << 30)) return QLIN_ERR_SHAPE;
     const int64_t codes = cache->pages * cache->heads * cache->page_size * d, scales = cache->pages * cache->heads * 4;
     const Span outs[5] = {{cache->k, codes}, {cache->v, codes}, {cache->k_scale, scales}, {cache->v_scale, scales},
                           {q_out, tokens > 0 ? ((tokens - 1) * ldq + heads_q * d) * 2 : 0}};

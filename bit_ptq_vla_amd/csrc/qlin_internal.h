@@ -113,7 +113,8 @@ hipError_t launch_rope_table(float* table, int64_t positions, int rot, double ba
 // blocks share a tile's keys (split_keys each; their partials, ws_bytes, are
 // joined by a second kernel).
 struct KvAttnPlan {
-    bool tile;   // 128 rows to a block, else 16
+    bool many;                // 256 query rows (128 of a 256-wide head) to a block; else 16
+    int lds_bytes;            // of the 16-row blocks
     int row_tiles, splits, split_keys;
     int64_t blocks, ws_bytes;
 };

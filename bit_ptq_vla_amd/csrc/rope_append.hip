@@ -8,15 +8,26 @@
 //
 // One launch.  A block owns one (page, head) of K or of V and every token the
 // call adds to it, so the page's scale is decided in one place; the blocks
-// after those turn q.  K is rotated in float64: a 16-bit value times an fp32
-// cosine is exact there, so scales and codes are those of exact arithmetic
-// (q's pairs take fp32, one rounding of the products more than its own).
+// after those turn q.  Scales and codes are those of exact arithmetic, which
+// float64 gives (a 16-bit value times an fp32 cosine is exact there): values
+// are turned in fp32, and what fp32 cannot decide, the maximum among values
+// close to it and the side of a half-integer a quotient lies on, is decided
+// again in float64 by the threads concerned.  (All of it in float64 took 21
+// vector instructions a value, more than the memory time of a prompt.)
 //
-// A task is 16 values of a head: the two 8-value chunks that hold each other's
-// partners (halves layout: 8s and 8s + rot/2; interleaved: 16s and 16s + 8).
-// V's codes cross LDS to lie keys-first ([d][page]) as the attention reads
-// them.
+// The values stay in registers between the scale's reduction and the codes,
+// x * (1 / s) rounded by a magic add, whose distance from a half-integer is
+// known.
+//
+// A K task is 16 values of a token's head: the two 8-value chunks that hold
+// each other's partners (halves layout: 8s and 8s + rot/2; interleaved: 16s
+// and 16s + 8).  A V task is 8 dimensions of four tokens, whose codes are four
+// bytes each of the keys-first page.
+//
+// Bound by memory for prompts: q|k|v read once, q written, one byte a key and
+// value (measured figures at the launch).
 
+#include "code_pack.h"
 #include "device_common.h"
 #include "kv_index.h"
 #include "qlin_internal.h"
@@ -40,19 +51,22 @@ struct AppendParams {
     int64_t ldq;
     int heads_q, heads, rot, interleaved;
     int touched;       // pages per sequence the grid covers
-    int64_t kv_blocks;
+    uint32_t kv_blocks, q_blocks;   // blocks that store; blocks of a sequence's q
 };
+
+typedef unsigned short us2 __attribute__((ext_vector_type(2)));
 
 // Columns of the two chunks of task s (of D / 16) and the angle its pairs start at.
 struct Task {
     int ca, cb, angle;
-    bool turn;
+    bool turn, neighbours;
 };
 
 __device__ __forceinline__ Task task_of(int s, int rot, int interleaved) {
     Task t;
     t.turn = 16 * s < rot;
     t.angle = t.turn ? 8 * s : 0;
+    t.neighbours = t.turn && interleaved;
     if (t.turn && !interleaved) {
         t.ca = 8 * s;
         t.cb = 8 * s + rot / 2;
@@ -63,26 +77,21 @@ __device__ __forceinline__ Task task_of(int s, int rot, int interleaved) {
     return t;
 }
 
-// a, b: the task's chunks, turned in place by the angles cs (cosines) and sn.
-template <typename F>
-__device__ __forceinline__ void turn16(F (&a)[8], F (&b)[8], const float cs[8], const float sn[8], int interleaved) {
-    if (interleaved) {
+// Two chunks (the values at t.ca .. and at t.cb ..) to pairs (x[2 i], x[2 i + 1])
+// and back: neighbours of a chunk in the interleaved layout, else one of each.
+__device__ __forceinline__ void to_pairs(const float a[8], const float b[8], bool neighbours, float x[16]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const F c0 = cs[i], s0 = sn[i], c1 = cs[4 + i], s1 = sn[4 + i];
-            const F x = a[2 * i], y = a[2 * i + 1], z = b[2 * i], w = b[2 * i + 1];
-            a[2 * i] = x * c0 - y * s0;
-            a[2 * i + 1] = y * c0 + x * s0;
-            b[2 * i] = z * c1 - w * s1;
-            b[2 * i + 1] = w * c1 + z * s1;
-        }
-    } else {
+    for (int i = 0; i < 8; ++i) {
+        x[2 * i] = neighbours ? (i < 4 ? a[(2 * i) & 7] : b[(2 * i) & 7]) : a[i];
+        x[2 * i + 1] = neighbours ? (i < 4 ? a[(2 * i + 1) & 7] : b[(2 * i + 1) & 7]) : b[i];
+    }
+}
+template <typename T>
+__device__ __forceinline__ void to_chunks(const T x[16], bool neighbours, T a[8], T b[8]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const F c = cs[i], s = sn[i], x = a[i], y = b[i];
-            a[i] = x * c - y * s;
-            b[i] = y * c + x * s;
-        }
+    for (int i = 0; i < 8; ++i) {
+        a[i] = neighbours ? x[i] : x[2 * i];
+        b[i] = neighbours ? x[8 + i] : x[2 * i + 1];
     }
 }
 
@@ -92,30 +101,58 @@ __device__ __forceinline__ const float* rope_row(const AppendParams& p, int64_t 
     return p.rope + pos * p.rot;
 }
 
+// A task's pairs and their angles (1, 0 where its columns do not turn).
 template <int DT>
-__device__ __forceinline__ void load16(const AppendParams& p, int64_t row, int64_t col0, const Task& t, bool turn,
-                                       int64_t place, double (&a)[8], double (&b)[8]) {
+__device__ __forceinline__ void load_pairs(const AppendParams& p, int64_t row, int64_t col0, const Task& t,
+                                           int64_t place, float x[16], float cs[8], float sn[8]) {
     const char* src = static_cast<const char*>(p.qkv) + (row * p.ld + col0) * 2;
-    float fa[8], fb[8];
-    load8<DT>(src + t.ca * 2, fa);
-    load8<DT>(src + t.cb * 2, fb);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        a[i] = fa[i];
-        b[i] = fb[i];
-    }
-    if (turn) {
+    float a[8], b[8];
+    load8<DT>(src + t.ca * 2, a);
+    load8<DT>(src + t.cb * 2, b);
+    if (t.turn) {
         const float* r = rope_row(p, row, place) + t.angle;
-        float cs[8], sn[8];
         load8<F32>(r, cs);
         load8<F32>(r + p.rot / 2, sn);
-        turn16<double>(a, b, cs, sn, p.interleaved);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            cs[i] = 1.f;
+            sn[i] = 0.f;
+        }
+    }
+    to_pairs(a, b, t.neighbours, x);
+}
+
+// The pairs turned in fp32.  (Columns that do not turn stay as they are: a
+// product with 0 would make an infinity's partner NaN.)
+template <int DT>
+__device__ __forceinline__ void load16(const AppendParams& p, int64_t row, int64_t col0, const Task& t, int64_t place,
+                                       float x[16]) {
+    float cs[8], sn[8];
+    load_pairs<DT>(p, row, col0, t, place, x, cs, sn);
+    if (t.turn) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float u = x[2 * i], w = x[2 * i + 1];
+            x[2 * i] = u * cs[i] - w * sn[i];
+            x[2 * i + 1] = w * cs[i] + u * sn[i];
+        }
     }
 }
 
-__device__ __forceinline__ double finite_abs(double v) {
-    const double a = fabs(v);
-    return a <= 1.7976931348623157e308 ? a : 0.0;   // infinities and NaN do not set the scale
+// f(i, u, w) for the pairs in float64, one at a time, so that few float64
+// values live together.
+template <int DT, typename F>
+__device__ __forceinline__ void each_pair(const AppendParams& p, int64_t row, int64_t col0, const Task& t,
+                                          int64_t place, F f) {
+    float x[16], cs[8], sn[8];
+    load_pairs<DT>(p, row, col0, t, place, x, cs, sn);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const double u = x[2 * i], w = x[2 * i + 1], c = cs[i], d = sn[i];
+        f(i, t.turn ? u * c - w * d : u, t.turn ? w * c + u * d : w);
+        __builtin_amdgcn_sched_barrier(0);
+    }
 }
 
 // rne(v / s) on the grid: infinities at its ends, NaN as 0.
@@ -124,157 +161,289 @@ __device__ __forceinline__ int code_of(double v, double s) {
     return static_cast<int>(fmin(fmax(rint(v / s), -127.0), 127.0));
 }
 
+// rne(v / s) where r is within a small fraction of a step of v / s, by the sign
+// of v - h s for the half-integer h next to r (h s is exact).
+__device__ __forceinline__ int code_near(double v, double s, float r) {
+    const float q = rintf(r), h = r > q ? q + 0.5f : q - 0.5f;
+    const double t = fma(-static_cast<double>(h), s, v);
+    const int lower = static_cast<int>(h - 0.5f);
+    const int code = t > 0.0 ? lower + 1 : t < 0.0 ? lower : lower + (lower & 1);
+    return code < -127 ? -127 : code > 127 ? 127 : code;
+}
+
+// The codes of n fp32 values in the low bytes of cb.  False where a value lies
+// so near a half-integer of v / s that fp32 cannot tell its side.  A turned
+// value fma(a, c, -(b d)) is off by 2^-24 (|b d| + |v|), and |b d| is at most
+// sqrt 2 times the page's maximum M, since a turn is a product of complex
+// numbers: 2.5 x 2^-24 M, 127 of which are 1.9e-5 in steps of s = M / 127; 1 / s
+// and its use add 127.5 x 2^-23 = 1.6e-5.  The window is wider.
+constexpr float kMagic = 12582912.f;   // 1.5 x 2^23: the sum's low bits are the rounded value
+template <int N>
+__device__ __forceinline__ bool codes_f32(const float* v, float inv, uint32_t* cb) {
+    float worst = 0.f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const float qb = fmaf(v[e], inv, kMagic);
+        worst = fmaxf(worst, fabsf(fmaf(v[e], inv, kMagic - qb)));
+        cb[e] = __float_as_uint(qb);
+    }
+    return worst < 0.5f - 6e-5f;
+}
+
+template <int TPB>
+__device__ __forceinline__ float block_max(float top, float* red) {
+    top = wave_max(top, 64);
+    if (TPB > 64) {
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < TPB / 64; ++w) top = fmaxf(top, red[w]);
+    }
+    return top;
+}
+
 template <int DT, int D, int TPB>
-__device__ __forceinline__ void store_page(const AppendParams& p, int64_t unit) {
+__device__ __forceinline__ void store_page(const AppendParams& p, uint32_t unit) {
     constexpr int S = D / 16;
-    __shared__ double red[TPB / 64];
-    __shared__ uint8_t tile[D * 64];
+    // most tasks a thread takes: 64 tokens (a page), or 64 / S of them to a wave
+    constexpr int KT = TPB == 64 ? 1 : 64 * S / TPB, VT = TPB == 64 ? 1 : 16 * (D / 8) / TPB > 0 ? 16 * (D / 8) / TPB : 1;
+    __shared__ float red[TPB / 64];
+    __shared__ unsigned long long exact;
     const int tid = threadIdx.x;
-    const bool is_v = unit & 1;
-    const int h = static_cast<int>((unit >> 1) % p.heads);
-    const int64_t rest = (unit >> 1) / p.heads;
-    const int b = static_cast<int>(rest / p.touched);
+    // the k blocks first, then the v blocks: 266 us for 52224 tokens of 8 heads of
+    // 256, alternating 293
+    const uint32_t half = p.kv_blocks >> 1;
+    const bool is_v = unit >= half;
+    if (is_v) unit -= half;
+    const uint32_t pair = unit / p.heads, h = unit - pair * p.heads;
+    const int b = static_cast<int>(pair / p.touched);
     const KvSeq seq = kv_seq(p.ix, b);
     if (seq.n == 0) return;
-    const KvSpan span = kv_touched(p.ix, seq, static_cast<int>(rest % p.touched));
+    const KvSpan span = kv_touched(p.ix, seq, static_cast<int>(pair - b * p.touched));
     if (span.hi <= span.lo) return;
     const int page = kv_page(p.ix, b, span.idx);
-    if (page == kNoPage) return;
 
     const int ps = p.ix.page_size;
     const int start = span.idx * ps, o_lo = span.lo - start, count = span.hi - span.lo;
     const int64_t col0 = (static_cast<int64_t>(p.heads_q) + (is_v ? p.heads : 0) + h) * D;
+    const int64_t row0 = seq.row0 + (span.lo - seq.first);        // the span's first row
+
+    // the span's values, and their maximum
+    const int wf = o_lo >> 2, nw = ((o_lo + count + 3) >> 2) - wf;       // V: words of four tokens
+    float kx[KT][16];                         // K: turned, fp32
+    uint4 vraw[VT][4];
+    float top = 0.f;
+    bool odd = false;                         // an infinity or a NaN among the thread's values
+    if (!is_v) {
+        float nan = 0.f;
+#pragma unroll
+        for (int n = 0; n < KT; ++n) {
+            const int i = tid + n * TPB;
+            if (i < count * S) {
+                const Task t = task_of(i % S, p.rot, p.interleaved);
+                load16<DT>(p, row0 + i / S, col0, t, span.lo + i / S, kx[n]);
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                    top = max3_abs(top, kx[n][e], kx[n][e + 1]);
+                    nan = fmaf(kx[n][e], 0.f, fmaf(kx[n][e + 1], 0.f, nan));
+                }
+            }
+        }
+        odd = nan != nan;
+        if (odd) top = __builtin_inff();
+    } else {
+#pragma unroll
+        for (int n = 0; n < VT; ++n) {
+            const int i = tid + n * TPB;
+            if (i < nw * (D / 8)) {
+                const int c8 = i / nw, w = wf + i - c8 * nw;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const int at = 4 * w + t - o_lo;              // token of the span
+                    const bool in = at >= 0 && at < count;
+                    const char* src = static_cast<const char*>(p.qkv) + ((row0 + (in ? at : 0)) * p.ld + col0 + 8 * c8) * 2;
+                    vraw[n][t] = *reinterpret_cast<const uint4*>(src);
+                    if (!in) vraw[n][t] = make_uint4(0, 0, 0, 0);
+                }
+            }
+        }
+        // magnitudes of 16-bit floats order as their bits (infinities and NaN last)
+        us2 m = {0, 0};
+#pragma unroll
+        for (int n = 0; n < VT; ++n) {
+            if (tid + n * TPB < nw * (D / 8)) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const uint32_t w[4] = {vraw[n][t].x, vraw[n][t].y, vraw[n][t].z, vraw[n][t].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const us2 x = __builtin_bit_cast(us2, w[e] & 0x7FFF7FFFu);
+                        m = m > x ? m : x;
+                    }
+                }
+            }
+        }
+        const uint16_t lo = m[0], hi = m[1], bits = lo > hi ? lo : hi;
+        odd = bits >= (DT == BF16 ? 0x7F80 : 0x7C00);
+        top = odd ? __builtin_inff() : DT == BF16 ? bf16_to_f32(bits) : f16_bits_to_f32(bits);
+    }
+    if (page == kNoPage) return;              // (the whole block)
     const int64_t slot = static_cast<int64_t>(page) * p.heads + h;
     float* scale = (is_v ? p.vs : p.ks) + slot;
     int8_t* base = (is_v ? p.v : p.k) + slot * ps * D;
     const float s_old = o_lo > 0 ? *scale : 0.f;
-
-    double top = 0.0;
-    for (int i = tid; i < count * S; i += TPB) {
-        const int j = span.lo + i / S;
-        const Task t = task_of(i % S, is_v ? 0 : p.rot, p.interleaved);
-        double a[8], c[8];
-        load16<DT>(p, seq.row0 + (j - seq.first), col0, t, !is_v && t.turn, j, a, c);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmax(top, fmax(finite_abs(a[e]), finite_abs(c[e])));
-    }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) top = fmax(top, __shfl_xor(top, d, 64));
-    if (TPB > 64) {
-        if ((tid & 63) == 0) red[tid >> 6] = top;
+    if (tid == 0) exact = 0;
+    const float mine = top;
+    top = block_max<TPB>(top, red);
+    // The maximum in exact arithmetic: V's is what it is; a turned K value is off
+    // by 2.5 x 2^-24 of it, so the threads whose own maximum comes within 2^-20
+    // look again.  With an infinity or a NaN in the page, all threads do, past those.
+    double most = top;
+    if (TPB == 64) __syncthreads();           // exact is set
+    if (!(top < __builtin_inff()) || (!is_v && p.rot > 0)) {
+        if (!(top < __builtin_inff()) || mine >= top * (1.f - 0x1p-20f)) {
+            double m = 0.0;
+#pragma unroll 1
+            for (int i = tid; i < count * S; i += TPB) {
+                const Task t = task_of(i % S, is_v ? 0 : p.rot, p.interleaved);
+                each_pair<DT>(p, row0 + i / S, col0, t, span.lo + i / S, [&](int, double u, double w) {
+                    u = fabs(u), w = fabs(w);
+                    if (u <= 1.7976931348623157e308) m = fmax(m, u);
+                    if (w <= 1.7976931348623157e308) m = fmax(m, w);
+                });
+            }
+            atomicMax(&exact, static_cast<unsigned long long>(__double_as_longlong(m)));   // m >= 0: ordered bits
+        }
         __syncthreads();
-        for (int w = 0; w < TPB / 64; ++w) top = fmax(top, red[w]);
+        most = __longlong_as_double(static_cast<long long>(exact));
     }
-    const float s_new = fmaxf(s_old, static_cast<float>(top / 127.0));
-    const bool grown = o_lo > 0 && s_new != s_old;
+    const float s_new = fmaxf(s_old, static_cast<float>(most / 127.0));
     const double s = s_new;
+    // 1 / s in fp32; a scale so small that it overflows takes the quotients
+    const float inv = s_new > 1e-36f ? 1.f / s_new : 0.f;
+    const bool plain = !odd && (s_new > 1e-36f || s_new == 0.f);
     if (tid == 0) *scale = s_new;
 
-    for (int i = tid; i < count * S; i += TPB) {
-        const int j = span.lo + i / S;
-        const Task t = task_of(i % S, is_v ? 0 : p.rot, p.interleaved);
-        double a[8], c[8];
-        load16<DT>(p, seq.row0 + (j - seq.first), col0, t, !is_v && t.turn, j, a, c);
-        const int off = j - start;
-        if (is_v) {
+    if (!is_v) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                tile[(t.ca + e) * ps + off] = static_cast<uint8_t>(code_of(a[e], s));
-                tile[(t.cb + e) * ps + off] = static_cast<uint8_t>(code_of(c[e], s));
+        for (int n = 0; n < KT; ++n) {
+            const int i = tid + n * TPB;
+            if (i < count * S) {
+                const Task t = task_of(i % S, p.rot, p.interleaved);
+                uint32_t cb[16];
+                if (!(codes_f32<16>(kx[n], inv, cb) && plain)) {
+                    each_pair<DT>(p, row0 + i / S, col0, t, span.lo + i / S, [&](int e, double u, double w) {
+                        cb[2 * e] = plain ? code_near(u, s, kx[n][2 * e] * inv) : code_of(u, s);
+                        cb[2 * e + 1] = plain ? code_near(w, s, kx[n][2 * e + 1] * inv) : code_of(w, s);
+                    });
+                }
+                uint32_t ca[8], cc[8];
+                to_chunks(cb, t.neighbours, ca, cc);
+                int8_t* dst = base + (o_lo + i / S) * D;
+                *reinterpret_cast<uint2*>(dst + t.ca) = pack8_i8(ca);
+                *reinterpret_cast<uint2*>(dst + t.cb) = pack8_i8(cc);
             }
-        } else {
-            uint32_t w[4] = {0, 0, 0, 0};
+        }
+    } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                w[e >> 2] |= (static_cast<uint32_t>(code_of(a[e], s)) & 0xFFu) << (8 * (e & 3));
-                w[2 + (e >> 2)] |= (static_cast<uint32_t>(code_of(c[e], s)) & 0xFFu) << (8 * (e & 3));
+        for (int n = 0; n < VT; ++n) {
+            const int i = tid + n * TPB;
+            if (i < nw * (D / 8)) {
+                const int c8 = i / nw, w = wf + i - c8 * nw;
+                uint32_t cb[4][8];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    float x[8];
+                    unpack8<DT>(vraw[n][t], x);
+                    if (!(codes_f32<8>(x, inv, cb[t]) && plain)) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            cb[t][e] = static_cast<uint32_t>(plain ? code_near(x[e], s, x[e] * inv) : code_of(x[e], s));
+                    }
+                }
+                const int off = 4 * w;
+                const bool whole = off >= o_lo && off + 4 <= o_lo + count;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    int8_t* dst = base + (8 * c8 + e) * ps + off;
+                    const uint32_t lo = __builtin_amdgcn_perm(cb[1][e], cb[0][e], 0x0C0C0400u);
+                    const uint32_t hi = __builtin_amdgcn_perm(cb[3][e], cb[2][e], 0x04000C0Cu);
+                    if (whole) {
+                        *reinterpret_cast<uint32_t*>(dst) = lo | hi;
+                    } else {
+#pragma unroll
+                        for (int t = 0; t < 4; ++t)
+                            if (off + t >= o_lo && off + t < o_lo + count) dst[t] = static_cast<int8_t>(cb[t][e]);
+                    }
+                }
             }
-            *reinterpret_cast<uint2*>(base + off * D + t.ca) = make_uint2(w[0], w[1]);
-            *reinterpret_cast<uint2*>(base + off * D + t.cb) = make_uint2(w[2], w[3]);
         }
     }
     // the page's earlier codes follow its scale
-    if (grown) {
+    if (o_lo > 0 && s_new != s_old) {
         const double so = s_old;
-        for (int i = tid; i < o_lo * D; i += TPB) {
-            const int off = is_v ? i % o_lo : i / D, col = is_v ? i / o_lo : i % D;
-            int8_t* at = is_v ? base + col * ps + off : base + off * D + col;
-            *at = static_cast<int8_t>(code_of(static_cast<double>(*at) * so, s));
-        }
-    }
-    if (is_v) {
-        __syncthreads();
-        for (int i = tid; i < D * ps / 4; i += TPB) {
-            const int col = i / (ps / 4), off = i % (ps / 4) * 4;
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(tile + col * ps + off);
-            if (off >= o_lo && off + 4 <= o_lo + count) {
-                *reinterpret_cast<uint32_t*>(base + col * ps + off) = w;
-            } else {
+        const int words = is_v ? (o_lo + 3) >> 2 : o_lo * (D / 4);
+        for (int i = tid; i < (is_v ? words * D : words); i += TPB) {
+            const int off = is_v ? i % words * 4 : 0;
+            int8_t* at = is_v ? base + i / words * ps + off : base + 4 * i;
+            const uint32_t was = *reinterpret_cast<const uint32_t*>(at);
+            uint32_t now = 0;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (off + e >= o_lo && off + e < o_lo + count)
-                        base[col * ps + off + e] = static_cast<int8_t>(w >> (8 * e));
+            for (int e = 0; e < 4; ++e) {
+                const int c = static_cast<int8_t>(was >> (8 * e));
+                now |= (static_cast<uint32_t>(code_of(static_cast<double>(c) * so, s)) & 0xFFu) << (8 * e);
+            }
+            if (!is_v || off + 4 <= o_lo) {
+                *reinterpret_cast<uint32_t*>(at) = now;
+            } else {
+                for (int e = 0; off + e < o_lo; ++e) at[e] = static_cast<int8_t>(now >> (8 * e));
             }
         }
     }
 }
 
 template <int DT, int D, int TPB>
-__device__ __forceinline__ void turn_q(const AppendParams& p, int64_t block) {
+__device__ __forceinline__ void turn_q(const AppendParams& p, uint32_t block) {
     constexpr int S = D / 16;
-    const int64_t i = block * TPB + threadIdx.x;
-    const int64_t head = i / S, row = head / p.heads_q;
-    if (row >= p.ix.tokens) return;
-    // the row's sequence: the last one that starts at or before it
-    int lo = 0, hi = p.ix.batch;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.ix.q_start[mid] <= row) lo = mid;
-        else hi = mid;
-    }
-    // rows behind the last sequence (or in front of the first) stay as they are
-    const KvSeq seq = kv_seq(p.ix, lo);
-    if (row < seq.row0 || row >= seq.row0 + seq.n) return;
+    // blocks of one sequence: its rows' q heads, 16 values to a thread
+    const uint32_t b = block / p.q_blocks;
+    const KvSeq seq = kv_seq(p.ix, static_cast<int>(b));
+    const uint32_t i = (block - b * p.q_blocks) * TPB + threadIdx.x;
+    const uint32_t head = i / S, r = head / p.heads_q;
+    if (r >= static_cast<uint32_t>(seq.n)) return;
+    const int64_t row = seq.row0 + r;
     const Task t = task_of(static_cast<int>(i % S), p.rot, p.interleaved);
-    const int64_t col0 = (head % p.heads_q) * D;
-    const char* src = static_cast<const char*>(p.qkv) + (row * p.ld + col0) * 2;
+    const int64_t col0 = static_cast<int64_t>(head - r * p.heads_q) * D;
     char* dst = static_cast<char*>(p.q_out) + (row * p.ldq + col0) * 2;
-    float a[8], b[8];
-    load8<DT>(src + t.ca * 2, a);
-    load8<DT>(src + t.cb * 2, b);
-    if (t.turn) {
-        const float* r = rope_row(p, row, seq.first + (row - seq.row0)) + t.angle;
-        float cs[8], sn[8];
-        load8<F32>(r, cs);
-        load8<F32>(r + p.rot / 2, sn);
-        turn16<float>(a, b, cs, sn, p.interleaved);
-    }
+    float x[16];
+    load16<DT>(p, row, col0, t, seq.first + static_cast<int64_t>(r), x);
+    float a[8], c[8];
+    to_chunks(x, t.neighbours, a, c);
     store8<DT>(dst + t.ca * 2, a);
-    store8<DT>(dst + t.cb * 2, b);
+    store8<DT>(dst + t.cb * 2, c);
 }
 
 template <int DT, int D, int TPB>
-__global__ __launch_bounds__(TPB) void rope_append_kernel(AppendParams p) {
-    const int64_t block = blockIdx.x;
-    if (block < p.kv_blocks)
-        store_page<DT, D, TPB>(p, block);
+__global__ __launch_bounds__(TPB, 4) void rope_append_kernel(AppendParams p) {
+    if (blockIdx.x < p.kv_blocks)
+        store_page<DT, D, TPB>(p, blockIdx.x);
     else
-        turn_q<DT, D, TPB>(p, block - p.kv_blocks);
+        turn_q<DT, D, TPB>(p, blockIdx.x - p.kv_blocks);
 }
 
 template <int DT, int D, int TPB>
 hipError_t launch_tpb(AppendParams p, hipStream_t st) {
-    p.kv_blocks = static_cast<int64_t>(p.ix.batch) * p.touched * p.heads * 2;
-    const int64_t q_blocks = (p.ix.tokens * p.heads_q * (D / 16) + TPB - 1) / TPB;
-    rope_append_kernel<DT, D, TPB><<<dim3(static_cast<unsigned>(p.kv_blocks + q_blocks)), TPB, 0, st>>>(p);
+    p.kv_blocks = static_cast<uint32_t>(p.ix.batch) * p.touched * p.heads * 2;
+    p.q_blocks = static_cast<uint32_t>((static_cast<int64_t>(p.ix.max_q) * p.heads_q * (D / 16) + TPB - 1) / TPB);
+    rope_append_kernel<DT, D, TPB><<<dim3(p.kv_blocks + p.q_blocks * p.ix.batch), TPB, 0, st>>>(p);
     return hipGetLastError();
 }
 
 template <int DT, int D>
 hipError_t launch_d(const AppendParams& p, hipStream_t st) {
     // a block per (page, head): one wave where a call adds few values to each
-    if (p.ix.max_q * (D / 16) <= 64) return launch_tpb<DT, D, 64>(p, st);
-    return launch_tpb<DT, D, 256>(p, st);
+    if (p.ix.max_q * (D / 16) <= 64 && (p.ix.max_q + 6) / 4 * (D / 8) <= 64) return launch_tpb<DT, D, 64>(p, st);
+    return launch_tpb<DT, D, D == 256 ? 512 : 256>(p, st);
 }
 
 template <int DT>
@@ -303,7 +472,7 @@ hipError_t launch_rope_append(const void* qkv, int dtype, int64_t ld, int heads_
                               int8_t* v, float* ks, float* vs, int heads, int d, void* q_out, int64_t ldq,
                               hipStream_t st) {
     AppendParams p{ix, qkv, ld, rope, rope_len, positions, k, v, ks, vs, q_out, ldq, heads_q, heads, rot, interleaved,
-                   kv_max_touched(ix.max_q, ix.page_size), 0};
+                   kv_max_touched(ix.max_q, ix.page_size), 0, 0};
     return dtype == F16 ? launch_dt<F16>(p, d, st) : launch_dt<BF16>(p, d, st);
 }
 

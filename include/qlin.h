@@ -500,7 +500,9 @@ typedef struct {
  *   infinity or a NaN does not enter the scale; they are stored as +-127 and 0.
  *   Calling again with the same arguments changes nothing.
  * Preconditions: tokens >= 0; heads_q a multiple of cache->heads; ld and ldq
- * multiples of 8; outputs (q_out and the cache) overlap no input.  One launch.
+ * multiples of 8; outputs (q_out and the cache) overlap no input; at most 2^29
+ * (page, head) pairs and 2^31 x 16 q values a sequence in one call (more than
+ * fits a device).  One launch.
  *
  * qlin_rope_table -- table[p][i] = cos(angle), table[p][rot_dim / 2 + i] =
  * sin(angle), angle = p / stretch * base^(-2 i / rot_dim) in float64 (far
