@@ -18,7 +18,15 @@
 // float64 too, so no fp32 row can overflow it.
 //
 // A row is held by g lanes (a power of two), lane t holding the 8 values from
-// 8 (c g + t) for chunk c.
+// 8 (c g + t) for chunk c: one chunk up to 8192 values.  More chunks a lane
+// (fewer lanes to reduce over) leave too few waves to cover the loads: at
+// 52224 x 2048 one, two and four chunks take 190, 194 and 222 us.
+//
+// Bound by vector issue at the backbone's widths: 53 instructions per 64 values
+// with a Hadamard of 128, 151 us of the 168 us that 52224 x 2048 bf16 rows take
+// (749 MB: 4.5 TB/s; a copy moves 5.1).
+
+#include <cmath>
 
 #include "code_pack.h"
 #include "device_common.h"
@@ -38,6 +46,7 @@ struct NormParams {
     int g;               // lanes per row
     int had_block;       // 0/1: none
     int bits;            // 8, 4 or 6; 0: float output
+    double unscale;      // 1 / (qmax sqrt b)
     void* q;             // codes, or y
     float* scale;
 };
@@ -57,6 +66,14 @@ __device__ __forceinline__ double lane_xor_d(double v) {
     return __hiloint2double(lane_xor_i<D>(__double2hiint(v)), lane_xor_i<D>(__double2loint(v)));
 }
 
+// The double a DPP pattern brings (the reductions' steps: the two quad swaps,
+// then the half-row and row mirrors, which meet the other half's result).
+template <int CTRL>
+__device__ __forceinline__ double across(double v) {
+    return __hiloint2double(__builtin_amdgcn_mov_dpp(__double2hiint(v), CTRL, 0xF, 0xF, false),
+                            __builtin_amdgcn_mov_dpp(__double2loint(v), CTRL, 0xF, 0xF, false));
+}
+
 template <int D, int NCH>
 __device__ __forceinline__ void xlane_stage_d(double (&v)[NCH][8], int lane) {
     const double sgn = (lane & D) ? -1.0 : 1.0;
@@ -73,14 +90,25 @@ __device__ __forceinline__ float round_to(float f) {
     else return f;
 }
 
-template <int DT, int NCH, int TPB, bool QUANT>
+// max(m, |a|) in one instruction (fmax first quiets operands the compiler does
+// not know to be canonical; a NaN operand is ignored either way).
+__device__ __forceinline__ double max_abs(double m, double a) {
+    double r;
+    asm("v_max_f64 %0, %1, |%2|" : "=v"(r) : "v"(m), "v"(a));
+    return r;
+}
+
+// HB: the Hadamard block at compile time (1: none), or 0 to take it from the
+// arguments.  A known block leaves the transform without branches, whose joins
+// cost a move a value and stage.
+template <int DT, int NCH, int TPB, bool QUANT, int HB>
 __global__ __launch_bounds__(TPB) void add_rmsnorm_kernel(NormParams p) {
     constexpr int ES = DT == F32 ? 4 : 2;
     constexpr int NW = TPB / 64;
     __shared__ double red[2][NW];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int g = p.g, t = tid & (g - 1);
-    const int b = p.had_block > 1 ? p.had_block : 1;
+    const int b = HB > 0 ? HB : p.had_block > 1 ? p.had_block : 1;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * (TPB / g) + tid / g;
     const bool row_ok = row < p.m;
     const int64_t rr = row_ok ? row : p.m - 1;
@@ -148,23 +176,23 @@ __global__ __launch_bounds__(TPB) void add_rmsnorm_kernel(NormParams p) {
 #pragma unroll
         for (int c = 0; c < NCH; ++c)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) top = fmax(top, fabs(v[c][e]));
+            for (int e = 0; e < 8; ++e) top = max_abs(top, v[c][e]);
     }
 
     // the row's sum of squares and maximum: lanes (g >= 32), then waves
-    ss += lane_xor_d<1>(ss);
-    ss += lane_xor_d<2>(ss);
-    ss += lane_xor_d<4>(ss);
-    ss += lane_xor_d<8>(ss);
+    ss += across<0xB1>(ss);
+    ss += across<0x4E>(ss);
+    ss += across<0x141>(ss);
+    ss += across<0x140>(ss);
     ss += lane_xor_d<16>(ss);
     if (g > 32) ss += lane_xor_d<32>(ss);
     if constexpr (QUANT) {
-        top = fmax(top, lane_xor_d<1>(top));
-        top = fmax(top, lane_xor_d<2>(top));
-        top = fmax(top, lane_xor_d<4>(top));
-        top = fmax(top, lane_xor_d<8>(top));
-        top = fmax(top, lane_xor_d<16>(top));
-        if (g > 32) top = fmax(top, lane_xor_d<32>(top));
+        top = max_abs(top, across<0xB1>(top));
+        top = max_abs(top, across<0x4E>(top));
+        top = max_abs(top, across<0x141>(top));
+        top = max_abs(top, across<0x140>(top));
+        top = max_abs(top, lane_xor_d<16>(top));
+        if (g > 32) top = max_abs(top, lane_xor_d<32>(top));
     }
     if (g > 64) {
         if (lane == 0) {
@@ -181,19 +209,26 @@ __global__ __launch_bounds__(TPB) void add_rmsnorm_kernel(NormParams p) {
         }
     }
     if (!row_ok) return;
-    const double rms = sqrt(ss / static_cast<double>(p.k) + static_cast<double>(p.eps));
 
     if constexpr (QUANT) {
         const double qmax = p.bits == 8 ? 127.0 : 7.0;
         if (t == 0) {
-            const double root = sqrt(static_cast<double>(b));
+            const double rms = sqrt(ss / static_cast<double>(p.k) + static_cast<double>(p.eps));
             // a row of zeros has scale 0 (also at eps = 0)
-            p.scale[row] = ss == 0.0 ? 0.f : static_cast<float>(top / (rms * root * qmax));
+            p.scale[row] = ss == 0.0 ? 0.f : static_cast<float>(top * p.unscale / rms);
         }
-        const double inv = top > 0.0 ? qmax / top : 0.0;
+        // qmax / top to a few 2^-52: the reciprocal's 2^-20 or better, squared twice
+        // (a subnormal or zero top, or one whose reciprocal is, takes the quotients)
+        double inv = 0.0;
+        const bool fast = top > 1e-290 && top < 1e290;
+        if (fast) {
+            inv = __builtin_amdgcn_rcp(top);
+            inv = fma(fma(-top, inv, 1.0), inv, inv);
+            inv = fma(fma(-top, inv, 1.0), inv, inv) * qmax;
+        }
         // fma(v, inv, M) with M = 1.5 * 2^52 rounds the product to an integer
         // once, half to even, and leaves it in the low mantissa bits; |v| <= top
-        // keeps it on the grid.  inv and the product are off by 2^-45 at most
+        // keeps it on the grid.  The product is off by 2^-43 at most
         // for codes up to 127: a residual that close to a half (the window is
         // far wider) is decided by the quotient itself.
         constexpr double M = 6755399441055744.0;
@@ -204,10 +239,10 @@ __global__ __launch_bounds__(TPB) void add_rmsnorm_kernel(NormParams p) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const double qb = fma(v[c][e], inv, M);
-                worst = fmax(worst, fabs(fma(v[c][e], inv, M - qb)));
+                worst = max_abs(worst, fma(v[c][e], inv, M - qb));
                 cb[e] = static_cast<uint32_t>(__double2loint(qb));
             }
-            if (worst >= 0.5 - 1e-9) {
+            if (worst >= 0.5 - 1e-9 || !fast) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     cb[e] = static_cast<uint32_t>(
@@ -216,6 +251,7 @@ __global__ __launch_bounds__(TPB) void add_rmsnorm_kernel(NormParams p) {
             if (ok[c]) store8_codes(p.bits, cb, p.q, row, p.k, col[c], lane);
         }
     } else {
+        const double rms = sqrt(ss / static_cast<double>(p.k) + static_cast<double>(p.eps));
         const float inv = ss == 0.0 ? 0.f : static_cast<float>(1.0 / rms);
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
@@ -232,10 +268,17 @@ template <int DT, int NCH, int TPB>
 hipError_t launch_tpb(const NormParams& p, hipStream_t st) {
     const int64_t rpb = TPB / p.g;
     const dim3 grid(static_cast<unsigned>((p.m + rpb - 1) / rpb));
-    if (p.bits)
-        add_rmsnorm_kernel<DT, NCH, TPB, true><<<grid, TPB, 0, st>>>(p);
+    constexpr bool known = DT != F32 && NCH == 1;   // 16-bit rows of up to 8192 values
+    if (!p.bits)
+        add_rmsnorm_kernel<DT, NCH, TPB, false, 1><<<grid, TPB, 0, st>>>(p);
+    else if (known && p.had_block <= 1)
+        add_rmsnorm_kernel<DT, NCH, TPB, true, known ? 1 : 0><<<grid, TPB, 0, st>>>(p);
+    else if (known && p.had_block == 64)
+        add_rmsnorm_kernel<DT, NCH, TPB, true, known ? 64 : 0><<<grid, TPB, 0, st>>>(p);
+    else if (known && p.had_block == 128)
+        add_rmsnorm_kernel<DT, NCH, TPB, true, known ? 128 : 0><<<grid, TPB, 0, st>>>(p);
     else
-        add_rmsnorm_kernel<DT, NCH, TPB, false><<<grid, TPB, 0, st>>>(p);
+        add_rmsnorm_kernel<DT, NCH, TPB, true, 0><<<grid, TPB, 0, st>>>(p);
     return hipGetLastError();
 }
 
@@ -256,7 +299,8 @@ hipError_t launch_dt(NormParams p, hipStream_t st) {
 hipError_t launch_add_rmsnorm(const void* x, int dtype, int64_t m, int64_t k, int64_t ldx, const void* res,
                               int64_t ldr, const float* w, float eps, int had_block, int bits, void* res_out,
                               void* q, float* scale, hipStream_t st) {
-    NormParams p{x, res, res_out, w, m, k, ldx, ldr, eps, 0, had_block, bits, q, scale};
+    const double unscale = 1.0 / ((bits == 8 ? 127.0 : 7.0) * std::sqrt(had_block > 1 ? had_block : 1));
+    NormParams p{x, res, res_out, w, m, k, ldx, ldr, eps, 0, had_block, bits, unscale, q, scale};
     switch (dtype) {
         case F16: return launch_dt<F16>(p, st);
         case BF16: return launch_dt<BF16>(p, st);
