@@ -27,7 +27,8 @@ Side legs (one JSON object each): the same sweep with the W4A4 codes in FP6
 E2M3 storage (the FP6 matrix-core GEMMs, bit-identical results), the sweep at
 M = 6528 and 816, the
 backbone MLP block at M = 816 (split-K down GEMM with its workspace), the W4A8
-GEMM, the 7B-decoder projections at M = 256 W8A8 (HBM-bound), the action
+GEMM, the 7B-decoder projections at M = 256 W8A8 (HBM-bound), one 7B-decoder
+layer over the paged int8 cache (1 and 256 single-token sequences), the action
 expert over 10 denoising steps (W4A4, per-step static tables, W4A16; warm and
 cold weights), the single W4A4 linear, the batch-1 W4A16 GEMV of a 7B-decoder
 layer (cold weights), the composite rotation, a per-launch breakdown of one sweep layer, the shader
@@ -671,6 +672,49 @@ def gemv_leg(dev, reps=5):
             "shapes": shapes}
 
 
+def decoder_layer_leg(dev, m, context=816, reps=5):
+    """One 7B-decoder layer (W8A8, int8 paged cache) at m sequences of one new
+    token each behind `context` - 1 cached ones: us per layer from a captured
+    step, and us per launch from events around eager launches.  The cache holds
+    the codes of random tokens; the weights (202 MB) fit the Infinity Cache, so
+    they are not counted as HBM traffic."""
+    import torch
+
+    import bit_ptq_vla_amd as q
+    from bit_ptq_vla_amd import synth
+    from bit_ptq_vla_amd.workload import DecoderLayer
+
+    page = 64
+    cols = -(-context // page)
+    layer = DecoderLayer(dev, m, m * cols, page)
+    layer.cache.k.random_(-127, 128)
+    layer.cache.v.random_(-127, 128)
+    layer.cache.k_scale.fill_(0.02)
+    layer.cache.v_scale.fill_(0.02)
+
+    def i32(t):
+        return t.to(torch.int32).to(dev)
+
+    batch = q.KvBatch(i32(torch.randperm(m * cols).reshape(m, cols)), i32(torch.arange(m + 1)),
+                      i32(torch.full((m,), context)), max_q=1, max_kv=context)
+    x, res = [synth.device_normal(3, f"decoder_layer/{n}/m{m}", (m, layer.hidden), dev) for n in "xr"]
+    # the step adds to the residual: a large one keeps its scale over the replays
+    res *= 100
+    work = q.kv_attention_workspace(layer.cache, batch, layer.heads)
+    g = _graph(lambda: layer.step(x, res, batch, attn_workspace=work))
+    us = _median_us(g.replay, reps)
+    evs = [[torch.cuda.Event(enable_timing=True) for _ in range(11)] for _ in range(reps)]
+    for e in evs:
+        layer.step(x, res, batch, attn_workspace=work, evs=e)
+    torch.cuda.synchronize()
+    split = {name: round(statistics.median(e[i].elapsed_time(e[i + 1]) for e in evs) * 1e3, 2)
+             for i, name in enumerate(layer.LAUNCHES)}
+    kv_bytes = 2 * m * context * layer.hidden
+    return {"m": m, "context": context, "us_per_layer": round(us, 2), "launch_us": split,
+            "attention_kv_bytes": kv_bytes,
+            "attention_kv_GBps": round(kv_bytes / (split["attention"] * 1e-6) / 1e9, 1)}
+
+
 def action_expert_leg(dev, reps=5):
     """The action expert's projections at M = 50 over 10 denoising steps:
     W4A4 (b = 64, with activation quantization), W4A4 with per-step static
@@ -859,6 +903,8 @@ def main():
         out["w4a4_e2m3"] = leg("w4a4_e2m3", lambda: e2m3_leg(dev))
         log("bench: 7B-decoder M = 256 W8A8 leg")
         out["decoder7b_m256_w8a8"] = leg("decoder7b_m256_w8a8", lambda: decoder_m256_leg(dev))
+        log("bench: 7B-decoder layer over the paged int8 cache (M = 1 and 256)")
+        out["decoder7b_layer_w8a8"] = leg("decoder7b_layer_w8a8", lambda: [decoder_layer_leg(dev, n) for n in (1, 256)])
         log("bench: action expert leg (M = 50, 10 steps)")
         out["action_expert"] = leg("action_expert", lambda: action_expert_leg(dev))
         log("bench: single linear leg")

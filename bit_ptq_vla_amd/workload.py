@@ -414,3 +414,102 @@ class ActionExpert:
             for pr, xs, wq16, ws16, y in self.w4a16:
                 q.qlin_gemv_w4a16(xs[t], wq16, ws16, out=y)
 
+
+
+class DecoderLayer:
+    """One decoder layer over a paged int8 cache, W8A8 (per token / per
+    channel, no fold, no rotation), at the 7B-decoder shapes by default:
+
+      residual + RMS norm + int8 quantizer, q|k|v GEMM, rotary append to the
+      cache, attention over it, int8 quantizer, o GEMM, residual + RMS norm +
+      int8 quantizer, gate|up GEMM, GeGLU + int8 quantizer, down GEMM.
+
+    The residual rows are updated in place; a layer's output is what the next
+    layer's first norm adds to them.  Every buffer is allocated here for up to
+    m_max tokens, so that step() can be captured into a graph.
+    """
+
+    LAUNCHES = ("norm_attn", "qkv", "append", "attention", "quant_o", "o", "norm_mlp", "gate_up", "quant_down", "down")
+
+    def __init__(self, dev, m_max: int, pages: int, page_size: int = 64, positions: int = 4096, hidden: int = 4096,
+                 heads: int = 32, heads_kv: int = 32, head_dim: int = 128, ffn: int = 11008, dtype: str = "f16",
+                 seed: int = 3):
+        import torch
+
+        import bit_ptq_vla_amd as q
+        from bit_ptq_vla_amd import synth
+
+        self.q, self.dev = q, dev
+        self.hidden, self.heads, self.ffn = hidden, heads, ffn
+        tdt = {"f16": torch.float16, "bf16": torch.bfloat16}[dtype]
+        width = (heads + 2 * heads_kv) * head_dim
+        self.shapes = {"qkv": (width, hidden), "o": (hidden, heads * head_dim), "gate_up": (2 * ffn, hidden),
+                       "down": (hidden, ffn)}
+        self.w = {}
+        for name, (n, k) in self.shapes.items():
+            w = synth.device_normal(seed, f"decoder_layer/{name}/{n}x{k}", (n, k), dev, std=k ** -0.5)
+            self.w[name] = q.qlin_quantize_weights(w, bits=8)
+            del w
+        self.gamma = [1.0 + synth.device_normal(seed, f"decoder_layer/gamma{i}/{hidden}", (hidden,), dev, std=0.1,
+                                                dtype="f32") for i in range(2)]
+        self.cache = q.KvCache.empty(pages, page_size, heads_kv, head_dim, dev)
+        self.rope = q.qlin_rope_table(positions, head_dim, device=dev)
+
+        def codes(k):
+            return (torch.empty((m_max, k), dtype=torch.int8, device=dev),
+                    torch.empty(m_max, dtype=torch.float32, device=dev))
+
+        def rows(n):
+            return torch.empty((m_max, n), dtype=tdt, device=dev)
+
+        self.a, self.qkv, self.qr, self.ctx = codes(hidden), rows(width), rows(heads * head_dim), rows(heads * head_dim)
+        self.cq, self.yo, self.b = codes(heads * head_dim), rows(hidden), codes(hidden)
+        self.gu, self.hq, self.y = rows(2 * ffn), codes(ffn), rows(hidden)
+        self._ws = {}
+
+    def workspace(self, m: int) -> dict:
+        """Split-K scratch of the GEMMs at m tokens."""
+        if m not in self._ws:
+            q = self.q
+            self._ws[m] = {name: q.gemm_workspace(q.QLIN_W8A8, m, n, k, self.dev)
+                           for name, (n, k) in self.shapes.items()}
+        return self._ws[m]
+
+    def step(self, x, residual, batch, attn_workspace=None, evs=None):
+        """residual [m][hidden] += x (the previous layer's output) and, behind
+        the attention, the attention branch; returns the MLP branch [m][hidden]
+        (a buffer of this layer).  batch holds the m new tokens; evs: 11 events
+        around the launches."""
+        q = self.q
+        m = x.shape[0]
+        ws = self.workspace(m)
+        mark = (lambda i: None) if evs is None else (lambda i: evs[i].record())
+
+        def gemm(name, codes, out):
+            wq, wsc = self.w[name]
+            q.qlin_gemm_w8a8(codes[0], codes[1], wq, wsc, self.shapes[name][1], out=out, workspace=ws[name])
+
+        a, cq, b, hq = [(t[:m], s[:m]) for t, s in (self.a, self.cq, self.b, self.hq)]
+        qkv, qr, ctx, yo, gu, y = [t[:m] for t in (self.qkv, self.qr, self.ctx, self.yo, self.gu, self.y)]
+        mark(0)
+        q.qlin_add_rmsnorm_quant(x, self.gamma[0], residual, bits=8, residual_out=residual, out=a)
+        mark(1)
+        gemm("qkv", a, qkv)
+        mark(2)
+        q.qlin_rope_append_kv(qkv, self.cache, batch, self.heads, self.rope, q_out=qr)
+        mark(3)
+        q.qlin_kv_attention(qr, self.cache, batch, self.heads, out=ctx, workspace=attn_workspace)
+        mark(4)
+        q.qlin_rotate_quant_act(ctx, bits=8, out=cq)
+        mark(5)
+        gemm("o", cq, yo)
+        mark(6)
+        q.qlin_add_rmsnorm_quant(yo, self.gamma[1], residual, bits=8, residual_out=residual, out=b)
+        mark(7)
+        gemm("gate_up", b, gu)
+        mark(8)
+        q.qlin_rotate_quant_act(gu, k=self.ffn, bits=8, pre=q.QLIN_PRE_GEGLU, out=hq)
+        mark(9)
+        gemm("down", hq, y)
+        mark(10)
+        return y
