@@ -675,6 +675,9 @@ class KvBatch:
     def __init__(self, page_table: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, max_q: int, max_kv: int,
                  prefix_len: Optional[torch.Tensor] = None):
         batch = kv_len.numel()
+        for name, n in (("max_q", max_q), ("max_kv", max_kv)):
+            if not 0 <= n <= 0x7FFFFFFF:
+                raise ValueError(f"{name} must be in 0 .. 2^31 - 1")
         for name, t, n in (("page_table", page_table, 0), ("q_start", q_start, batch + 1), ("kv_len", kv_len, batch),
                            ("prefix_len", prefix_len, batch)):
             if t is None:

@@ -174,7 +174,16 @@ KvAttnPlan plan_kv_attention(int64_t batch, int64_t max_q, int64_t max_kv, int h
                              bool allow_split) {
     KvAttnPlan p;
     const int64_t rows = max_q * (heads_q / heads), cus = device_cus();
-    p.many = rows > 64;
+    // Blocks of 128 (256-wide heads) or 256 rows pay once the call is long, counted
+    // in 16-row tiles times keys, and fill at least a quarter of theirs.  Measured,
+    // us for 16-row blocks / for these, bf16:
+    //   64 wide:   2.7 M (8 x 8 heads, 512 rows) 39 / 36, 4.5 M (32 x 8, 128) 86 / 76, 1.1 M (8 x 8, 256) 21 / 30
+    //   128 wide:  0.5 M (8 x 8 heads, 128 rows) 24 / 26, 0.8 M (192 rows) 27 / 30, 1.1 M (256) 37 / 36,
+    //              4.5 M (32 x 8, 128) 159 / 95, 2.7 M (8 x 8 prompts of 816) 66 / 40
+    //   256 wide:  0.06 M (8 heads, 128 rows) 17 / 31, 0.2 M (8 x 8, 64) 36 / 33, 1.1 M (32 x 8, 64) 107 / 71
+    // and with less than a quarter: 82 / 87 (128 wide, 32 x 8 heads, 64 rows), 57 / 70 (256 wide, 32 rows).
+    const int64_t least = d == 256 ? 1 << 17 : d == 128 ? 3 << 18 : 5 << 19;
+    p.many = rows > (d == 256 ? 32 : 64) && batch * heads * ((rows + 15) / 16) * max_kv > least;
     const int64_t per = !p.many ? 16 : d == 256 ? 128 : 256;
     p.row_tiles = static_cast<int>((rows + per - 1) / per);
     const int64_t units = batch * heads * p.row_tiles;

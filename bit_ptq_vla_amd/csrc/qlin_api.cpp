@@ -228,6 +228,9 @@ qlin_status kv_check(const qlin_kv_cache* c, const qlin_kv_batch* b, int64_t tok
     return QLIN_OK;
 }
 
+// Blocks of 512 threads that a launch (of 2^32 threads) holds.
+constexpr int64_t kMaxAttnBlocks = (1 << 23) - 1;
+
 // The call's index arrays as spans (4 of them).
 void kv_index_spans(const qlin_kv_cache* c, const qlin_kv_batch* b, Span* s) {
     const int64_t n = b->batch, used = (static_cast<int64_t>(b->max_kv) + c->page_size - 1) / c->page_size;
@@ -256,6 +259,9 @@ qlin_status add_rmsnorm(const void* x, qlin_dtype dt, int64_t m, int64_t k, int6
     if (m < 0 || m > 0x7FFFFFFF || k < 8 || (k % 8) != 0 || k > kMaxRowK) return QLIN_ERR_SHAPE;
     if ((ldx % 8) != 0 || ldx < k) return QLIN_ERR_SHAPE;
     if ((res || res_out) && ((ldr % 8) != 0 || ldr < k)) return QLIN_ERR_SHAPE;
+    int64_t row_threads = 32;      // of the 2^32 a launch holds
+    while (row_threads < 1024 && row_threads * 8 < k) row_threads *= 2;
+    if (m * row_threads > 0xFFFFFFFFLL) return QLIN_ERR_SHAPE;
     if (!bits_k_ok(bits, k)) return QLIN_ERR_SHAPE;
     if (had_block > 1 && (k % had_block) != 0) return QLIN_ERR_SHAPE;
     if (!aligned16(x) || !aligned16(res) || !aligned16(res_out) || !aligned16(w) || !aligned16(q) || !aligned16(scale))
@@ -607,7 +613,10 @@ qlin_status qlin_rope_append_kv(const void* qkv, qlin_dtype dtype, int64_t token
     const int64_t touched = qlin::kv_max_touched(batch->max_q, cache->page_size);
     if (touched > 0 && static_cast<int64_t>(batch->batch) * cache->heads > (1LL << 29) / touched) return QLIN_ERR_SHAPE;
     const int64_t q_tasks = static_cast<int64_t>(batch->max_q) * heads_q * (d / 16);
-    if (q_tasks > (1LL << 31) || batch->batch * (q_tasks / 64 + 1) > (1LL << 30)) return QLIN_ERR_SHAPE;
+    if (q_tasks > (1LL << 31)) return QLIN_ERR_SHAPE;
+    // (a launch holds 2^32 threads, and a block at most 512)
+    const int64_t threads = touched * cache->heads * 2 * 512 + q_tasks + 512;
+    if (batch->batch > 0 && threads > 0xFFFFFFFFLL / batch->batch) return QLIN_ERR_SHAPE;
     const int64_t codes = cache->pages * cache->heads * cache->page_size * d, scales = cache->pages * cache->heads * 4;
     const Span outs[5] = {{cache->k, codes}, {cache->v, codes}, {cache->k_scale, scales}, {cache->v_scale, scales},
                           {q_out, tokens > 0 ? ((tokens - 1) * ldq + heads_q * d) * 2 : 0}};
@@ -628,7 +637,7 @@ int64_t qlin_kv_attention_workspace_bytes(int32_t heads_q, const qlin_kv_cache* 
     if (kv_check(cache, batch, 0, heads_q) != QLIN_OK) return -1;
     const qlin::KvAttnPlan plan = qlin::plan_kv_attention(batch->batch, batch->max_q, batch->max_kv, heads_q,
                                                           cache->heads, cache->head_dim, true);
-    return plan.blocks > 0x7FFFFFFF ? -1 : plan.ws_bytes;
+    return plan.blocks > kMaxAttnBlocks ? -1 : plan.ws_bytes;
 }
 
 qlin_status qlin_kv_attention(const void* q, qlin_dtype dtype, int64_t tokens, int64_t ldq, int32_t heads_q,
@@ -646,8 +655,7 @@ qlin_status qlin_kv_attention(const void* q, qlin_dtype dtype, int64_t tokens, i
     if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return QLIN_ERR_ALIGN;
     const qlin::KvAttnPlan plan = qlin::plan_kv_attention(batch->batch, batch->max_q, batch->max_kv, heads_q,
                                                           cache->heads, cache->head_dim, workspace != nullptr);
-    if (plan.blocks > 0x7FFFFFFF || static_cast<int64_t>(batch->batch) * batch->max_q * heads_q > (1LL << 33))
-        return QLIN_ERR_SHAPE;
+    if (plan.blocks > kMaxAttnBlocks) return QLIN_ERR_SHAPE;
     if (workspace && workspace_bytes < plan.ws_bytes) return QLIN_ERR_WORKSPACE;
     const int64_t codes = cache->pages * cache->heads * cache->page_size * cache->head_dim;
     const int64_t scales = cache->pages * cache->heads * 4;
@@ -668,7 +676,8 @@ qlin_status qlin_rope_table(float* table, int64_t positions, int32_t rot_dim, do
                             void* stream) {
     if (!table) return QLIN_ERR_NULL;
     if (!(base > 0.0) || !(base < 1e300) || !(stretch > 0.0) || !(stretch < 1e300)) return QLIN_ERR_UNSUPPORTED;
-    if (positions < 0 || positions > 0x7FFFFFFF || rot_dim < 2 || rot_dim % 2 != 0 || rot_dim > 1024)
+    if (positions < 0 || positions > 0x7FFFFFFF || rot_dim < 2 || rot_dim % 2 != 0 || rot_dim > 1024 ||
+        positions * (rot_dim / 2) > 0xFFFFFF00LL)
         return QLIN_ERR_SHAPE;
     if (!aligned16(table)) return QLIN_ERR_ALIGN;
     if (positions == 0) return QLIN_OK;

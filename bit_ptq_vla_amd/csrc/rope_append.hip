@@ -24,8 +24,10 @@
 // and 16s + 8).  A V task is 8 dimensions of four tokens, whose codes are four
 // bytes each of the keys-first page.
 //
-// Bound by memory for prompts: q|k|v read once, q written, one byte a key and
-// value (measured figures at the launch).
+// Prompts: q|k|v read once, q written, one byte a key and value.  52224 tokens of
+// 8 + 8 + 8 heads of 256 (844 MB) take 266 us, 3.2 TB/s; q alone 69, k alone
+// about 95 of it: its 32 bytes of values need 64 of cosines and sines, which come
+// from L2.  A decode step is latency (64 requests of 8 heads: 7.4 us a call).
 
 #include "code_pack.h"
 #include "device_common.h"
@@ -188,6 +190,62 @@ __device__ __forceinline__ bool codes_f32(const float* v, float inv, uint32_t* c
         cb[e] = __float_as_uint(qb);
     }
     return worst < 0.5f - 6e-5f;
+}
+
+// rne(c s_old / s_new) of a word's four codes.  fp32 leaves c s_old / s_new
+// within 127 x 2^-23 (1.6e-5); what comes nearer than that to a half-integer
+// is decided in float64, where c s_old is exact.
+__device__ __forceinline__ uint32_t rescale4(uint32_t was, float ratio, double s_old, double s_new) {
+    float c[4];
+    uint32_t cb[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] = static_cast<float>(static_cast<int8_t>(was >> (8 * e)));
+    if (!(ratio >= 0.f && ratio <= 1.f)) {              // what no append leaves in a scale
+#pragma unroll 1
+        for (int e = 0; e < 4; ++e) cb[e] = static_cast<uint32_t>(code_of(c[e] * s_old, s_new));
+    } else if (!codes_f32<4>(c, ratio, cb)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) cb[e] = static_cast<uint32_t>(code_near(c[e] * s_old, s_new, c[e] * ratio));
+    }
+    return __builtin_amdgcn_perm(cb[1], cb[0], 0x0C0C0400u) | __builtin_amdgcn_perm(cb[3], cb[2], 0x04000C0Cu);
+}
+
+// A page's `held` earlier codes follow its scale: 16 codes to a thread, four
+// such loads under way together.  K's are contiguous; of a V row's only the
+// first `held` bytes are the page's.
+template <int TPB, int D>
+__device__ __forceinline__ void rescale_page(int8_t* base, bool is_v, int held, int ps, double s_old, double s_new) {
+    const float ratio = static_cast<float>(s_old) / static_cast<float>(s_new);
+    const int row = is_v ? (held + 15) >> 4 : 1, n = is_v ? row * D : held * (D / 16);
+#pragma unroll 1
+    for (int i0 = threadIdx.x; i0 < n; i0 += 4 * TPB) {
+        uint4 was[4];
+        int off[4], at[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * TPB < n ? i0 + u * TPB : i0, r = is_v ? i / row : 0;
+            off[u] = is_v ? (i - r * row) * 16 : 0;
+            at[u] = is_v ? r * ps + off[u] : 16 * i;
+            was[u] = *reinterpret_cast<const uint4*>(base + at[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (i0 + u * TPB >= n) break;
+            const uint32_t w[4] = {was[u].x, was[u].y, was[u].z, was[u].w};
+            uint32_t now[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) now[e] = rescale4(w[e], ratio, s_old, s_new);
+            if (!is_v || off[u] + 16 <= held) {
+                *reinterpret_cast<uint4*>(base + at[u]) = make_uint4(now[0], now[1], now[2], now[3]);
+            } else {
+#pragma unroll 1
+                for (int e = 0; off[u] + e < held; ++e) {
+                    const uint32_t word = e < 8 ? e < 4 ? now[0] : now[1] : e < 12 ? now[2] : now[3];
+                    base[at[u] + e] = static_cast<int8_t>(word >> (8 * (e & 3)));
+                }
+            }
+        }
+    }
 }
 
 template <int TPB>
@@ -379,27 +437,7 @@ __device__ __forceinline__ void store_page(const AppendParams& p, uint32_t unit)
             }
         }
     }
-    // the page's earlier codes follow its scale
-    if (o_lo > 0 && s_new != s_old) {
-        const double so = s_old;
-        const int words = is_v ? (o_lo + 3) >> 2 : o_lo * (D / 4);
-        for (int i = tid; i < (is_v ? words * D : words); i += TPB) {
-            const int off = is_v ? i % words * 4 : 0;
-            int8_t* at = is_v ? base + i / words * ps + off : base + 4 * i;
-            const uint32_t was = *reinterpret_cast<const uint32_t*>(at);
-            uint32_t now = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int c = static_cast<int8_t>(was >> (8 * e));
-                now |= (static_cast<uint32_t>(code_of(static_cast<double>(c) * so, s)) & 0xFFu) << (8 * e);
-            }
-            if (!is_v || off + 4 <= o_lo) {
-                *reinterpret_cast<uint32_t*>(at) = now;
-            } else {
-                for (int e = 0; off + e < o_lo; ++e) at[e] = static_cast<int8_t>(now >> (8 * e));
-            }
-        }
-    }
+    if (o_lo > 0 && s_new != s_old) rescale_page<TPB, D>(base, is_v, o_lo, ps, s_old, s_new);
 }
 
 template <int DT, int D, int TPB>

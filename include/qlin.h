@@ -187,7 +187,8 @@ qlin_status qlin_rotate_quant_act(const void* x, qlin_dtype x_dtype, int64_t m, 
  *   weight    float[k].  eps >= 0, finite.
  *   had_block, bits, xq, x_scale: as qlin_rotate_quant_act.
  * Preconditions: m >= 0; 8 <= k <= 32768, k % 8 == 0 (k % 128 == 0 for E2M3);
- * k % had_block == 0; ldx, ldr % 8 == 0 and >= k.  One launch; no workspace.
+ * k % had_block == 0; ldx, ldr % 8 == 0 and >= k; m below 2^32 / 32 (k <= 256)
+ * to 2^32 / 1024 (k > 4096).  One launch; no workspace.
  */
 qlin_status qlin_add_rmsnorm_quant(const void* x, qlin_dtype x_dtype, int64_t m, int64_t k, int64_t ldx,
                                    const void* residual, int64_t ldr, const float* weight, float eps,
@@ -459,7 +460,8 @@ qlin_status qlin_gemv_w4a16(const void* x, const void* wq, const void* w_scale, 
  *   and a page number outside the pool counts as no page (its tokens are not
  *   stored, its keys not seen).  A sequence may have no new tokens or no
  *   tokens at all; rows of no sequence are left as they are.  Sequences may
- *   share pages that they only read; a page that a call writes belongs to one.
+ *   share pages that they only read; a page that a call writes belongs to one
+ *   and stands in its row once.
  */
 typedef struct {
     int8_t* k;
@@ -500,9 +502,9 @@ typedef struct {
  *   infinity or a NaN does not enter the scale; they are stored as +-127 and 0.
  *   Calling again with the same arguments changes nothing.
  * Preconditions: tokens >= 0; heads_q a multiple of cache->heads; ld and ldq
- * multiples of 8; outputs (q_out and the cache) overlap no input; at most 2^29
- * (page, head) pairs and 2^31 x 16 q values a sequence in one call (more than
- * fits a device).  One launch.
+ * multiples of 8; outputs (q_out and the cache) overlap no input; batch x (1024
+ * heads x (pages max_q tokens can touch) + heads_q max_q head_dim / 16) below
+ * 2^32, the threads of a launch.  One launch.
  *
  * qlin_rope_table -- table[p][i] = cos(angle), table[p][rot_dim / 2 + i] =
  * sin(angle), angle = p / stretch * base^(-2 i / rot_dim) in float64 (far
@@ -536,7 +538,8 @@ qlin_status qlin_rope_table(float* table, int64_t positions, int32_t rot_dim, do
  * qlin_kv_attention_workspace_bytes: 0 where the call takes no split, -1 for
  * arguments the call would refuse.
  * Preconditions: tokens >= 0; heads_q a multiple of cache->heads; ldq, ldo
- * multiples of 8; sm_scale finite; softcap >= 0, finite; out overlaps no input.
+ * multiples of 8; sm_scale finite; softcap >= 0, finite; out overlaps no input;
+ * batch x heads x ceil(max_q x heads_q / heads / 16) below 2^23.
  */
 int64_t qlin_kv_attention_workspace_bytes(int32_t heads_q, const qlin_kv_cache* cache, const qlin_kv_batch* batch);
 qlin_status qlin_kv_attention(const void* q, qlin_dtype dtype, int64_t tokens, int64_t ldq, int32_t heads_q,

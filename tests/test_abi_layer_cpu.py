@@ -81,6 +81,29 @@ def test_add_rmsnorm_empty_is_ok(lib):
     assert norm(lib, m=0) == q.QLIN_OK
 
 
+def test_more_threads_than_a_launch_holds_are_refused(lib):
+    """2^32 threads: 32 to 1024 a row of the norm, 512 a (page, head) and one to
+    16 values of q in the append, 512 a block of the attention."""
+    big = 1 << 62                           # (any overlap of the fake spans comes later)
+    for k, rows in ((64, 1 << 27), (4096, 1 << 23), (4104, 1 << 22), (32768, 1 << 22)):
+        assert norm_quant(lib, m=rows, k=k, ldx=k, res=None, ro=None, b=0, x=big) == q.QLIN_ERR_SHAPE
+        assert norm(lib, m=rows, k=k, ldx=k, res=None, ro=None, x=big) == q.QLIN_ERR_SHAPE
+    wide = cache(heads=32, d=128)
+    many = batch(n=1 << 16, max_q=8192, max_kv=64)
+    assert append(lib, c=wide, b=many, hq=32, ld=96 * 128, ldq=32 * 128) == q.QLIN_ERR_SHAPE
+    deep = batch(n=1 << 18, max_q=16, max_kv=64)
+    assert attention(lib, c=wide, b=deep, hq=32, ldq=32 * 128, ldo=32 * 128) == q.QLIN_ERR_SHAPE
+    assert lib.qlin_kv_attention_workspace_bytes(32, *refs(wide, deep)) == -1
+    assert lib.qlin_rope_table(R, (1 << 31) - 1, 128, 1e4, 1.0, None) == q.QLIN_ERR_SHAPE
+
+
+def test_batch_bounds_are_32_bit():
+    i32 = q.torch.zeros(2, dtype=q.torch.int32)
+    for bad in (dict(max_q=1 << 32, max_kv=1), dict(max_q=1, max_kv=(1 << 32) + 1), dict(max_q=-1, max_kv=1)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            q.KvBatch(i32.reshape(1, 2), i32, i32[:1], **bad)
+
+
 # ---- paged cache descriptors
 
 I1, I2, I3, I4, R = 0x91000000, 0x92000000, 0x93000000, 0x94000000, 0x95000000   # index arrays, the rope table

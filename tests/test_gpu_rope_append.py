@@ -257,3 +257,22 @@ def test_rope_table(n, rot, base, stretch):
     torch.cuda.synchronize()
     # float64 angles up to n, whose own rounding is 2^-53 n; then one fp32 rounding each
     assert np.all(np.abs(f64(t) - oracle.rope_table(n, rot, base, stretch).astype(np.float64)) <= 2.0 ** -24 + 2.0 ** -50 * n)
+
+
+@pytest.mark.parametrize("d,page,held,ratio", [(128, 64, 45, 0.5), (64, 32, 31, 0.25), (256, 16, 15, 0.5), (128, 64, 63, 3 / 254),
+                                               (64, 64, 1, -2.0), (128, 32, 17, 0.0), (256, 64, 50, 1e-30)])
+def test_held_codes_follow_the_scale(d, page, held, ratio):
+    """A page's earlier codes when its scale rises: all of them ties (ratios of
+    1/2, 1/4), far below the new scale, and scales no append leaves behind."""
+    pool = Pool(3, page, 2, d)
+    pool.host["k"][:] = (np.arange(pool.host["k"].size) % 255 - 127).reshape(pool.host["k"].shape)
+    pool.host["v"][:] = (np.arange(pool.host["v"].size) % 255 - 127).reshape(pool.host["v"].shape)
+    pool.host["k_scale"][:] = pool.host["v_scale"][:] = np.float32(ratio * 2.0 ** -7)
+    for n, t in (("k", pool.cache.k), ("v", pool.cache.v), ("k_scale", pool.cache.k_scale), ("v_scale", pool.cache.v_scale)):
+        t.copy_(torch.from_numpy(pool.host[n]))
+    x = torch.zeros((1, 6 * d), dtype=torch.float16)
+    x[0, ::d] = 127 * 2.0 ** -7          # the new scale is 2^-7
+    append(pool, x, pool.table(1, 1), np.array([0, 1]), np.array([held + 1]), 2, None, False)
+    torch.cuda.synchronize()
+    oracle.rope_append_kv(f64(x), pool.host, pool.table(1, 1), np.array([0, 1]), np.array([held + 1]), 2, None, 0, False)
+    pool.same()
