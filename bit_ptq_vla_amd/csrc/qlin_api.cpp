@@ -614,8 +614,8 @@ qlin_status qlin_rope_append_kv(const void* qkv, qlin_dtype dtype, int64_t token
     if (touched > 0 && static_cast<int64_t>(batch->batch) * cache->heads > (1LL << 29) / touched) return QLIN_ERR_SHAPE;
     const int64_t q_tasks = static_cast<int64_t>(batch->max_q) * heads_q * (d / 16);
     if (q_tasks > (1LL << 31)) return QLIN_ERR_SHAPE;
-    // (a launch holds 2^32 threads, and a block at most 512)
-    const int64_t threads = touched * cache->heads * 2 * 512 + q_tasks + 512;
+    // (a launch holds 2^32 threads, and a block at most 256)
+    const int64_t threads = touched * cache->heads * 2 * 256 + q_tasks + 256;
     if (batch->batch > 0 && threads > 0xFFFFFFFFLL / batch->batch) return QLIN_ERR_SHAPE;
     const int64_t codes = cache->pages * cache->heads * cache->page_size * d, scales = cache->pages * cache->heads * 4;
     const Span outs[5] = {{cache->k, codes}, {cache->v, codes}, {cache->k_scale, scales}, {cache->v_scale, scales},

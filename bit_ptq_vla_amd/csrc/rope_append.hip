@@ -25,9 +25,11 @@
 // bytes each of the keys-first page.
 //
 // Prompts: q|k|v read once, q written, one byte a key and value.  52224 tokens of
-// 8 + 8 + 8 heads of 256 (844 MB) take 266 us, 3.2 TB/s; q alone 69, k alone
-// about 95 of it: its 32 bytes of values need 64 of cosines and sines, which come
-// from L2.  A decode step is latency (64 requests of 8 heads: 7.4 us a call).
+// 8 + 8 + 8 heads of 256 (844 MB) take 248 us, 3.4 TB/s.  The k blocks bound it
+// (of 266 us with larger blocks: q and v alone 167, q and k alone 263): 64 bytes
+// of cosines and sines, from L2, to 32 of values, and a chain of loads, maximum,
+// its check in float64, and codes in each.  A decode step is latency (64 requests
+// of 8 heads: 7.4 us a call).
 
 #include "code_pack.h"
 #include "device_common.h"
@@ -269,7 +271,7 @@ __device__ __forceinline__ void store_page(const AppendParams& p, uint32_t unit)
     __shared__ unsigned long long exact;
     const int tid = threadIdx.x;
     // the k blocks first, then the v blocks: 266 us for 52224 tokens of 8 heads of
-    // 256, alternating 293
+    // 256 in blocks of 512 threads, alternating 293
     const uint32_t half = p.kv_blocks >> 1;
     const bool is_v = unit >= half;
     if (is_v) unit -= half;
@@ -462,7 +464,7 @@ __device__ __forceinline__ void turn_q(const AppendParams& p, uint32_t block) {
 }
 
 template <int DT, int D, int TPB>
-__global__ __launch_bounds__(TPB, 4) void rope_append_kernel(AppendParams p) {
+__global__ __launch_bounds__(TPB, TPB > 64 && D == 256 ? 3 : 4) void rope_append_kernel(AppendParams p) {
     if (blockIdx.x < p.kv_blocks)
         store_page<DT, D, TPB>(p, blockIdx.x);
     else
@@ -479,9 +481,13 @@ hipError_t launch_tpb(AppendParams p, hipStream_t st) {
 
 template <int DT, int D>
 hipError_t launch_d(const AppendParams& p, hipStream_t st) {
-    // a block per (page, head): one wave where a call adds few values to each
+    // A block per (page, head): one wave where a call adds few values to each (256
+    // tokens of 32 heads of 128: 30 us, 256 threads 68), else 256 threads, so that
+    // several pages share a CU and hide each other's waits (52224 tokens of 8 heads
+    // of 256: 248 us, 512 threads 265, 1024 354; 6528 of 32 heads of 128: 75, 512
+    // threads 94, 128 threads 86).
     if (p.ix.max_q * (D / 16) <= 64 && (p.ix.max_q + 6) / 4 * (D / 8) <= 64) return launch_tpb<DT, D, 64>(p, st);
-    return launch_tpb<DT, D, D == 256 ? 512 : 256>(p, st);
+    return launch_tpb<DT, D, 256>(p, st);
 }
 
 template <int DT>

@@ -502,7 +502,7 @@ typedef struct {
  *   infinity or a NaN does not enter the scale; they are stored as +-127 and 0.
  *   Calling again with the same arguments changes nothing.
  * Preconditions: tokens >= 0; heads_q a multiple of cache->heads; ld and ldq
- * multiples of 8; outputs (q_out and the cache) overlap no input; batch x (1024
+ * multiples of 8; outputs (q_out and the cache) overlap no input; batch x (512
  * heads x (pages max_q tokens can touch) + heads_q max_q head_dim / 16) below
  * 2^32, the threads of a launch.  One launch.
  *

@@ -82,7 +82,7 @@ def test_add_rmsnorm_empty_is_ok(lib):
 
 
 def test_more_threads_than_a_launch_holds_are_refused(lib):
-    """2^32 threads: 32 to 1024 a row of the norm, 512 a (page, head) and one to
+    """2^32 threads: 32 to 1024 a row of the norm, 256 a (page, head) and one to
     16 values of q in the append, 512 a block of the attention."""
     big = 1 << 62                           # (any overlap of the fake spans comes later)
     for k, rows in ((64, 1 << 27), (4096, 1 << 23), (4104, 1 << 22), (32768, 1 << 22)):
