@@ -252,13 +252,17 @@ __global__ __launch_bounds__(TPB) void add_rmsnorm_kernel(NormParams p) {
         }
     } else {
         const double rms = sqrt(ss / static_cast<double>(p.k) + static_cast<double>(p.eps));
-        const float inv = ss == 0.0 ? 0.f : static_cast<float>(1.0 / rms);
+        const double inv64 = ss == 0.0 ? 0.0 : 1.0 / rms;
+        const float inv = static_cast<float>(inv64);
+        // a reciprocal near the ends of fp32's range multiplies in float64
+        const bool plain = inv64 < 0x1p126 && (inv64 > 0x1p-126 || ss == 0.0);
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
             float w[8];
             load8<F32>(p.w + col[c], w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) r[c][e] = r[c][e] * inv * w[e];
+            for (int e = 0; e < 8; ++e)
+                r[c][e] = (plain ? r[c][e] * inv : static_cast<float>(r[c][e] * inv64)) * w[e];
             if (ok[c]) store8<DT>(static_cast<char*>(p.q) + (row * p.k + col[c]) * ES, r[c]);
         }
     }

@@ -214,3 +214,18 @@ def test_other_stream_and_replayed_graph():
         g.replay()
         torch.cuda.synchronize()
         check_quant((xq, xs, ro), x2, res2, w, 1e-6, 64, 8, "bf16")
+
+
+@pytest.mark.parametrize("dtype,size", [("f32", 2.0 ** 124), ("f32", 2.0 ** -135), ("bf16", 2.0 ** 122), ("bf16", 2.0 ** -128),
+                                        ("f16", 2.0 ** -22), ("f16", 2.0 ** 13)])
+def test_float_rows_at_the_ends_of_the_range(dtype, size):
+    """1 / rms past or near the ends of fp32's range; eps 0."""
+    m, k = 3, 512
+    base = synth.normal_tensor(SEED, f"norm/ends/{dtype}/{size}", (m, k), dtype="f32").clamp(-3.5, 3.5)
+    x = (base.to(torch.float64) * size).to(DT[dtype])
+    w = 1.0 + synth.normal_tensor(SEED, "norm/ends/w", (k,), std=0.25, dtype="f32")
+    y, _ = q.qlin_add_rmsnorm(x.to(DEV), w.to(DEV), eps=0.0)
+    torch.cuda.synchronize()
+    _, want = oracle.add_rmsnorm(f64(x), None, w.numpy(), 0.0, dtype)
+    tiny = 2.0 ** -25 if dtype == "f16" else 2.0 ** -133
+    assert np.all(np.abs(f64(y) - want) <= (3 * 2.0 ** -24 * (1 + 2.0 ** -20) + HALF_STEP[dtype]) * np.abs(want) + tiny)
