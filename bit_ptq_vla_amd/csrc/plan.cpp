@@ -177,23 +177,24 @@ KvAttnPlan plan_kv_attention(int64_t batch, int64_t max_q, int64_t max_kv, int h
     // Blocks of 128 (256-wide heads) or 256 rows pay once the call is long, counted
     // in 16-row tiles times keys, and fill at least a quarter of theirs.  Measured,
     // us for 16-row blocks / for these, bf16:
-    //   64 wide:   2.7 M (8 x 8 heads, 512 rows) 39 / 36, 4.5 M (32 x 8, 128) 86 / 76, 1.1 M (8 x 8, 256) 21 / 30
-    //   128 wide:  0.5 M (8 x 8 heads, 128 rows) 24 / 26, 0.8 M (192 rows) 27 / 30, 1.1 M (256) 37 / 36,
-    //              4.5 M (32 x 8, 128) 159 / 95, 2.7 M (8 x 8 prompts of 816) 66 / 40
-    //   256 wide:  0.06 M (8 heads, 128 rows) 17 / 31, 0.2 M (8 x 8, 64) 36 / 33, 1.1 M (32 x 8, 64) 107 / 71
-    // and with less than a quarter: 82 / 87 (128 wide, 32 x 8 heads, 64 rows), 57 / 70 (256 wide, 32 rows).
-    const int64_t least = d == 256 ? 1 << 17 : d == 128 ? 3 << 18 : 5 << 19;
-    p.many = rows > (d == 256 ? 32 : 64) && batch * heads * ((rows + 15) / 16) * max_kv > least;
+    //   64 wide:   1.1 M (8 x 8 heads, 256 rows) 21 / 30, 2.7 M (512 rows) 39 / 36, 4.5 M (32 x 8, 128) 88 / 75
+    //   128 wide:  0.5 M (8 x 8 heads, 128 rows) 24 / 27, 0.8 M (192 rows) 27 / 30, 1.1 M (256) 36 / 36,
+    //              4.5 M (32 x 8, 128) 160 / 93, 2.7 M (8 x 8 prompts of 816) 66 / 40
+    //   256 wide:  0.07 M (1 head, 256 rows) 19 / 31, 0.2 M (8 x 8, 64) 25 / 32, 1.1 M (32 x 8, 64) 106 / 72
+    // and with less than a quarter: 81 / 88 (128 wide, 32 x 8 heads, 64 rows), 57 / 69 (256 wide, 32 rows).
+    const int64_t least = d == 256 ? 3 << 17 : d == 128 ? 1 << 20 : 5 << 19;
+    p.many = rows > (d == 256 ? 32 : 64) && max_kv > 0 && batch * heads * ((rows + 15) / 16) > least / max_kv;
     const int64_t per = !p.many ? 16 : d == 256 ? 128 : 256;
     p.row_tiles = static_cast<int>((rows + per - 1) / per);
     const int64_t units = batch * heads * p.row_tiles;
     p.lds_bytes = static_cast<int>(4 * (rows < 16 ? rows : 16) * (d + 6) * 4);
-    // Few tiles: their keys are split until there are two blocks of 16 rows for
-    // each CU, or one of many rows (which fill a CU each), 256 keys at least to a
-    // block.
+    // Few tiles: their keys are split while that gives no more blocks than CUs, 256
+    // keys at least to a block.  Two blocks to a CU, us: 131101 keys of 8 heads 58,
+    // one 55; 8 x 50 rows of 8 heads over 866 keys 20 and 15; a part of a second
+    // one (24 requests of 8 heads, 4097 keys, 384 blocks) 50, none (192) 42.
     int64_t splits = 1;
     if (allow_split && units > 0) {
-        const int64_t want = p.many ? cus / units : (2 * cus + units - 1) / units, most = (max_kv + 255) / 256;
+        const int64_t want = cus / units, most = (max_kv + 255) / 256;
         splits = want < most ? want : most;
         splits = splits < 1 ? 1 : splits;
     }

@@ -222,6 +222,7 @@ qlin_status kv_check(const qlin_kv_cache* c, const qlin_kv_batch* b, int64_t tok
     // positions and (token, head) rows are 32-bit integers in the kernels
     if (b->table_ld > 0x7FFFFFFF || b->max_kv > (1 << 30)) return QLIN_ERR_SHAPE;
     if (static_cast<int64_t>(b->max_q) * (heads_q / c->heads) > (1LL << 30)) return QLIN_ERR_SHAPE;
+    if (static_cast<int64_t>(b->batch) * c->heads > 0x7FFFFFFF) return QLIN_ERR_SHAPE;
     if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_scale) || !aligned16(c->v_scale)) return QLIN_ERR_ALIGN;
     if (!aligned4(b->page_table) || !aligned4(b->q_start) || !aligned4(b->kv_len) || !aligned4(b->prefix_len))
         return QLIN_ERR_ALIGN;

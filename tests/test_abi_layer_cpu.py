@@ -94,6 +94,9 @@ def test_more_threads_than_a_launch_holds_are_refused(lib):
     deep = batch(n=1 << 18, max_q=16, max_kv=64)
     assert attention(lib, c=wide, b=deep, hq=32, ldq=32 * 128, ldo=32 * 128) == q.QLIN_ERR_SHAPE
     assert lib.qlin_kv_attention_workspace_bytes(32, *refs(wide, deep)) == -1
+    huge = batch(n=(1 << 31) - 1, max_q=1 << 20, max_kv=64)
+    assert attention(lib, c=wide, b=huge, hq=32, ldq=32 * 128, ldo=32 * 128) == q.QLIN_ERR_SHAPE
+    assert append(lib, c=wide, b=huge, hq=32, ld=96 * 128, ldq=32 * 128) == q.QLIN_ERR_SHAPE
     assert lib.qlin_rope_table(R, (1 << 31) - 1, 128, 1e4, 1.0, None) == q.QLIN_ERR_SHAPE
 
 
