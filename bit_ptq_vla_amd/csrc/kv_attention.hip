@@ -115,7 +115,7 @@ __device__ __forceinline__ Row row_of(const AttnParams& p, const KvSeq& s, int b
 //
 // For single tokens, bound by the cache's bytes: 64 requests of up to 4096 keys
 // (32 heads over 8, 128 wide, 411 MB) take 81 us, 5.1 TB/s, the rate of a large
-// copy; one request of 131101 keys (268 MB) 51 us, and 5.5 to join its splits.
+// copy; one request of 131101 keys (268 MB) 50 us, and 5 to join its splits.
 // A short request is bound by latency (817 keys, 32 heads: 7 us and 3.4).
 template <int DT, int D, bool CAP>
 __global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
@@ -379,7 +379,7 @@ __device__ __forceinline__ int key_row(int j) {
 // and QK(t): after the last use of K(t - 1) and V(t - 2), before the next of both.
 //
 // Bound by the matrix units and the softmax's issue beside them: 8192 causal
-// tokens (32 heads over 8, 128 wide, 549 GFLOP) take 618 us, 890 TFLOP/s, 74% of
+// tokens (32 heads over 8, 128 wide, 549 GFLOP) take 620 us, 886 TFLOP/s, 74% of
 // a large fp16 product's rate; four waves that did both kinds of work in turn
 // took 643.  256-wide heads compute K Q in both waves of a pair: prompts of up to
 // 816 tokens, 8 x 8 capped heads, 28.6 GFLOP in 109 us.
@@ -631,6 +631,15 @@ __global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
             top = fmaxf(top, hi * sc_[g]);
         }
         top = fmaxf(top, lane_xor<32>(top));
+        // The weights below take x sc unrounded, off the rounded product by 2^-24 of
+        // it: nothing up to 2^20, past the range of the exponent at the far end.
+        // There they take the product that the maximum saw.
+        if (!CAP && __any(fabsf(top) > 0x1p20f && top > kNegInf)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] *= sc_[i >> 3];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) sc_[g] = 1.f;
+        }
         // the reference follows the maximum once that is 2^8 past it: weights stay
         // below 2^8, far inside fp16, and most steps rescale nothing
         if (__any(top > m + 8.f || unit != vr)) {
