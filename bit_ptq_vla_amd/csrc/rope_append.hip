@@ -357,11 +357,11 @@ __device__ __forceinline__ void store_page(const AppendParams& p, uint32_t unit)
     top = block_max<TPB>(top, red);
     // The maximum in exact arithmetic: V's is what it is; a turned K value is off
     // by 2.5 x 2^-24 of it, so the threads whose own maximum comes within 2^-20
-    // look again.  With an infinity or a NaN in the page, all threads do, past those.
+    // (or within 1e-36, where products leave fp32's normal range) look again.  With an infinity or a NaN in the page, all threads do, past those.
     double most = top;
     if (TPB == 64) __syncthreads();           // exact is set
     if (!(top < __builtin_inff()) || (!is_v && p.rot > 0)) {
-        if (!(top < __builtin_inff()) || mine >= top * (1.f - 0x1p-20f)) {
+        if (!(top < __builtin_inff()) || mine >= top * (1.f - 0x1p-20f) - 1e-36f) {
             double m = 0.0;
 #pragma unroll 1
             for (int i = tid; i < count * S; i += TPB) {

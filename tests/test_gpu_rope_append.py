@@ -276,3 +276,17 @@ def test_held_codes_follow_the_scale(d, page, held, ratio):
     torch.cuda.synchronize()
     oracle.rope_append_kv(f64(x), pool.host, pool.table(1, 1), np.array([0, 1]), np.array([held + 1]), 2, None, 0, False)
     pool.same()
+
+
+@pytest.mark.parametrize("size", [2.0 ** -133, 2.0 ** -126, 2.0 ** -110, 2.0 ** 126])
+def test_values_at_the_ends_of_the_range(size):
+    """bf16 values whose turned products leave fp32's normal range (the oracle is exact there too)."""
+    d, page = 64, 16
+    pool = Pool(4, page, 1, d)
+    x = (inputs(18, 3 * d, "bf16", "ends").to(torch.float64).clamp(-3.5, 3.5) * size).to(torch.bfloat16)
+    rope = oracle.rope_table(32, d)
+    append(pool, x, pool.table(1, 3), np.array([0, 18]), np.array([25]), 1, rope, False)
+    torch.cuda.synchronize()
+    with np.errstate(over="ignore"):
+        oracle.rope_append_kv(f64(x), pool.host, pool.table(1, 3), np.array([0, 18]), np.array([25]), 1, rope, d, False)
+    pool.same()
