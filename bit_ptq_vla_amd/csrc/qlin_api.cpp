@@ -649,7 +649,9 @@ qlin_status qlin_kv_attention(const void* q, qlin_dtype dtype, int64_t tokens, i
     if (tokens > 0 && (!q || !out)) return QLIN_ERR_NULL;
     if (dtype != QLIN_F16 && dtype != QLIN_BF16) return QLIN_ERR_DTYPE;
     constexpr float kMax = 3.402823466e38f;
-    if (!(sm_scale >= -kMax && sm_scale <= kMax) || !(softcap >= 0.f && softcap <= kMax)) return QLIN_ERR_UNSUPPORTED;
+    if (!(sm_scale >= -kMax && sm_scale <= kMax)) return QLIN_ERR_UNSUPPORTED;
+    // (a capped score is off by 2^-21 of the cap; 2 / cap must stay in range)
+    if (softcap != 0.f && !(softcap >= 0x1p-20f && softcap <= 4096.f)) return QLIN_ERR_UNSUPPORTED;
     const int64_t wide = static_cast<int64_t>(heads_q) * cache->head_dim;
     if (ldq % 8 != 0 || ldq < wide || ldo % 8 != 0 || ldo < wide || workspace_bytes < 0) return QLIN_ERR_SHAPE;
     if (!workspace && workspace_bytes > 0) return QLIN_ERR_NULL;

@@ -538,7 +538,8 @@ qlin_status qlin_rope_table(float* table, int64_t positions, int32_t rot_dim, do
  * qlin_kv_attention_workspace_bytes: 0 where the call takes no split, -1 for
  * arguments the call would refuse.
  * Preconditions: tokens >= 0; heads_q a multiple of cache->heads; ldq, ldo
- * multiples of 8; sm_scale finite; softcap >= 0, finite; out overlaps no input;
+ * multiples of 8; sm_scale finite; softcap 0 or in [2^-20, 4096] (a capped score
+ * is off by at most 2^-21 of it); out overlaps no input;
  * batch x heads x ceil(max_q x heads_q / heads / 16) below 2^23.
  */
 int64_t qlin_kv_attention_workspace_bytes(int32_t heads_q, const qlin_kv_cache* cache, const qlin_kv_batch* batch);

@@ -100,6 +100,11 @@ def test_more_threads_than_a_launch_holds_are_refused(lib):
     assert lib.qlin_rope_table(R, (1 << 31) - 1, 128, 1e4, 1.0, None) == q.QLIN_ERR_SHAPE
 
 
+@pytest.mark.parametrize("cap", [-0.5, 1e-7, 4097.0, 1e30, float("inf"), float("nan")])
+def test_caps_out_of_range_are_refused(lib, cap):
+    assert attention(lib, cap=cap) == q.QLIN_ERR_UNSUPPORTED
+
+
 def test_batch_bounds_are_32_bit():
     i32 = q.torch.zeros(2, dtype=q.torch.int32)
     for bad in (dict(max_q=1 << 32, max_kv=1), dict(max_q=1, max_kv=(1 << 32) + 1), dict(max_q=-1, max_kv=1)):
