@@ -77,7 +77,7 @@ __device__ __forceinline__ float groups_sum(float v) {
 
 // A score in base-2 units from the raw product: capped where CAP.
 template <bool CAP>
-__device__ __forceinline__ float score(float raw, float mul, float cap_in, float cap_out) {
+__device__ __forceinline__ float score(float raw, float mul, float cap_out) {
     if constexpr (CAP) {
         // c tanh(x / c) = c (1 - 2 / (1 + exp(2 x / c))): mul holds 2 / c * log2 e, cap_out c log2 e
         const float e = __builtin_amdgcn_exp2f(raw * mul);
@@ -252,7 +252,7 @@ __global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
         const float mul = qmul * ks_t;
         const int lim = live ? vis - (t0 + 16 * g) : 0;      // keys of the granule that the query sees
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = i < lim ? score<CAP>(x[i], mul, 0.f, cap_out) : kNegInf;
+        for (int i = 0; i < 16; ++i) x[i] = i < lim ? score<CAP>(x[i], mul, cap_out) : kNegInf;
 
         float top = x[0];
 #pragma unroll
@@ -600,7 +600,7 @@ __global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
         for (int g = 0; g < 4; ++g) sc_[g] = qmul * sc[g];
         if (CAP) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = score<CAP>(x[i], sc_[i >> 3], 0.f, cap_out);
+            for (int i = 0; i < 32; ++i) x[i] = score<CAP>(x[i], sc_[i >> 3], cap_out);
 #pragma unroll
             for (int g = 0; g < 4; ++g) sc_[g] = 1.f;
         }
