@@ -533,6 +533,8 @@ qlin_status qlin_rope_table(float* table, int64_t positions, int32_t rot_dim, do
  *            sequence are then not split over blocks, which is slower for few
  *            rows.  Calls (and replays of captured calls) that can run at the
  *            same time need different workspaces.
+ * max_q and max_kv choose the kernel (a block to up to 16 or up to 256 query
+ * rows), so long prompts and many single tokens are quicker in a call each.
  * fp32 scores, statistics and sums; weights are rounded to fp16 (2^-11 each)
  * before their product with v.  The same call gives the same bits.
  * qlin_kv_attention_workspace_bytes: 0 where the call takes no split, -1 for
