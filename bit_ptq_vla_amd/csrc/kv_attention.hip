@@ -485,9 +485,12 @@ __global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
     };
     if (steps > 0) fetch_k(page_of(en0, 0));
 
-    // queries: dimensions 16 j + 8 hf .. + 7 of row c
+    // queries: dimensions 16 j + 8 hf .. + 7 of row c, with sm_scale's sign: what
+    // is left of the scale is not negative, so a granule's largest score is that
+    // of its largest product
     h8 qf[NS];
-    float qmul = p.sm_scale;
+    const float sign = p.sm_scale < 0.f ? -1.f : 1.f;
+    float qmul = fabsf(p.sm_scale);
     {
         const char* src = static_cast<const char*>(p.q) + (row.token * p.ldq + static_cast<int64_t>(row.head) * D) * 2;
         int e = 0;
@@ -503,7 +506,7 @@ __global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
             top = fmaxf(top, lane_xor<32>(top));
             if (top > 0.f && top < __builtin_inff()) e = 14 - __builtin_amdgcn_frexp_expf(top);
             e = e > 120 ? 120 : e < -120 ? -120 : e;
-            qmul = __builtin_amdgcn_ldexpf(p.sm_scale, -e);
+            qmul = __builtin_amdgcn_ldexpf(qmul, -e);
         }
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
@@ -511,7 +514,7 @@ __global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
             load8<DT>(src + (16 * j + 8 * hf) * 2, f);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                qf[j][i] = static_cast<_Float16>(DT == BF16 ? __builtin_amdgcn_ldexpf(f[i], e) : f[i]);
+                qf[j][i] = static_cast<_Float16>(sign * (DT == BF16 ? __builtin_amdgcn_ldexpf(f[i], e) : f[i]));
         }
     }
     qmul *= CAP ? 2.f * kLog2e / p.cap : kLog2e;
@@ -609,11 +612,10 @@ __global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const int lim = (dead_t >> g & 1) ? 0 : vis - (t0 + 16 * g + 8 * hf);
-                // masked scores leave as the value that scales to -inf (a zero scale: all scores 0)
-                const float out = sc_[g] < 0.f ? -kNegInf : kNegInf;
+                // (a zero scale: the scores seen are 0, and a masked one stays -inf)
                 const bool zero = sc_[g] == 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[8 * g + e] = e < lim ? (zero ? 0.f : x[8 * g + e]) : out;
+                for (int e = 0; e < 8; ++e) x[8 * g + e] = e < lim ? (zero ? 0.f : x[8 * g + e]) : kNegInf;
                 if (zero) sc_[g] = 1.f;
             }
         }
@@ -621,13 +623,8 @@ __global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
             float hi = x[8 * g];
-            if (!CAP && p.sm_scale < 0.f) {
 #pragma unroll
-                for (int e = 1; e < 8; ++e) hi = fminf(hi, x[8 * g + e]);
-            } else {
-#pragma unroll
-                for (int e = 1; e < 8; ++e) hi = fmaxf(hi, x[8 * g + e]);
-            }
+            for (int e = 1; e < 8; ++e) hi = fmaxf(hi, x[8 * g + e]);
             top = fmaxf(top, hi * sc_[g]);
         }
         top = fmaxf(top, lane_xor<32>(top));

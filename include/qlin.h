@@ -443,7 +443,7 @@ qlin_status qlin_gemv_w4a16(const void* x, const void* wq, const void* w_scale, 
  *   stored value is code * scale, codes int8 in [-127, 127].
  *     k        int8 [pages][heads][page_size][head_dim]
  *     v        int8 [pages][heads][head_dim][page_size]   (keys contiguous)
- *     k_scale, v_scale  float [pages][heads]
+ *     k_scale, v_scale  float [pages][heads], not negative
  *   page_size 16, 32 or 64; head_dim 64, 128 or 256.
  * qlin_kv_batch -- the sequences of one call.  Sequence b's position j lies in
  *   page page_table[b * table_ld + j / page_size] at j % page_size.  Its new
