@@ -19,9 +19,12 @@
 // Codes become fp16 exactly (|code| <= 127): byte + 128 under the exponent of
 // 1024, minus 1152.  bf16 queries become fp16 under a power of two per row that
 // brings the row's maximum to 2^13..2^14: exact but for elements 2^-27 below
-// that maximum.  Scores, statistics and sums are fp32.  The weights are rounded
-// to fp16 after multiplication by vs_j / vr, vr the largest v scale met so far
-// (in the exponent; no page overflows them): 2^-11 each at most.
+// that maximum.  Scores, statistics and sums are fp32.
+// A weight is rounded to fp16 after multiplication by its page's v scale over vr,
+// the largest met so far (in the exponent, as s_ij + log2(vs_j / vr)), and the
+// maximum m is that of these exponents: the largest contribution to a row has a
+// weight of 1 whatever the pages' scales, so each is rounded by 2^-11 of itself
+// or 2^-25 of the largest.  The sum of the weights takes the scale out again.
 
 #include "device_common.h"
 #include "kv_index.h"
@@ -53,6 +56,31 @@ struct AttnParams {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_inff();
+// Octaves below vr at which a page's v scale stops: what its keys weigh in the sum
+// (2^80 to 2^88 each, where a key of the largest scale weighs 1 to 2^8) stays
+// inside fp32.  A row whose sum passes 2^79 saw none but such pages, up to the
+// number of its keys: those count as zeros.  (A sum past the top is such a row's.)
+constexpr float kFloor = 80.f, kOnlyZeros = 0x1p79f, kSumTop = 0x1p112f;
+
+// log2(vs / vr) down to the floor (NaN, both zero, becomes it too).
+__device__ __forceinline__ float scale_log(float vs, float vr) {
+    return fmaxf(__builtin_amdgcn_logf(vs) - __builtin_amdgcn_logf(vr), -kFloor);
+}
+
+// The largest v scale rises from vr to vn and the exponents seen have a new
+// maximum top: a row's reference m, its sum l, and the factor of its products.
+// In units of vn a row's earlier exponents are lower, and so is its reference
+// (past 2^20, where exponents are rounded by more than 2^-5, it stays).
+__device__ __forceinline__ float follow(float& m, float& l, float& vr, float vn, float top) {
+    const float rise = vr > 0.f && fabsf(m) < 0x1p20f ? -scale_log(vr, vn) : 0.f;
+    const float mn = fmaxf(m - rise, top);
+    const float r = m > kNegInf ? __builtin_amdgcn_exp2f(m - mn) : 1.f;
+    const float ro = vr > 0.f ? r * (vr / vn) : 0.f;      // (products of zero scales count nothing)
+    l = fminf(l * r, kSumTop);
+    m = mn;
+    vr = vn;
+    return ro;
+}
 
 // Eight codes (two words) as fp16.
 __device__ __forceinline__ h8 codes_f16(uint32_t w0, uint32_t w1) {
@@ -75,15 +103,15 @@ __device__ __forceinline__ float groups_sum(float v) {
     return v + lane_xor<32>(v);
 }
 
-// A score in base-2 units from the raw product: capped where CAP.
+// A score in base-2 units from the raw product, capped where CAP, plus add.
 template <bool CAP>
-__device__ __forceinline__ float score(float raw, float mul, float cap_out) {
+__device__ __forceinline__ float score(float raw, float mul, float cap_out, float add) {
     if constexpr (CAP) {
         // c tanh(x / c) = c (1 - 2 / (1 + exp(2 x / c))): mul holds 2 / c * log2 e, cap_out c log2 e
         const float e = __builtin_amdgcn_exp2f(raw * mul);
-        return cap_out - 2.f * cap_out * __builtin_amdgcn_rcpf(1.f + e);
+        return cap_out + add - 2.f * cap_out * __builtin_amdgcn_rcpf(1.f + e);
     } else {
-        return raw * mul;
+        return fmaf(raw, mul, add);
     }
 }
 
@@ -161,7 +189,7 @@ __global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
         const int idx = (t0 + 16 * gran) >> psl;
         return table[idx < last_idx ? idx : last_idx];
     };
-    // granules past the cache read its last page (their keys are masked)
+    // granules past the keys that the block's rows see read some page (theirs are masked)
     const uint32_t pool = static_cast<uint32_t>(p.ix.pages);
     u4 kw[4][NL], vw[ND];
     float ksc = 0.f, vsc = 0.f;
@@ -175,7 +203,7 @@ __global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
             for (int j = 0; j < NL; ++j) kw[t][j] = *reinterpret_cast<const u4*>(kb + 4 * t * D + 64 * j);
     };
     auto load_v = [&](int t0) {
-        live_next = (static_cast<uint32_t>(nv) < pool) & (t0 + 16 * g < s.kv);
+        live_next = (static_cast<uint32_t>(nv) < pool) & (t0 + 16 * g < k1);
         const int pv = live_next ? nv : 0;
         const int8_t* vb = vh + pv * pool_step;
         const int64_t sv = static_cast<int64_t>(pv) * p.heads + h;
@@ -250,37 +278,28 @@ __global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
         }
         if (more) load_k();
         const float mul = qmul * ks_t;
+        const float vn = fmaxf(vr, groups_max(vs_t)), vlog = scale_log(vs_t, vn);
         const int lim = live ? vis - (t0 + 16 * g) : 0;      // keys of the granule that the query sees
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = i < lim ? score<CAP>(x[i], mul, cap_out) : kNegInf;
+        for (int i = 0; i < 16; ++i) x[i] = i < lim ? score<CAP>(x[i], mul, cap_out, vlog) : kNegInf;
 
         float top = x[0];
 #pragma unroll
         for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
         top = groups_max(top);
-        const float vn = fmaxf(vr, groups_max(vs_t));
         // the reference follows the maximum once that is 2^8 past it (weights stay
         // far inside fp16): most steps rescale nothing
         if (__any(top > m + 8.f || vn != vr)) {
-            const float mn = fmaxf(m, top);
-            const float r = m > kNegInf ? __builtin_amdgcn_exp2f(m - mn) : 1.f;
-            const float ro = r * (vr > 0.f ? vr / vn : 1.f);
+            const float ro = follow(m, l, vr, vn, top);
 #pragma unroll
             for (int t = 0; t < ND; ++t) o[t] *= ro;
-            l *= r;
-            m = mn;
-            vr = vn;
         }
-        // weights times the page's v scale over the largest (at least 2^-30 of it:
-        // below, they leave fp16 anyway); the sum takes that out again
         const float base = m > kNegInf ? m : 0.f;            // nothing seen yet: all weights 0
-        const float vlog = fmaxf(__builtin_amdgcn_logf(vs_t) - __builtin_amdgcn_logf(vr), -30.f);
-        const float off = vlog - base;
         h8 pf[2];
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const float w = __builtin_amdgcn_exp2f(x[i] + off);
+            const float w = __builtin_amdgcn_exp2f(x[i] - base);
             sum += w;
             pf[i >> 3][i & 7] = static_cast<_Float16>(w);
         }
@@ -300,11 +319,12 @@ __global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
 
     // join the waves: element i of tile t is dimension 16 t + 4 g + i of query c
     l = groups_sum(l);
+    const float vo = l < kOnlyZeros ? vr : 0.f;
     if (c < rmax) {
 #pragma unroll
         for (int t = 0; t < ND; ++t)
             *reinterpret_cast<float4*>(lo + (wave * rmax + c) * (D + 4) + 16 * t + 4 * g) =
-                make_float4(o[t][0] * vr, o[t][1] * vr, o[t][2] * vr, o[t][3] * vr);
+                make_float4(o[t][0] * vo, o[t][1] * vo, o[t][2] * vo, o[t][3] * vo);
         if (g == 0) {
             lm[wave * rmax + c] = m;
             ll[wave * rmax + c] = l;
@@ -444,7 +464,7 @@ __global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
     };
     const uint32_t pool = static_cast<uint32_t>(p.ix.pages);
     auto page_of = [&](int entry, int t) {
-        const bool in = static_cast<uint32_t>(entry) < pool, short_of = k0 + 64 * t + 16 * x4 < s.kv;
+        const bool in = static_cast<uint32_t>(entry) < pool, short_of = k0 + 64 * t + 16 * x4 < k1;
         return (in & short_of) ? entry : kNoPage;
     };
     int en0 = 0, en1 = 0, en2 = 0;           // entries of steps t, t + 1, t + 2
@@ -584,9 +604,7 @@ __global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
         float vtop = fmaxf(vs, dpp_mov<0xB1>(vs));
         vtop = fmaxf(vtop, dpp_mov<0x4E>(vtop));
         unit = fmaxf(vr, vtop);
-        // a page 2^-30 below the largest keeps that ratio: its weights leave fp16
-        // there anyway (and a NaN, all scales 0, becomes it too)
-        const float lg = fmaxf(__builtin_amdgcn_logf(vs) - __builtin_amdgcn_logf(unit), -30.f);
+        const float lg = scale_log(vs, unit);
         const float li = __builtin_amdgcn_exp2f(-lg);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -603,7 +621,7 @@ __global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
         for (int g = 0; g < 4; ++g) sc_[g] = qmul * sc[g];
         if (CAP) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = score<CAP>(x[i], sc_[i >> 3], cap_out);
+            for (int i = 0; i < 32; ++i) x[i] = score<CAP>(x[i], sc_[i >> 3], cap_out, 0.f);
 #pragma unroll
             for (int g = 0; g < 4; ++g) sc_[g] = 1.f;
         }
@@ -625,37 +643,37 @@ __global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
             float hi = x[8 * g];
 #pragma unroll
             for (int e = 1; e < 8; ++e) hi = fmaxf(hi, x[8 * g + e]);
-            top = fmaxf(top, hi * sc_[g]);
+            top = fmaxf(top, fmaf(hi, sc_[g], vlog[g]));
         }
         top = fmaxf(top, lane_xor<32>(top));
-        // The weights below take x sc unrounded, off the rounded product by 2^-24 of
+        // The weights below take x sc unrounded, off the rounded exponent by 2^-24 of
         // it: nothing up to 2^20, past the range of the exponent at the far end.
-        // There they take the product that the maximum saw.
+        // There they take the exponent that the maximum saw.
+        float vl[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) vl[g] = vlog[g];
         if (!CAP && __any(fabsf(top) > 0x1p20f && top > kNegInf)) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] *= sc_[i >> 3];
+            for (int i = 0; i < 32; ++i) x[i] = fmaf(x[i], sc_[i >> 3], vlog[i >> 3]);
 #pragma unroll
-            for (int g = 0; g < 4; ++g) sc_[g] = 1.f;
+            for (int g = 0; g < 4; ++g) {
+                sc_[g] = 1.f;
+                vl[g] = 0.f;
+            }
         }
         // the reference follows the maximum once that is 2^8 past it: weights stay
         // below 2^8, far inside fp16, and most steps rescale nothing
         if (__any(top > m + 8.f || unit != vr)) {
-            const float mn = fmaxf(m, top);
-            const float r = m > kNegInf ? __builtin_amdgcn_exp2f(m - mn) : 1.f;
-            const float ro = r * (vr > 0.f ? vr / unit : 1.f);
+            const float ro = follow(m, l, vr, unit, top);
 #pragma unroll
             for (int d = 0; d < ND; ++d)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[d][i] *= ro;
-            l *= r;
-            m = mn;
-            vr = unit;
         }
         const float base = m > kNegInf ? m : 0.f;        // nothing seen yet: all weights 0
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            // weights times the page's v scale over the unit; the sum takes that out again
-            const float off = vlog[g] - base;
+            const float off = vl[g] - base;
             float sum = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -710,11 +728,12 @@ __global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
     if (!grp) __syncthreads();
 
     l += lane_xor<32>(l);
+    const float vo = l < kOnlyZeros ? vr : 0.f;
     if (rw + c >= rows) return;
     // element i of tile d is dimension 32 (half ND + d) + 8 (i / 4) + 4 hf + i % 4 of query c
     const int d0 = 32 * ND * half + 4 * hf;
     if (p.splits == 1) {
-        const float inv = l > 0.f ? vr / l : 0.f;
+        const float inv = l > 0.f ? vo / l : 0.f;
         char* dst = static_cast<char*>(p.out) + (row.token * p.ldo + static_cast<int64_t>(row.head) * D + d0) * 2;
 #pragma unroll
         for (int d = 0; d < ND; ++d)
@@ -737,7 +756,7 @@ __global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
                 *reinterpret_cast<float4*>(p.part_o + at * D + 32 * d + 2 * i + d0) =
-                    make_float4(o[d][i] * vr, o[d][i + 1] * vr, o[d][i + 2] * vr, o[d][i + 3] * vr);
+                    make_float4(o[d][i] * vo, o[d][i + 1] * vo, o[d][i + 2] * vo, o[d][i + 3] * vo);
         if (hf == 0 && half == 0) {
             p.part_ml[2 * at] = m;
             p.part_ml[2 * at + 1] = l;

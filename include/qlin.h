@@ -535,8 +535,11 @@ qlin_status qlin_rope_table(float* table, int64_t positions, int32_t rot_dim, do
  *            same time need different workspaces.
  * max_q and max_kv choose the kernel (a block to up to 16 or up to 256 query
  * rows), so long prompts and many single tokens are quicker in a call each.
- * fp32 scores, statistics and sums; weights are rounded to fp16 (2^-11 each)
- * before their product with v.  The same call gives the same bits.
+ * fp32 scores, statistics and sums.  A weight times its page's v scale is rounded
+ * to fp16 before the product with v's codes: by 2^-11 of itself, or by 2^-25 of
+ * the largest such product among the keys the query sees.  v scales below 2^-71
+ * times the number of keys, of the largest one that a block of queries reads, may
+ * count as 0.  The same call gives the same bits.
  * qlin_kv_attention_workspace_bytes: 0 where the call takes no split, -1 for
  * arguments the call would refuse.
  * Preconditions: tokens >= 0; heads_q a multiple of cache->heads; ldq, ldo
