@@ -820,19 +820,22 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(AttnParams p) {
     store8<DT>(static_cast<char*>(p.out) + ((s.row0 + i) * p.ldo + static_cast<int64_t>(head) * D + d) * 2, f);
 }
 
-void launch_lds(void (*kernel)(AttnParams), int64_t blocks, int threads, int lds, const AttnParams& p, hipStream_t st) {
-    if (lds > 65536)     // a launch's default limit
-        (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+hipError_t launch_lds(void (*kernel)(AttnParams), int64_t blocks, int threads, int lds, const AttnParams& p,
+                      hipStream_t st) {
+    if (lds > 65536) {   // a launch's default limit
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess) return e;
+    }
     kernel<<<dim3(static_cast<unsigned>(blocks)), threads, lds, st>>>(p);
+    return hipGetLastError();
 }
 
 template <int DT, int D, bool CAP>
 hipError_t launch_cap(const AttnParams& p, const KvAttnPlan& plan, hipStream_t st) {
-    if (plan.many)
-        launch_lds(kv_attn_phase_kernel<DT, D, CAP>, plan.blocks, 512, 2 * 2 * 64 * D * 2, p, st);
-    else
-        launch_lds(kv_attn_rows16_kernel<DT, D, CAP>, plan.blocks, 256, plan.lds_bytes, p, st);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e =
+        plan.many ? launch_lds(kv_attn_phase_kernel<DT, D, CAP>, plan.blocks, 512, 2 * 2 * 64 * D * 2, p, st)
+                  : launch_lds(kv_attn_rows16_kernel<DT, D, CAP>, plan.blocks, 256, plan.lds_bytes, p, st);
     if (e != hipSuccess || p.splits == 1) return e;
     const int64_t rows = static_cast<int64_t>(p.ix.batch) * p.ix.max_q * p.heads_q;
     if (p.splits > 8)
