@@ -166,7 +166,7 @@ __global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
     const int rows = s.n * p.group, r0 = rt * 16;
     if (r0 >= rows) return;
     const int last = (r0 + 16 < rows ? r0 + 16 : rows) - 1;
-    const int vis_hi = row_of(p, s, b, h, last).vis, vis_lo = row_of(p, s, b, h, r0).vis;
+    const int vis_hi = row_of(p, s, b, h, last).vis;
     const int k0 = sp * p.split_keys;
     if (sp > 0 && k0 >= vis_hi) return;      // the join reads only the splits below the row's limit
     const int k1 = k0 + p.split_keys < vis_hi ? k0 + p.split_keys : vis_hi;
@@ -559,7 +559,7 @@ __global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
     // with one wave of each kind on a SIMD: 32.6 cycles a product and nothing
     // beside it without the pause; 34.5, and the other wave at 4/5 of its rate, with).
     constexpr int NP = 4 * ND + 2 * NS;
-    auto products = [&](int t, bool first, bool second) {
+    auto products = [&](int t, bool second) {
         const char* vl = lds + 2 * KB + ((t - 1) & 1) * KB;
         const char* kl = lds + (t & 1) * KB;
         auto operand = [&](int i) {
@@ -571,18 +571,18 @@ __global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
         f16v a0, a1;
 #pragma unroll
         for (int i = 0; i < 16; ++i) a0[i] = a1[i] = 0.f;
-        const int from = first ? 0 : 4 * ND, to = second ? NP : 4 * ND;
+        const int to = second ? NP : 4 * ND;
         h8 fr[AHEAD];
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) fr[i] = operand(from + i);
+        for (int i = 0; i < AHEAD; ++i) fr[i] = operand(i);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = from; i < to; ++i) {
-            const h8 w = fr[(i - from) % AHEAD];
+        for (int i = 0; i < to; ++i) {
+            const h8 w = fr[i % AHEAD];
             if (i < 4 * ND) o[i / 4] = __builtin_amdgcn_mfma_f32_32x32x16_f16(w, pf[i % 4], o[i / 4], 0, 0, 0);
             else if ((i - 4 * ND) & 1) a1 = __builtin_amdgcn_mfma_f32_32x32x16_f16(w, qf[(i - 4 * ND) >> 1], a1, 0, 0, 0);
             else a0 = __builtin_amdgcn_mfma_f32_32x32x16_f16(w, qf[(i - 4 * ND) >> 1], a0, 0, 0, 0);
-            if (i + AHEAD < to) fr[(i - from) % AHEAD] = operand(i + AHEAD);
+            if (i + AHEAD < to) fr[i % AHEAD] = operand(i + AHEAD);
             const int part = second && i >= 4 && (i & 1) == 0 ? (i - 4) / 2 : 4 * NC;
             if (part < 4 * NC) stage_part(part, t + 1, t);
             else asm volatile("s_nop 4");
@@ -717,14 +717,14 @@ __global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
     __syncthreads();
     if (grp) __syncthreads();
     for (int t = 0; t < steps; ++t) {
-        products(t, true, true);
+        products(t, true);
         scales(t);
         __syncthreads();
         ahead(t);
         softmax(t);
         __syncthreads();
     }
-    if (steps > 0) products(steps, true, false);
+    if (steps > 0) products(steps, false);
     if (!grp) __syncthreads();
 
     l += lane_xor<32>(l);
