@@ -480,6 +480,9 @@ class DecoderLayer:
         the attention, the attention branch; returns the MLP branch [m][hidden]
         (a buffer of this layer).  batch holds the m new tokens; evs: 11 events
         around the launches."""
+        if batch.max_kv > self.rope.shape[0]:
+            # (the append would turn the tokens behind the table's last row by that row)
+            raise ValueError(f"the layer's rotary table of {self.rope.shape[0]} positions does not hold max_kv = {batch.max_kv}")
         q = self.q
         m = x.shape[0]
         ws = self.workspace(m)

@@ -492,7 +492,9 @@ typedef struct {
  *            (2i, 2i + 1) with interleaved = 1.  rot_dim 0: no rotation, rope
  *            may be NULL; else a multiple of 16 up to head_dim.
  *   positions int32 [tokens]: the rope row of each token; NULL: its place in
- *            the cache.  Cut to 0 .. rope_len - 1.
+ *            the cache.  Cut to 0 .. rope_len - 1: tokens behind the table turn
+ *            by its last row, so a table of max_kv rows serves any length (max_kv
+ *            may lie above it where the lengths do not).
  *   q_out    out [tokens][ldq], heads_q * head_dim columns, dtype; fp32 products.
  * Scales and codes, per (page, head), for k after its rotation and for v:
  *   s = max(s_old, fp32(max |new values of the page| / 127)), s_old = 0 where

@@ -1,0 +1,15 @@
+"""Checks of the layer's Python side that need no GPU."""
+
+import types
+
+import pytest
+import torch
+
+from bit_ptq_vla_amd.workload import DecoderLayer
+
+
+def test_decoder_layer_refuses_lengths_behind_its_rotary_table():
+    layer = DecoderLayer.__new__(DecoderLayer)
+    layer.rope = torch.zeros((64, 16))
+    with pytest.raises(ValueError, match="rotary table of 64 positions"):
+        layer.step(torch.zeros((1, 16)), torch.zeros((1, 16)), types.SimpleNamespace(max_kv=65))
