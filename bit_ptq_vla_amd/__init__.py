@@ -117,10 +117,15 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+# the raw handle of a device's current stream, without building the Stream
+# object (2 us of a call that takes 6); a torch without it builds one
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(dev: torch.device) -> int:
-    # the raw handle of torch.cuda.current_stream(dev), without building the
-    # Stream object (2 us of a call that takes 6)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev.index is None else dev.index)
+    if _raw_stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return _raw_stream(torch.cuda.current_device() if dev.index is None else dev.index)
 
 
 def _check(status: int, where: str) -> None:
