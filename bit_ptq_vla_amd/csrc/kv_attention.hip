@@ -142,9 +142,11 @@ __device__ __forceinline__ Row row_of(const AttnParams& p, const KvSeq& s, int b
 // through LDS, [wave][row][D + 4] sums and then the statistics.
 //
 // For single tokens, bound by the cache's bytes: 64 requests of up to 4096 keys
-// (32 heads over 8, 128 wide, 411 MB) take 81 us, 5.1 TB/s, the rate of a large
+// (32 heads over 8, 128 wide, 411 MB) take 82 us, 5.0 TB/s, the rate of a large
 // copy; one request of 131101 keys (268 MB) 50 us, and 5 to join its splits.
-// A short request is bound by latency (817 keys, 32 heads: 7 us and 3.4).
+// A short request is bound by latency (817 keys, 32 heads: 7 us and 3.5), and so
+// are tens of rows: 8 x 50 rows of 8 heads over 866 keys 15 us, each 16-row block
+// reading and expanding its head's keys anew (60 MB fetched for 16).
 template <int DT, int D, bool CAP>
 __global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
     constexpr int NWV = 4;
@@ -399,10 +401,12 @@ __device__ __forceinline__ int key_row(int j) {
 // and QK(t): after the last use of K(t - 1) and V(t - 2), before the next of both.
 //
 // Bound by the matrix units and the softmax's issue beside them: 8192 causal
-// tokens (32 heads over 8, 128 wide, 549 GFLOP) take 620 us, 886 TFLOP/s, 74% of
-// a large fp16 product's rate; four waves that did both kinds of work in turn
-// took 643.  256-wide heads compute K Q in both waves of a pair: prompts of up to
-// 816 tokens, 8 x 8 capped heads, 28.6 GFLOP in 109 us.
+// tokens (32 heads over 8, 128 wide, 549 GFLOP) take 622 us, 882 TFLOP/s, 63% of
+// a large fp16 product's rate (1.4 PFLOP/s on the same card); four waves that did
+// both kinds of work in turn took 643 where these took 620.  256-wide heads
+// compute K Q, the softmax and the cap in both waves of a pair, and one block fits
+// a CU: prompts of up to 816 tokens, 8 x 8 capped heads, are two uneven rounds of
+// blocks, 28.6 GFLOP in 110 us with neither unit busy half of the time.
 template <int DT, int D, bool CAP>
 __global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
     constexpr int TPB = 512;

@@ -18,13 +18,13 @@
 // float64 too, so no fp32 row can overflow it.
 //
 // A row is held by g lanes (a power of two), lane t holding the 8 values from
-// 8 (c g + t) for chunk c: one chunk up to 8192 values.  More chunks a lane
-// (fewer lanes to reduce over) leave too few waves to cover the loads: at
-// 52224 x 2048 one, two and four chunks take 190, 194 and 222 us.
+// 8 (c g + t) for chunk c: one chunk up to 8192 values.  (At 52224 x 2048 bf16,
+// Hadamard 128, one, two and four chunks a lane take 168, 161 and 171 us.)
 //
 // Bound by vector issue at the backbone's widths: 53 instructions per 64 values
 // with a Hadamard of 128, 151 us of the 168 us that 52224 x 2048 bf16 rows take
-// (749 MB: 4.5 TB/s; a copy moves 5.1).
+// (749 MB: 4.5 TB/s; a copy moves 5.1).  Without a transform 156, to int4 codes
+// 167, to E2M3 177, the float output 146, fp32 rows 241.
 
 #include <cmath>
 
@@ -272,7 +272,13 @@ template <int DT, int NCH, int TPB>
 hipError_t launch_tpb(const NormParams& p, hipStream_t st) {
     const int64_t rpb = TPB / p.g;
     const dim3 grid(static_cast<unsigned>((p.m + rpb - 1) / rpb));
-    constexpr bool known = DT != F32 && NCH == 1;   // 16-bit rows of up to 8192 values
+    // The blocks 1, 64 and 128 are compiled in for 16-bit rows of up to 8192 values,
+    // those of the quantized layers: 52224 x 2048 bf16 take 164 us with 64 (175 with
+    // the block from the arguments) and 168 with 128 (182).  The others take it from
+    // the arguments: 32 takes 169 us, 256 190.  Above 8192 values a lane holds several
+    // chunks: as many values in rows of 16384 take 189 us without a transform and 244
+    // with 128, in rows of 32768 282 and 301 (32 registers spill).
+    constexpr bool known = DT != F32 && NCH == 1;
     if (!p.bits)
         add_rmsnorm_kernel<DT, NCH, TPB, false, 1><<<grid, TPB, 0, st>>>(p);
     else if (known && p.had_block <= 1)
