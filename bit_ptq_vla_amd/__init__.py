@@ -77,6 +77,17 @@ SIGNATURES = {
     "qlin_kv_attention_workspace_bytes": [_I32, _P, _P],
     "qlin_rope_table": [_P, _I64, _I32, ctypes.c_double, ctypes.c_double, _P],
     "qlin_add_rmsnorm": [_P, _I32, _I64, _I64, _I64, _P, _I64, _P, _F32, _P, _P, _P],
+    "qlin_tree_plan": [_P, _I64, _P, _P, _I64, _P, _P],
+    "qlin_tree_accept": [_P, _P, _P, _I64, _P, _P, _I64, _P, _P, _P],
+    "qlin_kv_attention_tree": [_P, _I32, _I64, _I64, _I32, _P, _P, _P, _I64, _F32, _F32, _P, _I64, _P, _I64, _P],
+    "qlin_kv_attention_tree_workspace_bytes": [_I32, _P, _P],
+    "qlin_sample": [_P, _I32, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P],
+    "qlin_sample_workspace_bytes": [_I64, _I64],
+    "qlin_kv_pool_init": [_P, _P],
+    "qlin_kv_resize": [_P, _P, _I32, _I32, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P],
+    "qlin_kv_fork": [_P, _I32, _P, _I64, _I64, _I64, _P, _P, _P, _I64, _P],
+    "qlin_kv_copy_pages": [_P, _I32, _P, _I64, _P],
+    "qlin_kv_compact": [_P, _I32, _P, _P, _I64, _P, _P, _P],
 }
 
 _lib = None
@@ -802,6 +813,276 @@ def qlin_kv_attention(q: torch.Tensor, cache: KvCache, batch: KvBatch, heads_q: 
                     0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(cache.device))
     _check(st, "qlin_kv_attention")
     return out
+
+
+# --------------------------------------------------------------------------
+# trees of drafted tokens, sampling, pages of the cache
+# --------------------------------------------------------------------------
+
+QLIN_MAX_TREE_NODES = 1024
+QLIN_MAX_POOL_ROWS = 1024
+
+
+def _index(t: torch.Tensor, name: str, n: int, dev: torch.device) -> None:
+    """An int32 array of n values on dev."""
+    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must hold {n} contiguous int32 values")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the call on {dev}")
+    _dev_tensor(t, name)
+
+
+def _index_rows(t: torch.Tensor, name: str, rows: int, cols: int, dev: torch.device) -> int:
+    """Row pitch of a row-major int32 [rows][>= cols] tensor on dev."""
+    if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != rows or t.shape[1] < cols or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a row-major int32 [{rows}][>= {cols}] tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the call on {dev}")
+    _dev_tensor(t, name)
+    return t.stride(0) if rows > 1 else t.shape[1]
+
+
+def qlin_tree_plan(parents: torch.Tensor, batch: KvBatch, mask: Optional[torch.Tensor] = None,
+                   positions: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """mask int32 [tokens][ceil(max_q / 32)] (the bits of each node's ancestors
+    and its own) and positions int32 [tokens] (rope rows) of the trees whose
+    nodes are the batch's new tokens; parents int32 [tokens]: an earlier node of
+    the sequence, or -1."""
+    dev, tokens = batch.device, parents.numel()
+    _index(parents, "parents", tokens, dev)
+    words = -(-batch.max_q // 32)
+    if mask is None:
+        mask = torch.empty((tokens, words), dtype=torch.int32, device=dev)
+    if positions is None:
+        positions = torch.empty(tokens, dtype=torch.int32, device=dev)
+    ld = _index_rows(mask, "mask", tokens, words, dev)
+    _index(positions, "positions", tokens, dev)
+    st = _on_device(load().qlin_tree_plan, dev, parents.data_ptr(), tokens, batch._ref, mask.data_ptr(), ld,
+                    positions.data_ptr(), _stream(dev))
+    _check(st, "qlin_tree_plan")
+    return mask, positions
+
+
+def qlin_tree_accept(parents: torch.Tensor, draft: torch.Tensor, sampled: torch.Tensor, batch: KvBatch,
+                     out: Optional[Tuple[torch.Tensor, torch.Tensor, torch.Tensor]] = None
+                     ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """The path of nodes (int32 [batch][max_q], -1 behind it) that the sampled
+    tokens confirm, its length (int32 [batch]) and the token sampled behind it
+    (int32 [batch]); parents, draft and sampled int32 [tokens]."""
+    dev, tokens = batch.device, parents.numel()
+    for name, t in (("parents", parents), ("draft", draft), ("sampled", sampled)):
+        _index(t, name, tokens, dev)
+    if out is None:
+        i32 = dict(dtype=torch.int32, device=dev)
+        out = (torch.empty((batch.batch, batch.max_q), **i32), torch.empty(batch.batch, **i32),
+               torch.empty(batch.batch, **i32))
+    path, count, token = out
+    ld = _index_rows(path, "path", batch.batch, batch.max_q, dev)
+    _index(count, "count", batch.batch, dev)
+    _index(token, "token", batch.batch, dev)
+    st = _on_device(load().qlin_tree_accept, dev, parents.data_ptr(), draft.data_ptr(), sampled.data_ptr(), tokens,
+                    batch._ref, path.data_ptr(), ld, count.data_ptr(), token.data_ptr(), _stream(dev))
+    _check(st, "qlin_tree_accept")
+    return path, count, token
+
+
+def kv_attention_tree_workspace(cache: KvCache, batch: KvBatch, heads_q: int) -> Optional[torch.Tensor]:
+    """A device buffer for qlin_kv_attention_tree (None when the call takes none)."""
+    nbytes = _on_device(load().qlin_kv_attention_tree_workspace_bytes, cache.device, heads_q, cache._ref, batch._ref)
+    if nbytes < 0:
+        raise QlinError(QLIN_ERR_SHAPE, "qlin_kv_attention_tree_workspace_bytes")
+    return torch.empty(nbytes, dtype=torch.uint8, device=cache.device) if nbytes else None
+
+
+def qlin_kv_attention_tree(q: torch.Tensor, cache: KvCache, batch: KvBatch, heads_q: int, mask: torch.Tensor,
+                           sm_scale: Optional[float] = None, softcap: float = 0.0, out: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of tree nodes q [tokens][heads_q d] over the cache: each sees the
+    cached keys and the new ones of its mask row (int32 [tokens][>= max_q / 32],
+    qlin_tree_plan); sm_scale defaults to d^-0.5, workspace
+    (kv_attention_tree_workspace) is allocated here when None."""
+    d, dev = cache.head_dim, cache.device
+    ldq = _rows16(q, "q", heads_q * d)
+    batch.check(cache)
+    if out is None:
+        out = torch.empty((q.shape[0], heads_q * d), dtype=q.dtype, device=q.device)
+    ldo = _rows16(out, "out", heads_q * d)
+    if out.shape[0] != q.shape[0] or out.dtype != q.dtype:
+        raise ValueError("out must have q's rows and type")
+    ldm = _index_rows(mask, "mask", q.shape[0], -(-batch.max_q // 32), dev)
+    if workspace is None and batch.prefix_len is None:
+        workspace = kv_attention_tree_workspace(cache, batch, heads_q)
+    _need(workspace, 0, "workspace")
+    _same_device(dev, q=q, out=out, workspace=workspace)
+    st = _on_device(load().qlin_kv_attention_tree, dev, q.data_ptr(), _TORCH_TO_QLIN.get(q.dtype, -1), q.shape[0], ldq,
+                    heads_q, cache._ref, batch._ref, mask.data_ptr(), ldm, d ** -0.5 if sm_scale is None else sm_scale,
+                    softcap, out.data_ptr(), ldo, _ptr(workspace),
+                    0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(dev))
+    _check(st, "qlin_kv_attention_tree")
+    return out
+
+
+def sample_workspace(rows: int, vocab: int, device) -> Optional[torch.Tensor]:
+    """A device buffer for qlin_sample (None when the call takes none)."""
+    nbytes = _on_device(load().qlin_sample_workspace_bytes, torch.device(device), rows, vocab)
+    if nbytes < 0:
+        raise QlinError(QLIN_ERR_SHAPE, "qlin_sample_workspace_bytes")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def qlin_sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Tensor] = None,
+                top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+                min_p: Optional[torch.Tensor] = None,
+                out: Optional[Tuple[torch.Tensor, Optional[torch.Tensor]]] = None,
+                workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """A token (int32 [rows]) from each row of logits [rows][vocab] and its log
+    probability (float32 [rows], or None in out): temperature, then min-p, top-k
+    and top-p (float32 / int32 [rows], None: no filter), then the given u
+    (float32 [rows], in [0, 1)).  workspace (sample_workspace) is allocated here
+    when None."""
+    dev, rows = logits.device, logits.shape[0]
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be a row-major [rows][vocab] tensor")
+    _dev_tensor(logits, "logits")
+    vocab, size = logits.shape[1], logits.element_size()
+    ld = logits.stride(0) if rows > 1 else -(-vocab * size // 16) * 16 // size
+    for name, t, dt in (("u", u, torch.float32), ("temperature", temperature, torch.float32),
+                        ("top_k", top_k, torch.int32), ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+        if t is not None and (t.dtype != dt or t.numel() != rows or not t.is_contiguous() or t.device != dev):
+            raise ValueError(f"{name} must hold {rows} contiguous {dt} values on {dev}")
+    if out is None:
+        out = (torch.empty(rows, dtype=torch.int32, device=dev), torch.empty(rows, dtype=torch.float32, device=dev))
+    token, logprob = out
+    _index(token, "token", rows, dev)
+    if logprob is not None and (logprob.dtype != torch.float32 or logprob.numel() != rows
+                                or not logprob.is_contiguous() or logprob.device != dev):
+        raise ValueError(f"logprob must hold {rows} contiguous float32 values on {dev}")
+    if workspace is None:
+        workspace = sample_workspace(rows, vocab, dev)
+    _need(workspace, 0, "workspace")
+    _same_device(dev, workspace=workspace)
+    st = _on_device(load().qlin_sample, dev, logits.data_ptr(), _TORCH_TO_QLIN.get(logits.dtype, -1), rows, vocab, ld,
+                    u.data_ptr(), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), token.data_ptr(),
+                    _ptr(logprob), _ptr(workspace),
+                    0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(dev))
+    _check(st, "qlin_sample")
+    return token, logprob
+
+
+class KvStack:
+    """The caches of a model's layers, of one shape, as the page calls take them
+    (kept alive here)."""
+
+    def __init__(self, caches):
+        caches = list(caches)
+        if not caches:
+            raise ValueError("a stack needs a cache at least")
+        c = caches[0]
+        for x in caches:
+            if (x.pages, x.heads, x.page_size, x.head_dim, x.device) != (c.pages, c.heads, c.page_size, c.head_dim, c.device):
+                raise ValueError("the caches of a stack have one shape and device")
+        self.caches, self.layers, self.device, self.page_size = caches, len(caches), c.device, c.page_size
+        self._c = (_KvCacheC * len(caches))(*[x._c for x in caches])
+        self._ref = ctypes.addressof(self._c)
+
+
+class _KvPoolC(ctypes.Structure):
+    _fields_ = [("refs", _P), ("free_bits", _P), ("pages", _I64)]
+
+
+class KvPool:
+    """Which pages are in use, over int32 device tensors the caller owns (kept
+    alive here): refs [pages] (rows that hold a page) and free_bits
+    [ceil(pages / 32)] (bit p % 32 of word p / 32 set where page p is free)."""
+
+    def __init__(self, refs: torch.Tensor, free_bits: torch.Tensor):
+        self.pages, self.device = refs.numel(), refs.device
+        _index(refs, "refs", self.pages, self.device)
+        _index(free_bits, "free_bits", -(-self.pages // 32), self.device)
+        self.refs, self.free_bits = refs, free_bits
+        self._c = _KvPoolC(refs.data_ptr(), free_bits.data_ptr(), self.pages)
+        self._ref = ctypes.addressof(self._c)
+
+    @classmethod
+    def empty(cls, pages: int, device) -> "KvPool":
+        """A pool of free pages (qlin_kv_pool_init)."""
+        i32 = dict(dtype=torch.int32, device=device)
+        pool = cls(torch.empty(pages, **i32), torch.empty(-(-pages // 32), **i32))
+        _check(_on_device(load().qlin_kv_pool_init, pool.device, pool._ref, _stream(pool.device)), "qlin_kv_pool_init")
+        return pool
+
+
+def qlin_kv_resize(pool: KvPool, stack: Optional[KvStack], page_table: torch.Tensor, old_len: torch.Tensor,
+                   new_len: torch.Tensor, page_size: Optional[int] = None, len_out: Optional[torch.Tensor] = None,
+                   moved: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rows of the page table [rows][pages] from lengths old_len to new_len (int32
+    [rows]): pages given back, then new ones; a shared last page of a growing row
+    is copied in every cache of the stack (None: the copies are the caller's; give
+    page_size).  Returns the lengths the rows have now; moved int32 [rows][2]
+    receives the pages copied from and to."""
+    dev, rows = pool.device, old_len.numel()
+    if stack is not None:
+        _same_device(dev, caches=stack.caches[0].k)
+        if page_size is not None and page_size != stack.page_size:
+            raise ValueError(f"page_size {page_size}, the stack's pages hold {stack.page_size}")
+        page_size = stack.page_size
+    if page_size is None:
+        raise ValueError("without a stack page_size is needed")
+    ld = _index_rows(page_table, "page_table", rows, 0, dev)
+    if len_out is None:
+        len_out = torch.empty(rows, dtype=torch.int32, device=dev)
+    if moved is None:
+        moved = torch.empty((rows, 2), dtype=torch.int32, device=dev)
+    for name, t, n in (("old_len", old_len, rows), ("new_len", new_len, rows), ("len_out", len_out, rows),
+                       ("moved", moved, 2 * rows)):
+        _index(t, name, n, dev)
+    st = _on_device(load().qlin_kv_resize, dev, pool._ref, None if stack is None else stack._ref,
+                    0 if stack is None else stack.layers, page_size, page_table.data_ptr(), ld, page_table.shape[1], rows,
+                    old_len.data_ptr(), new_len.data_ptr(), len_out.data_ptr(), moved.data_ptr(), _stream(dev))
+    _check(st, "qlin_kv_resize")
+    return len_out
+
+
+def qlin_kv_fork(pool: KvPool, page_table: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, length: torch.Tensor,
+                 page_size: int) -> None:
+    """Rows dst of the page table come to hold the pages of the first `length`
+    tokens of rows src too (int32 [n] each; dst rows hold none before)."""
+    dev, n = pool.device, src.numel()
+    ld = _index_rows(page_table, "page_table", page_table.shape[0], 0, dev)
+    for name, t in (("src", src), ("dst", dst), ("length", length)):
+        _index(t, name, n, dev)
+    st = _on_device(load().qlin_kv_fork, dev, pool._ref, page_size, page_table.data_ptr(), ld, page_table.shape[1],
+                    page_table.shape[0], src.data_ptr(), dst.data_ptr(), length.data_ptr(), n, _stream(dev))
+    _check(st, "qlin_kv_fork")
+
+
+def qlin_kv_copy_pages(stack: KvStack, pairs: torch.Tensor) -> None:
+    """pairs int32 [n][2]: page pairs[i][1] becomes a copy of page pairs[i][0] in
+    every cache of the stack."""
+    if pairs.dim() != 2 or pairs.shape[1] != 2:
+        raise ValueError("pairs must be [n][2]")
+    _index(pairs, "pairs", pairs.numel(), stack.device)
+    st = _on_device(load().qlin_kv_copy_pages, stack.device, stack._ref, stack.layers, pairs.data_ptr(), pairs.shape[0],
+                    _stream(stack.device))
+    _check(st, "qlin_kv_copy_pages")
+
+
+def qlin_kv_compact(stack: KvStack, batch: KvBatch, path: torch.Tensor, count: torch.Tensor,
+                    kv_len_out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The tokens of each sequence's path of nodes (int32 [batch][>= max_q], count
+    int32 [batch]: qlin_tree_accept) to the places behind its cached ones, in every
+    cache of the stack; returns the new lengths, int32 [batch]."""
+    dev = stack.device
+    batch.check(stack.caches[0])
+    ld = _index_rows(path, "path", batch.batch, batch.max_q, dev)
+    if kv_len_out is None:
+        kv_len_out = torch.empty(batch.batch, dtype=torch.int32, device=dev)
+    _index(count, "count", batch.batch, dev)
+    _index(kv_len_out, "kv_len_out", batch.batch, dev)
+    st = _on_device(load().qlin_kv_compact, dev, stack._ref, stack.layers, batch._ref, path.data_ptr(), ld,
+                    count.data_ptr(), kv_len_out.data_ptr(), _stream(dev))
+    _check(st, "qlin_kv_compact")
+    return kv_len_out
 
 
 QLIN_STREAM_READ_SINK_WORDS = 4096

@@ -96,8 +96,44 @@ hipError_t launch_rope_table(float*, int64_t, int, double, double, hipStream_t) 
 }
 
 hipError_t launch_kv_attention(const KvAttnPlan&, const void*, int, int64_t, int, const KvIndex&, const int8_t*,
-                               const int8_t*, const float*, const float*, int, int, float, float, void*, int64_t,
-                               void*, hipStream_t) {
+                               const int8_t*, const float*, const float*, int, int, float, float, const uint32_t*,
+                               int64_t, void*, int64_t, void*, hipStream_t) {
+    return hipErrorNoBinaryForGpu;
+}
+
+hipError_t launch_tree_plan(const KvIndex&, const int32_t*, uint32_t*, int64_t, int32_t*, hipStream_t) {
+    return hipErrorNoBinaryForGpu;
+}
+
+hipError_t launch_tree_accept(const KvIndex&, const int32_t*, const int32_t*, const int32_t*, int32_t*, int64_t,
+                              int32_t*, int32_t*, hipStream_t) {
+    return hipErrorNoBinaryForGpu;
+}
+
+hipError_t launch_sample(const SampleArgs&, int, void*, hipStream_t) {
+    return hipErrorNoBinaryForGpu;
+}
+
+hipError_t launch_pool_init(const KvPoolArgs&, hipStream_t) {
+    return hipErrorNoBinaryForGpu;
+}
+
+hipError_t launch_kv_resize(const KvPoolArgs&, int32_t*, int64_t, int, int, int, const int32_t*, const int32_t*,
+                            int32_t*, int32_t*, hipStream_t) {
+    return hipErrorNoBinaryForGpu;
+}
+
+hipError_t launch_kv_fork(const KvPoolArgs&, int32_t*, int64_t, int, int, int, const int32_t*, const int32_t*,
+                          const int32_t*, int, hipStream_t) {
+    return hipErrorNoBinaryForGpu;
+}
+
+hipError_t launch_kv_copy_pages(const KvStackArgs&, const int32_t*, int64_t, hipStream_t) {
+    return hipErrorNoBinaryForGpu;
+}
+
+hipError_t launch_kv_compact(const KvIndex&, const KvStackArgs&, const int32_t*, int64_t, const int32_t*, int32_t*,
+                             hipStream_t) {
     return hipErrorNoBinaryForGpu;
 }
 

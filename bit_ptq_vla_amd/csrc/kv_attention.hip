@@ -25,6 +25,11 @@
 // maximum m is that of these exponents: the largest contribution to a row has a
 // weight of 1 whatever the pages' scales, so each is rounded by 2^-11 of itself
 // or 2^-25 of the largest.  The sum of the weights takes the scale out again.
+//
+// TREE: the new tokens are the nodes of a tree, and which of them a query sees
+// stands in its mask row.  Only the steps that reach behind the cached keys read
+// masks, 8 or 16 keys to a lane as bits of one shifted word; a block reads the
+// keys to the sequence's end, whatever its rows.
 
 #include "device_common.h"
 #include "kv_index.h"
@@ -52,6 +57,8 @@ struct AttnParams {
     int row_tiles, splits, split_keys;
     float* part_o;     // [splits][batch * max_q][heads_q][D]
     float* part_ml;    // [splits][batch * max_q][heads_q][2]
+    const uint32_t* mask;   // [tokens][mask_ld] of a tree, or nullptr
+    int64_t mask_ld;
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -124,6 +131,7 @@ struct Row {
     int vis;            // keys it sees
 };
 
+template <bool TREE>
 __device__ __forceinline__ Row row_of(const AttnParams& p, const KvSeq& s, int b, int h, int r) {
     Row x;
     const int i = r / p.group;
@@ -132,7 +140,7 @@ __device__ __forceinline__ Row row_of(const AttnParams& p, const KvSeq& s, int b
     x.token = s.row0 + ii;
     x.slot = static_cast<int64_t>(b) * p.ix.max_q + ii;
     x.head = h * p.group + r % p.group;
-    x.vis = x.ok ? kv_visible(p.ix, s, b, s.first + i) : 0;
+    x.vis = !x.ok ? 0 : TREE ? s.kv : kv_visible(p.ix, s, b, s.first + i);
     return x;
 }
 
@@ -147,7 +155,7 @@ __device__ __forceinline__ Row row_of(const AttnParams& p, const KvSeq& s, int b
 // A short request is bound by latency (817 keys, 32 heads: 7 us and 3.5), and so
 // are tens of rows: 8 x 50 rows of 8 heads over 866 keys 15 us, each 16-row block
 // reading and expanding its head's keys anew (60 MB fetched for 16).
-template <int DT, int D, bool CAP>
+template <int DT, int D, bool CAP, bool TREE>
 __global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
     constexpr int NWV = 4;
     constexpr int NL = D / 64;     // 16-byte K loads per key row and lane
@@ -168,15 +176,16 @@ __global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
     const int rows = s.n * p.group, r0 = rt * 16;
     if (r0 >= rows) return;
     const int last = (r0 + 16 < rows ? r0 + 16 : rows) - 1;
-    const int vis_hi = row_of(p, s, b, h, last).vis;
+    const int vis_hi = row_of<TREE>(p, s, b, h, last).vis;
     const int k0 = sp * p.split_keys;
     if (sp > 0 && k0 >= vis_hi) return;      // the join reads only the splits below the row's limit
     const int k1 = k0 + p.split_keys < vis_hi ? k0 + p.split_keys : vis_hi;
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = lane & 15, g = lane >> 4;
-    const Row row = row_of(p, s, b, h, r0 + c < rows ? r0 + c : last);
+    const Row row = row_of<TREE>(p, s, b, h, r0 + c < rows ? r0 + c : last);
     const int vis = r0 + c < rows ? row.vis : 0;
+    const uint32_t* mask = TREE ? p.mask + row.token * p.mask_ld : nullptr;
     const int ps = p.ix.page_size;
 
     const int psl = 31 - __builtin_clz(ps);
@@ -282,8 +291,14 @@ __global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
         const float mul = qmul * ks_t;
         const float vn = fmaxf(vr, groups_max(vs_t)), vlog = scale_log(vs_t, vn);
         const int lim = live ? vis - (t0 + 16 * g) : 0;      // keys of the granule that the query sees
+        if (TREE) {
+            const uint32_t bits = lim > 0 ? kv_tree_bits(mask, s, t0 + 16 * g) : 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = i < lim ? score<CAP>(x[i], mul, cap_out, vlog) : kNegInf;
+            for (int i = 0; i < 16; ++i) x[i] = bits >> i & 1 ? score<CAP>(x[i], mul, cap_out, vlog) : kNegInf;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = i < lim ? score<CAP>(x[i], mul, cap_out, vlog) : kNegInf;
+        }
 
         float top = x[0];
 #pragma unroll
@@ -336,7 +351,7 @@ __global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
     for (int e = threadIdx.x; e < rmax * (D / 8); e += 64 * NWV) {
         const int r = e / (D / 8), d = e % (D / 8) * 8;
         if (r0 + r >= rows) continue;
-        const Row x = row_of(p, s, b, h, r0 + r);
+        const Row x = row_of<TREE>(p, s, b, h, r0 + r);
         float mt = lm[r];
 #pragma unroll
         for (int w = 1; w < NWV; ++w) mt = fmaxf(mt, lm[w * rmax + r]);
@@ -407,7 +422,7 @@ __device__ __forceinline__ int key_row(int j) {
 // compute K Q, the softmax and the cap in both waves of a pair, and one block fits
 // a CU: prompts of up to 816 tokens, 8 x 8 capped heads, are two uneven rounds of
 // blocks, 28.6 GFLOP in 110 us with neither unit busy half of the time.
-template <int DT, int D, bool CAP>
+template <int DT, int D, bool CAP, bool TREE>
 __global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
     constexpr int TPB = 512;
     constexpr int HV = D == 256 ? 2 : 1;
@@ -432,7 +447,7 @@ __global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
     const int rows = s.n * p.group, r0 = rt * ROWS;
     if (r0 >= rows) return;
     const int last = (r0 + ROWS < rows ? r0 + ROWS : rows) - 1;
-    const int vis_hi = row_of(p, s, b, h, last).vis;
+    const int vis_hi = row_of<TREE>(p, s, b, h, last).vis;
     const int k0 = sp * p.split_keys;
     if (sp > 0 && k0 >= vis_hi) return;
     const int k1 = k0 + p.split_keys < vis_hi ? k0 + p.split_keys : vis_hi;
@@ -443,10 +458,11 @@ __global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
     const int grp = wave >> 2, half = HV == 2 ? wave & 1 : 0;
     const int c = lane & 31, hf = lane >> 5;
     const int rw = r0 + 32 * (wave / HV);                // the wave's first row
-    const Row row = row_of(p, s, b, h, rw + c < rows ? rw + c : last);
+    const Row row = row_of<TREE>(p, s, b, h, rw + c < rows ? rw + c : last);
     const int vis = rw + c < rows ? row.vis : 0;
     // the wave's rows see at least these keys
-    const int wave_lo = rw + 31 < rows ? row_of(p, s, b, h, rw).vis : 0;
+    const int wave_lo = rw + 31 >= rows ? 0 : TREE ? s.first : row_of<TREE>(p, s, b, h, rw).vis;
+    const uint32_t* mask = TREE ? p.mask + row.token * p.mask_ld : nullptr;
     const int ps = p.ix.page_size, psl = 31 - __builtin_clz(ps);
     const int last_idx = s.kv > 0 ? (s.kv - 1) >> psl : 0;
 
@@ -636,8 +652,10 @@ __global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
                 const int lim = (dead_t >> g & 1) ? 0 : vis - (t0 + 16 * g + 8 * hf);
                 // (a zero scale: the scores seen are 0, and a masked one stays -inf)
                 const bool zero = sc_[g] == 0.f;
+                const uint32_t bits = TREE && lim > 0 ? kv_tree_bits(mask, s, t0 + 16 * g + 8 * hf) : 0;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[8 * g + e] = e < lim ? (zero ? 0.f : x[8 * g + e]) : kNegInf;
+                for (int e = 0; e < 8; ++e)
+                    x[8 * g + e] = (TREE ? bits >> e & 1 : e < lim) ? (zero ? 0.f : x[8 * g + e]) : kNegInf;
                 if (zero) sc_[g] = 1.f;
             }
         }
@@ -783,7 +801,7 @@ __global__ __launch_bounds__(256) void kv_attn_join_kernel(AttnParams p) {
     if (b >= p.ix.batch) return;
     const KvSeq s = kv_seq(p.ix, b);
     if (i >= s.n) return;
-    const int vis = kv_visible(p.ix, s, b, s.first + i);
+    const int vis = p.mask ? s.kv : kv_visible(p.ix, s, b, s.first + i);
     const int grp = GROUPS > 1 ? threadIdx.x / LANES : 0, d = threadIdx.x % LANES * 8;
     const int used = vis > 0 ? (vis - 1) / p.split_keys + 1 : 0;
     float m = kNegInf, sum = 0.f, f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -835,11 +853,11 @@ hipError_t launch_lds(void (*kernel)(AttnParams), int64_t blocks, int threads, i
     return hipGetLastError();
 }
 
-template <int DT, int D, bool CAP>
+template <int DT, int D, bool CAP, bool TREE>
 hipError_t launch_cap(const AttnParams& p, const KvAttnPlan& plan, hipStream_t st) {
     const hipError_t e =
-        plan.many ? launch_lds(kv_attn_phase_kernel<DT, D, CAP>, plan.blocks, 512, 2 * 2 * 64 * D * 2, p, st)
-                  : launch_lds(kv_attn_rows16_kernel<DT, D, CAP>, plan.blocks, 256, plan.lds_bytes, p, st);
+        plan.many ? launch_lds(kv_attn_phase_kernel<DT, D, CAP, TREE>, plan.blocks, 512, 2 * 2 * 64 * D * 2, p, st)
+                  : launch_lds(kv_attn_rows16_kernel<DT, D, CAP, TREE>, plan.blocks, 256, plan.lds_bytes, p, st);
     if (e != hipSuccess || p.splits == 1) return e;
     const int64_t rows = static_cast<int64_t>(p.ix.batch) * p.ix.max_q * p.heads_q;
     if (p.splits > 8)
@@ -849,27 +867,29 @@ hipError_t launch_cap(const AttnParams& p, const KvAttnPlan& plan, hipStream_t s
     return hipGetLastError();
 }
 
-template <int DT>
+template <int DT, bool TREE>
 hipError_t launch_dt(const AttnParams& p, const KvAttnPlan& plan, int d, hipStream_t st) {
     const bool cap = p.cap > 0.f;
-    if (d == 64) return cap ? launch_cap<DT, 64, true>(p, plan, st) : launch_cap<DT, 64, false>(p, plan, st);
-    if (d == 128) return cap ? launch_cap<DT, 128, true>(p, plan, st) : launch_cap<DT, 128, false>(p, plan, st);
-    return cap ? launch_cap<DT, 256, true>(p, plan, st) : launch_cap<DT, 256, false>(p, plan, st);
+    if (d == 64) return cap ? launch_cap<DT, 64, true, TREE>(p, plan, st) : launch_cap<DT, 64, false, TREE>(p, plan, st);
+    if (d == 128)
+        return cap ? launch_cap<DT, 128, true, TREE>(p, plan, st) : launch_cap<DT, 128, false, TREE>(p, plan, st);
+    return cap ? launch_cap<DT, 256, true, TREE>(p, plan, st) : launch_cap<DT, 256, false, TREE>(p, plan, st);
 }
 
 }  // namespace
 
 hipError_t launch_kv_attention(const KvAttnPlan& plan, const void* q, int dtype, int64_t ldq, int heads_q,
                                const KvIndex& ix, const int8_t* k, const int8_t* v, const float* ks, const float* vs,
-                               int heads, int d, float sm_scale, float cap, void* out, int64_t ldo, void* ws,
-                               hipStream_t st) {
+                               int heads, int d, float sm_scale, float cap, const uint32_t* mask, int64_t mask_ld,
+                               void* out, int64_t ldo, void* ws, hipStream_t st) {
     AttnParams p{ix, q, ldq, k, v, ks, vs, out, ldo, heads_q, heads, heads_q / heads, sm_scale, cap, plan.row_tiles,
-                 plan.splits, plan.split_keys, nullptr, nullptr};
+                 plan.splits, plan.split_keys, nullptr, nullptr, mask, mask_ld};
     if (plan.splits > 1) {
         p.part_o = static_cast<float*>(ws);
         p.part_ml = p.part_o + static_cast<int64_t>(plan.splits) * ix.batch * ix.max_q * heads_q * d;
     }
-    return dtype == F16 ? launch_dt<F16>(p, plan, d, st) : launch_dt<BF16>(p, plan, d, st);
+    if (mask) return dtype == F16 ? launch_dt<F16, true>(p, plan, d, st) : launch_dt<BF16, true>(p, plan, d, st);
+    return dtype == F16 ? launch_dt<F16, false>(p, plan, d, st) : launch_dt<BF16, false>(p, plan, d, st);
 }
 
 }  // namespace qlin

@@ -94,4 +94,25 @@ QLIN_HD int32_t kv_visible(const KvIndex& x, const KvSeq& s, int b, int32_t p) {
     return e < 0 ? 0 : e < s.kv ? e : s.kv;
 }
 
+// What a node of a tree of new tokens sees of the 32 keys from j0 on, bit i for
+// key j0 + i: the cached keys, and behind them the new tokens whose bits its mask
+// row has (32 to a word, ceil(n / 32) words read, bits from n on count as none).
+QLIN_HD uint32_t kv_tree_bits(const uint32_t* row, const KvSeq& s, int32_t j0) {
+    const int32_t rel = j0 - s.first;
+    if (rel <= -32) return 0xFFFFFFFFu;
+    const int32_t at = rel < 0 ? 0 : rel;
+    if (at >= s.n) return rel < 0 ? (1u << -rel) - 1 : 0;
+    const int32_t w = at >> 5, sh = at & 31, left = s.n - 32 * w;   // new tokens from word w's first on
+    uint32_t lo = row[w];
+    if (left < 32) lo &= (1u << left) - 1;
+    if (rel < 0) return lo << -rel | ((1u << -rel) - 1);
+    if (sh == 0) return lo;
+    uint32_t hi = 0;
+    if (left > 32) {
+        hi = row[w + 1];
+        if (left < 64) hi &= (1u << (left - 32)) - 1;
+    }
+    return lo >> sh | hi << (32 - sh);
+}
+
 }  // namespace qlin

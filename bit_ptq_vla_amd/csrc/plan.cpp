@@ -170,6 +170,12 @@ int64_t composite_calib_work_bytes(int64_t n, int64_t k, int b) {
     return (chunks * k + k + k * b) * 8;
 }
 
+int64_t sample_workspace_bytes(int64_t rows, int64_t vocab) {
+    (void)rows;
+    (void)vocab;
+    return 0;
+}
+
 KvAttnPlan plan_kv_attention(int64_t batch, int64_t max_q, int64_t max_kv, int heads_q, int heads, int d,
                              bool allow_split) {
     KvAttnPlan p;

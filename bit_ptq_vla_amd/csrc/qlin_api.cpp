@@ -246,6 +246,125 @@ qlin::KvIndex kv_index(const qlin_kv_cache* c, const qlin_kv_batch* b, int64_t t
             b->max_kv, c->page_size};
 }
 
+// Rows of qlin_sample (a block of 1024 threads each, of the 2^32 a launch holds).
+constexpr int64_t kMaxSampleRows = 1 << 21;
+
+// Shared checks of the tree calls, which read a batch's lengths only.
+qlin_status tree_check(const qlin_kv_batch* b, int64_t tokens) {
+    if (!b) return QLIN_ERR_NULL;
+    if (b->batch > 0 && (!b->q_start || !b->kv_len)) return QLIN_ERR_NULL;
+    if (tokens < 0 || tokens > 0x7FFFFFFF || b->batch < 0 || b->batch > (1 << 23) || b->max_q < 0 || b->max_kv < 0 ||
+        b->max_kv > (1 << 30) || b->max_q > qlin::kMaxTreeNodes)
+        return QLIN_ERR_SHAPE;
+    return aligned4(b->q_start) && aligned4(b->kv_len) ? QLIN_OK : QLIN_ERR_ALIGN;
+}
+
+qlin::KvIndex tree_index(const qlin_kv_batch* b, int64_t tokens) {
+    return {nullptr, 0, b->q_start, b->kv_len, nullptr, tokens, 0, b->batch, b->max_q, b->max_kv, 16};
+}
+
+qlin_status pool_check(const qlin_kv_pool* p) {
+    if (!p || !p->refs || !p->free_bits) return QLIN_ERR_NULL;
+    if (p->pages < 1 || p->pages > 0x7FFFFFFF) return QLIN_ERR_SHAPE;
+    return aligned16(p->refs) && aligned16(p->free_bits) ? QLIN_OK : QLIN_ERR_ALIGN;
+}
+
+qlin_status table_check(int32_t page_size, const int32_t* table, int64_t ld, int64_t cols, int64_t rows) {
+    if (rows > 0 && !table) return QLIN_ERR_NULL;
+    if (page_size != 16 && page_size != 32 && page_size != 64) return QLIN_ERR_UNSUPPORTED;
+    if (rows < 0 || rows > 0x7FFFFFFF || cols < 0 || cols > (1 << 24) || ld < cols || ld > 0x7FFFFFFF) return QLIN_ERR_SHAPE;
+    return aligned4(table) ? QLIN_OK : QLIN_ERR_ALIGN;
+}
+
+// A stack of layers' caches: each complete, all of one shape, none twice.
+qlin_status stack_check(const qlin_kv_cache* c, int32_t layers) {
+    if (!c) return QLIN_ERR_NULL;
+    if (layers < 1 || layers > 4096) return QLIN_ERR_SHAPE;
+    for (int32_t i = 0; i < layers; ++i)
+        if (!c[i].k || !c[i].v || !c[i].k_scale || !c[i].v_scale) return QLIN_ERR_NULL;
+    if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64) return QLIN_ERR_UNSUPPORTED;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return QLIN_ERR_UNSUPPORTED;
+    if (c->pages < 1 || c->pages > 0x7FFFFFFF || c->heads < 1 || c->heads > 4096) return QLIN_ERR_SHAPE;
+    for (int32_t i = 0; i < layers; ++i) {
+        if (c[i].pages != c->pages || c[i].page_size != c->page_size || c[i].heads != c->heads ||
+            c[i].head_dim != c->head_dim)
+            return QLIN_ERR_SHAPE;
+        if (!aligned16(c[i].k) || !aligned16(c[i].v) || !aligned16(c[i].k_scale) || !aligned16(c[i].v_scale))
+            return QLIN_ERR_ALIGN;
+        for (int32_t j = 0; j < i; ++j)
+            if (c[i].k == c[j].k || c[i].v == c[j].v || c[i].k_scale == c[j].k_scale || c[i].v_scale == c[j].v_scale)
+                return QLIN_ERR_ALIAS;
+    }
+    return QLIN_OK;
+}
+
+bool stack_overlaps(const qlin_kv_cache* c, int32_t layers, const Span* s, int n) {
+    for (int32_t i = 0; i < layers; ++i) {
+        const int64_t scales = c[i].pages * c[i].heads * 4, codes = scales / 4 * c[i].page_size * c[i].head_dim;
+        const Span own[4] = {{c[i].k, codes}, {c[i].v, codes}, {c[i].k_scale, scales}, {c[i].v_scale, scales}};
+        for (const Span& o : own)
+            for (int j = 0; j < n; ++j)
+                if (overlap(o, s[j])) return true;
+    }
+    return false;
+}
+
+// The layers from `at` on that one launch takes.
+qlin::KvStackArgs stack_args(const qlin_kv_cache* c, int32_t layers, int32_t at) {
+    qlin::KvStackArgs a{};
+    a.pages = c->pages;
+    a.page_size = c->page_size;
+    a.heads = c->heads;
+    a.head_dim = c->head_dim;
+    a.layers = layers - at < qlin::kMaxStackLayers ? layers - at : qlin::kMaxStackLayers;
+    for (int i = 0; i < a.layers; ++i) a.layer[i] = {c[at + i].k, c[at + i].v, c[at + i].k_scale, c[at + i].v_scale};
+    return a;
+}
+
+// Checks and launch of the two attention entry points (tree: with a mask).
+int64_t attention_bytes(int32_t heads_q, const qlin_kv_cache* cache, const qlin_kv_batch* batch) {
+    if (kv_check(cache, batch, 0, heads_q) != QLIN_OK) return -1;
+    const qlin::KvAttnPlan plan = qlin::plan_kv_attention(batch->batch, batch->max_q, batch->max_kv, heads_q,
+                                                          cache->heads, cache->head_dim, true);
+    return plan.blocks > kMaxAttnBlocks ? -1 : plan.ws_bytes;
+}
+
+qlin_status attention(const void* q, qlin_dtype dtype, int64_t tokens, int64_t ldq, int32_t heads_q,
+                      const qlin_kv_cache* cache, const qlin_kv_batch* batch, const uint32_t* mask, int64_t mask_ld,
+                      float sm_scale, float softcap, void* out, int64_t ldo, void* workspace, int64_t workspace_bytes,
+                      void* stream) {
+    qlin_status st = kv_check(cache, batch, tokens, heads_q);
+    if (st != QLIN_OK) return st;
+    if (tokens > 0 && (!q || !out)) return QLIN_ERR_NULL;
+    if (dtype != QLIN_F16 && dtype != QLIN_BF16) return QLIN_ERR_DTYPE;
+    constexpr float kMax = 3.402823466e38f;
+    if (!(sm_scale >= -kMax && sm_scale <= kMax)) return QLIN_ERR_UNSUPPORTED;
+    // (a capped score is off by 2^-21 of the cap; 2 / cap must stay in range)
+    if (softcap != 0.f && !(softcap >= 0x1p-20f && softcap <= 4096.f)) return QLIN_ERR_UNSUPPORTED;
+    const int64_t wide = static_cast<int64_t>(heads_q) * cache->head_dim;
+    if (ldq % 8 != 0 || ldq < wide || ldo % 8 != 0 || ldo < wide || workspace_bytes < 0) return QLIN_ERR_SHAPE;
+    if (!workspace && workspace_bytes > 0) return QLIN_ERR_NULL;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return QLIN_ERR_ALIGN;
+    const qlin::KvAttnPlan plan = qlin::plan_kv_attention(batch->batch, batch->max_q, batch->max_kv, heads_q,
+                                                          cache->heads, cache->head_dim, workspace != nullptr);
+    if (plan.blocks > kMaxAttnBlocks) return QLIN_ERR_SHAPE;
+    if (workspace && workspace_bytes < plan.ws_bytes) return QLIN_ERR_WORKSPACE;
+    const int64_t codes = cache->pages * cache->heads * cache->page_size * cache->head_dim;
+    const int64_t scales = cache->pages * cache->heads * 4;
+    const Span outs[2] = {{out, tokens > 0 ? ((tokens - 1) * ldo + wide) * 2 : 0}, {workspace, workspace_bytes}};
+    Span ins[10] = {{q, tokens > 0 ? ((tokens - 1) * ldq + wide) * 2 : 0}, {cache->k, codes}, {cache->v, codes},
+                   {cache->k_scale, scales}, {cache->v_scale, scales},
+                   {mask, tokens > 0 ? ((tokens - 1) * mask_ld + (batch->max_q + 31) / 32) * 4 : 0}};
+    kv_index_spans(cache, batch, ins + 6);
+    if (any_overlap(outs, 2, ins, 10)) return QLIN_ERR_ALIAS;
+    if (tokens == 0 || batch->batch == 0 || batch->max_q == 0) return QLIN_OK;
+    st = check_device();
+    if (st != QLIN_OK) return st;
+    return map_err(qlin::launch_kv_attention(plan, q, dtype, ldq, heads_q, kv_index(cache, batch, tokens), cache->k,
+                                             cache->v, cache->k_scale, cache->v_scale, cache->heads, cache->head_dim,
+                                             sm_scale, softcap, mask, mask_ld, out, ldo, workspace, as_stream(stream)));
+}
+
 // Checks and launch of the two residual + RMS norm entry points (bits 0: the
 // float output, no scale).
 qlin_status add_rmsnorm(const void* x, qlin_dtype dt, int64_t m, int64_t k, int64_t ldx, const void* res, int64_t ldr,
@@ -635,44 +754,34 @@ qlin_status qlin_rope_append_kv(const void* qkv, qlin_dtype dtype, int64_t token
 }
 
 int64_t qlin_kv_attention_workspace_bytes(int32_t heads_q, const qlin_kv_cache* cache, const qlin_kv_batch* batch) {
-    if (kv_check(cache, batch, 0, heads_q) != QLIN_OK) return -1;
-    const qlin::KvAttnPlan plan = qlin::plan_kv_attention(batch->batch, batch->max_q, batch->max_kv, heads_q,
-                                                          cache->heads, cache->head_dim, true);
-    return plan.blocks > kMaxAttnBlocks ? -1 : plan.ws_bytes;
+    return attention_bytes(heads_q, cache, batch);
 }
 
 qlin_status qlin_kv_attention(const void* q, qlin_dtype dtype, int64_t tokens, int64_t ldq, int32_t heads_q,
                               const qlin_kv_cache* cache, const qlin_kv_batch* batch, float sm_scale, float softcap,
                               void* out, int64_t ldo, void* workspace, int64_t workspace_bytes, void* stream) {
-    qlin_status st = kv_check(cache, batch, tokens, heads_q);
-    if (st != QLIN_OK) return st;
-    if (tokens > 0 && (!q || !out)) return QLIN_ERR_NULL;
-    if (dtype != QLIN_F16 && dtype != QLIN_BF16) return QLIN_ERR_DTYPE;
-    constexpr float kMax = 3.402823466e38f;
-    if (!(sm_scale >= -kMax && sm_scale <= kMax)) return QLIN_ERR_UNSUPPORTED;
-    // (a capped score is off by 2^-21 of the cap; 2 / cap must stay in range)
-    if (softcap != 0.f && !(softcap >= 0x1p-20f && softcap <= 4096.f)) return QLIN_ERR_UNSUPPORTED;
-    const int64_t wide = static_cast<int64_t>(heads_q) * cache->head_dim;
-    if (ldq % 8 != 0 || ldq < wide || ldo % 8 != 0 || ldo < wide || workspace_bytes < 0) return QLIN_ERR_SHAPE;
-    if (!workspace && workspace_bytes > 0) return QLIN_ERR_NULL;
-    if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return QLIN_ERR_ALIGN;
-    const qlin::KvAttnPlan plan = qlin::plan_kv_attention(batch->batch, batch->max_q, batch->max_kv, heads_q,
-                                                          cache->heads, cache->head_dim, workspace != nullptr);
-    if (plan.blocks > kMaxAttnBlocks) return QLIN_ERR_SHAPE;
-    if (workspace && workspace_bytes < plan.ws_bytes) return QLIN_ERR_WORKSPACE;
-    const int64_t codes = cache->pages * cache->heads * cache->page_size * cache->head_dim;
-    const int64_t scales = cache->pages * cache->heads * 4;
-    const Span outs[2] = {{out, tokens > 0 ? ((tokens - 1) * ldo + wide) * 2 : 0}, {workspace, workspace_bytes}};
-    Span ins[9] = {{q, tokens > 0 ? ((tokens - 1) * ldq + wide) * 2 : 0}, {cache->k, codes}, {cache->v, codes},
-                   {cache->k_scale, scales}, {cache->v_scale, scales}};
-    kv_index_spans(cache, batch, ins + 5);
-    if (any_overlap(outs, 2, ins, 9)) return QLIN_ERR_ALIAS;
-    if (tokens == 0 || batch->batch == 0 || batch->max_q == 0) return QLIN_OK;
-    st = check_device();
-    if (st != QLIN_OK) return st;
-    return map_err(qlin::launch_kv_attention(plan, q, dtype, ldq, heads_q, kv_index(cache, batch, tokens), cache->k,
-                                             cache->v, cache->k_scale, cache->v_scale, cache->heads, cache->head_dim,
-                                             sm_scale, softcap, out, ldo, workspace, as_stream(stream)));
+    return attention(q, dtype, tokens, ldq, heads_q, cache, batch, nullptr, 0, sm_scale, softcap, out, ldo, workspace,
+                     workspace_bytes, stream);
+}
+
+int64_t qlin_kv_attention_tree_workspace_bytes(int32_t heads_q, const qlin_kv_cache* cache,
+                                               const qlin_kv_batch* batch) {
+    if (!batch || batch->prefix_len || batch->max_q > qlin::kMaxTreeNodes) return -1;
+    return attention_bytes(heads_q, cache, batch);
+}
+
+qlin_status qlin_kv_attention_tree(const void* q, qlin_dtype dtype, int64_t tokens, int64_t ldq, int32_t heads_q,
+                                   const qlin_kv_cache* cache, const qlin_kv_batch* batch, const uint32_t* mask,
+                                   int64_t mask_ld, float sm_scale, float softcap, void* out, int64_t ldo,
+                                   void* workspace, int64_t workspace_bytes, void* stream) {
+    if (!batch || !mask) return QLIN_ERR_NULL;
+    if (batch->prefix_len) return QLIN_ERR_UNSUPPORTED;
+    if (batch->max_q > qlin::kMaxTreeNodes || mask_ld < (static_cast<int64_t>(batch->max_q) + 31) / 32 ||
+        mask_ld > 0x7FFFFFFF)
+        return QLIN_ERR_SHAPE;
+    if (!aligned4(mask)) return QLIN_ERR_ALIGN;
+    return attention(q, dtype, tokens, ldq, heads_q, cache, batch, mask, mask_ld, sm_scale, softcap, out, ldo,
+                     workspace, workspace_bytes, stream);
 }
 
 qlin_status qlin_rope_table(float* table, int64_t positions, int32_t rot_dim, double base, double stretch,
@@ -687,6 +796,187 @@ qlin_status qlin_rope_table(float* table, int64_t positions, int32_t rot_dim, do
     qlin_status st = check_device();
     if (st != QLIN_OK) return st;
     return map_err(qlin::launch_rope_table(table, positions, rot_dim, base, stretch, as_stream(stream)));
+}
+
+qlin_status qlin_tree_plan(const int32_t* parents, int64_t tokens, const qlin_kv_batch* batch, uint32_t* mask,
+                           int64_t mask_ld, int32_t* positions, void* stream) {
+    qlin_status st = tree_check(batch, tokens);
+    if (st != QLIN_OK) return st;
+    if (tokens > 0 && (!parents || !mask || !positions)) return QLIN_ERR_NULL;
+    const int64_t words = (static_cast<int64_t>(batch->max_q) + 31) / 32;
+    if (mask_ld < words || mask_ld > 0x7FFFFFFF) return QLIN_ERR_SHAPE;
+    if (!aligned4(parents) || !aligned4(mask) || !aligned4(positions)) return QLIN_ERR_ALIGN;
+    const Span outs[2] = {{mask, tokens > 0 ? ((tokens - 1) * mask_ld + words) * 4 : 0}, {positions, tokens * 4}};
+    const Span ins[3] = {{parents, tokens * 4}, {batch->q_start, (batch->batch + 1LL) * 4},
+                         {batch->kv_len, batch->batch * 4LL}};
+    if (any_overlap(outs, 2, ins, 3)) return QLIN_ERR_ALIAS;
+    if (tokens == 0 || batch->batch == 0 || batch->max_q == 0) return QLIN_OK;
+    st = check_device();
+    if (st != QLIN_OK) return st;
+    return map_err(qlin::launch_tree_plan(tree_index(batch, tokens), parents, mask, mask_ld, positions, as_stream(stream)));
+}
+
+qlin_status qlin_tree_accept(const int32_t* parents, const int32_t* draft, const int32_t* sampled, int64_t tokens,
+                             const qlin_kv_batch* batch, int32_t* path, int64_t path_ld, int32_t* count,
+                             int32_t* token, void* stream) {
+    qlin_status st = tree_check(batch, tokens);
+    if (st != QLIN_OK) return st;
+    if (tokens > 0 && (!parents || !draft || !sampled)) return QLIN_ERR_NULL;
+    const int64_t n = batch->batch;
+    if (n > 0 && (!path || !count || !token)) return QLIN_ERR_NULL;
+    if (path_ld < batch->max_q || path_ld > 0x7FFFFFFF) return QLIN_ERR_SHAPE;
+    if (!aligned4(parents) || !aligned4(draft) || !aligned4(sampled) || !aligned4(path) || !aligned4(count) ||
+        !aligned4(token))
+        return QLIN_ERR_ALIGN;
+    const Span outs[3] = {{path, n > 0 ? ((n - 1) * path_ld + batch->max_q) * 4 : 0}, {count, n * 4}, {token, n * 4}};
+    const Span ins[5] = {{parents, tokens * 4}, {draft, tokens * 4}, {sampled, tokens * 4},
+                         {batch->q_start, (n + 1) * 4}, {batch->kv_len, n * 4}};
+    if (any_overlap(outs, 3, ins, 5)) return QLIN_ERR_ALIAS;
+    if (n == 0) return QLIN_OK;
+    st = check_device();
+    if (st != QLIN_OK) return st;
+    return map_err(qlin::launch_tree_accept(tree_index(batch, tokens), parents, draft, sampled, path, path_ld, count,
+                                            token, as_stream(stream)));
+}
+
+int64_t qlin_sample_workspace_bytes(int64_t rows, int64_t vocab) {
+    if (rows < 0 || rows > kMaxSampleRows || vocab < 1 || vocab > qlin::kMaxVocab) return -1;
+    return qlin::sample_workspace_bytes(rows, vocab);
+}
+
+qlin_status qlin_sample(const void* logits, qlin_dtype dtype, int64_t rows, int64_t vocab, int64_t ld, const float* u,
+                        const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                        int32_t* token, float* logprob, void* workspace, int64_t workspace_bytes, void* stream) {
+    if (rows > 0 && (!logits || !u || !token)) return QLIN_ERR_NULL;
+    if (!is_float_in(dtype)) return QLIN_ERR_DTYPE;
+    if (rows < 0 || rows > kMaxSampleRows || vocab < 1 || vocab > qlin::kMaxVocab) return QLIN_ERR_SHAPE;
+    const int64_t size = dtype_size(dtype);
+    if (ld < vocab || ld > 0x7FFFFFFF || (ld * size) % 16 != 0 || workspace_bytes < 0) return QLIN_ERR_SHAPE;
+    if (!workspace && workspace_bytes > 0) return QLIN_ERR_NULL;
+    if (!aligned16(logits) || !aligned16(workspace)) return QLIN_ERR_ALIGN;
+    if (!aligned4(u) || !aligned4(temperature) || !aligned4(top_k) || !aligned4(top_p) || !aligned4(min_p) ||
+        !aligned4(token) || !aligned4(logprob))
+        return QLIN_ERR_ALIGN;
+    if (workspace && workspace_bytes < qlin::sample_workspace_bytes(rows, vocab)) return QLIN_ERR_WORKSPACE;
+    const Span outs[3] = {{token, rows * 4}, {logprob, rows * 4}, {workspace, workspace_bytes}};
+    const Span ins[6] = {{logits, rows > 0 ? ((rows - 1) * ld + vocab) * size : 0}, {u, rows * 4},
+                         {temperature, rows * 4}, {top_k, rows * 4}, {top_p, rows * 4}, {min_p, rows * 4}};
+    if (any_overlap(outs, 3, ins, 6)) return QLIN_ERR_ALIAS;
+    if (rows == 0) return QLIN_OK;
+    qlin_status st = check_device();
+    if (st != QLIN_OK) return st;
+    const qlin::SampleArgs a{logits, ld, static_cast<int>(rows), static_cast<int>(vocab), u, temperature, top_k, top_p,
+                             min_p, token, logprob};
+    return map_err(qlin::launch_sample(a, dtype, workspace, as_stream(stream)));
+}
+
+qlin_status qlin_kv_pool_init(const qlin_kv_pool* pool, void* stream) {
+    qlin_status st = pool_check(pool);
+    if (st != QLIN_OK) return st;
+    const Span outs[2] = {{pool->refs, pool->pages * 4}, {pool->free_bits, (pool->pages + 31) / 32 * 4}};
+    if (any_overlap(outs, 2, nullptr, 0)) return QLIN_ERR_ALIAS;
+    st = check_device();
+    if (st != QLIN_OK) return st;
+    return map_err(qlin::launch_pool_init({pool->refs, pool->free_bits, pool->pages}, as_stream(stream)));
+}
+
+qlin_status qlin_kv_resize(const qlin_kv_pool* pool, const qlin_kv_cache* caches, int32_t layers, int32_t page_size,
+                           int32_t* page_table, int64_t table_ld, int64_t table_cols, int64_t rows,
+                           const int32_t* old_len, const int32_t* new_len, int32_t* len_out, int32_t* moved,
+                           void* stream) {
+    qlin_status st = pool_check(pool);
+    if (st != QLIN_OK) return st;
+    st = table_check(page_size, page_table, table_ld, table_cols, rows);
+    if (st != QLIN_OK) return st;
+    if (layers < 0 || rows > qlin::kMaxPoolRows) return QLIN_ERR_SHAPE;
+    if (layers > 0) {
+        st = stack_check(caches, layers);
+        if (st != QLIN_OK) return st;
+        if (caches[0].page_size != page_size || caches[0].pages != pool->pages) return QLIN_ERR_SHAPE;
+    }
+    if (rows > 0 && (!old_len || !new_len || !len_out || !moved)) return QLIN_ERR_NULL;
+    if (!aligned4(old_len) || !aligned4(new_len) || !aligned4(len_out) || !aligned4(moved)) return QLIN_ERR_ALIGN;
+    const Span outs[5] = {{pool->refs, pool->pages * 4}, {pool->free_bits, (pool->pages + 31) / 32 * 4},
+                          {page_table, rows > 0 ? ((rows - 1) * table_ld + table_cols) * 4 : 0},
+                          {len_out, rows * 4}, {moved, rows * 8}};
+    const Span ins[2] = {{old_len, rows * 4}, {new_len, rows * 4}};
+    if (any_overlap(outs, 5, ins, 2)) return QLIN_ERR_ALIAS;
+    if (stack_overlaps(caches, layers, outs, 5) || stack_overlaps(caches, layers, ins, 2)) return QLIN_ERR_ALIAS;
+    if (rows == 0) return QLIN_OK;
+    st = check_device();
+    if (st != QLIN_OK) return st;
+    st = map_err(qlin::launch_kv_resize({pool->refs, pool->free_bits, pool->pages}, page_table, table_ld,
+                                        static_cast<int>(table_cols), static_cast<int>(rows), page_size, old_len,
+                                        new_len, len_out, moved, as_stream(stream)));
+    for (int32_t at = 0; st == QLIN_OK && at < layers; at += qlin::kMaxStackLayers)
+        st = map_err(qlin::launch_kv_copy_pages(stack_args(caches, layers, at), moved, rows, as_stream(stream)));
+    return st;
+}
+
+qlin_status qlin_kv_fork(const qlin_kv_pool* pool, int32_t page_size, int32_t* page_table, int64_t table_ld,
+                         int64_t table_cols, int64_t rows, const int32_t* src, const int32_t* dst,
+                         const int32_t* len, int64_t n, void* stream) {
+    qlin_status st = pool_check(pool);
+    if (st != QLIN_OK) return st;
+    st = table_check(page_size, page_table, table_ld, table_cols, rows);
+    if (st != QLIN_OK) return st;
+    if (n < 0 || n > (1 << 20)) return QLIN_ERR_SHAPE;
+    if (n > 0 && (!src || !dst || !len)) return QLIN_ERR_NULL;
+    if (!aligned4(src) || !aligned4(dst) || !aligned4(len)) return QLIN_ERR_ALIGN;
+    const Span outs[2] = {{pool->refs, pool->pages * 4},
+                          {page_table, rows > 0 ? ((rows - 1) * table_ld + table_cols) * 4 : 0}};
+    const Span ins[3] = {{src, n * 4}, {dst, n * 4}, {len, n * 4}};
+    if (any_overlap(outs, 2, ins, 3)) return QLIN_ERR_ALIAS;
+    if (n == 0 || rows == 0) return QLIN_OK;
+    st = check_device();
+    if (st != QLIN_OK) return st;
+    return map_err(qlin::launch_kv_fork({pool->refs, pool->free_bits, pool->pages}, page_table, table_ld,
+                                        static_cast<int>(table_cols), static_cast<int>(rows), page_size, src, dst, len,
+                                        static_cast<int>(n), as_stream(stream)));
+}
+
+qlin_status qlin_kv_copy_pages(const qlin_kv_cache* caches, int32_t layers, const int32_t* pairs, int64_t n,
+                               void* stream) {
+    qlin_status st = stack_check(caches, layers);
+    if (st != QLIN_OK) return st;
+    if (n < 0 || n > (1 << 24)) return QLIN_ERR_SHAPE;
+    if (n > 0 && !pairs) return QLIN_ERR_NULL;
+    if (!aligned4(pairs)) return QLIN_ERR_ALIGN;
+    const Span ins[1] = {{pairs, n * 8}};
+    if (stack_overlaps(caches, layers, ins, 1)) return QLIN_ERR_ALIAS;
+    if (n == 0) return QLIN_OK;
+    st = check_device();
+    for (int32_t at = 0; st == QLIN_OK && at < layers; at += qlin::kMaxStackLayers)
+        st = map_err(qlin::launch_kv_copy_pages(stack_args(caches, layers, at), pairs, n, as_stream(stream)));
+    return st;
+}
+
+qlin_status qlin_kv_compact(const qlin_kv_cache* caches, int32_t layers, const qlin_kv_batch* batch,
+                            const int32_t* path, int64_t path_ld, const int32_t* count, int32_t* kv_len_out,
+                            void* stream) {
+    if (!batch) return QLIN_ERR_NULL;
+    qlin_status st = stack_check(caches, layers);
+    if (st != QLIN_OK) return st;
+    st = kv_check(&caches[0], batch, 0, caches[0].heads);
+    if (st != QLIN_OK) return st;
+    const int64_t n = batch->batch;
+    if (n > 0 && (!path || !count)) return QLIN_ERR_NULL;
+    if (batch->max_q > qlin::kMaxTreeNodes || path_ld < batch->max_q || path_ld > 0x7FFFFFFF) return QLIN_ERR_SHAPE;
+    const int64_t wide = layers < qlin::kMaxStackLayers ? layers : qlin::kMaxStackLayers;
+    if (n * wide * caches[0].heads > kMaxAttnBlocks) return QLIN_ERR_SHAPE;
+    if (!aligned4(path) || !aligned4(count) || !aligned4(kv_len_out)) return QLIN_ERR_ALIGN;
+    const Span outs[1] = {{kv_len_out, n * 4}};
+    Span ins[6] = {{path, n > 0 ? ((n - 1) * path_ld + batch->max_q) * 4 : 0}, {count, n * 4}};
+    kv_index_spans(&caches[0], batch, ins + 2);
+    if (any_overlap(outs, 1, ins, 6) || stack_overlaps(caches, layers, ins, 6) || stack_overlaps(caches, layers, outs, 1))
+        return QLIN_ERR_ALIAS;
+    if (n == 0) return QLIN_OK;
+    st = check_device();
+    const qlin::KvIndex ix = kv_index(&caches[0], batch, 0x7FFFFFFF);
+    for (int32_t at = 0; st == QLIN_OK && at < layers; at += qlin::kMaxStackLayers)
+        st = map_err(qlin::launch_kv_compact(ix, stack_args(caches, layers, at), path, path_ld, count,
+                                             at == 0 ? kv_len_out : nullptr, as_stream(stream)));
+    return st;
 }
 
 qlin_status qlin_stream_read(const void* src, int64_t bytes, uint32_t* sink, void* stream) {

@@ -109,7 +109,8 @@ hipError_t launch_rope_append(const void* qkv, int dtype, int64_t ld, int heads_
                               hipStream_t st);
 hipError_t launch_rope_table(float* table, int64_t positions, int rot, double base, double stretch, hipStream_t st);
 
-// Attention over the paged cache.  The plan: query-row tiles, and how many
+// Attention over the paged cache (mask: the new tokens are the nodes of a tree,
+// mask_ld words to a row; else nullptr).  The plan: query-row tiles, and how many
 // blocks share a tile's keys (split_keys each; their partials, ws_bytes, are
 // joined by a second kernel).
 struct KvAttnPlan {
@@ -122,8 +123,62 @@ KvAttnPlan plan_kv_attention(int64_t batch, int64_t max_q, int64_t max_kv, int h
                              bool allow_split);
 hipError_t launch_kv_attention(const KvAttnPlan& plan, const void* q, int dtype, int64_t ldq, int heads_q,
                                const KvIndex& ix, const int8_t* k, const int8_t* v, const float* ks, const float* vs,
-                               int heads, int d, float sm_scale, float cap, void* out, int64_t ldo, void* ws,
-                               hipStream_t st);
+                               int heads, int d, float sm_scale, float cap, const uint32_t* mask, int64_t mask_ld,
+                               void* out, int64_t ldo, void* ws, hipStream_t st);
+
+// Trees of drafted tokens: masks and positions from parents, the confirmed path.
+constexpr int kMaxTreeNodes = 1024;
+hipError_t launch_tree_plan(const KvIndex& ix, const int32_t* parents, uint32_t* mask, int64_t mask_ld,
+                            int32_t* positions, hipStream_t st);
+hipError_t launch_tree_accept(const KvIndex& ix, const int32_t* parents, const int32_t* draft, const int32_t* sampled,
+                              int32_t* path, int64_t path_ld, int32_t* count, int32_t* token, hipStream_t st);
+
+// A token from each row of logits (the arrays of settings may be null).
+constexpr int64_t kMaxVocab = 1 << 18;
+struct SampleArgs {
+    const void* logits;
+    int64_t ld;
+    int rows, vocab;
+    const float* u;
+    const float* temperature;
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+    int32_t* token;
+    float* logprob;
+};
+int64_t sample_workspace_bytes(int64_t rows, int64_t vocab);
+hipError_t launch_sample(const SampleArgs& a, int dtype, void* ws, hipStream_t st);
+
+// Pages of the cache: the pool, a stack of layers' caches (as kernel arguments),
+// growth, sharing, copies and the compaction of accepted paths.
+constexpr int kMaxPoolRows = 1024;
+constexpr int kMaxStackLayers = 32;    // to a launch
+struct KvPoolArgs {
+    int32_t* refs;
+    uint32_t* free_bits;
+    int64_t pages;
+};
+struct KvLayerArgs {
+    int8_t* k;
+    int8_t* v;
+    float* ks;
+    float* vs;
+};
+struct KvStackArgs {
+    KvLayerArgs layer[kMaxStackLayers];
+    int64_t pages;
+    int layers, page_size, heads, head_dim;
+};
+hipError_t launch_pool_init(const KvPoolArgs& pool, hipStream_t st);
+hipError_t launch_kv_resize(const KvPoolArgs& pool, int32_t* table, int64_t ld, int cols, int rows, int page_size,
+                            const int32_t* old_len, const int32_t* new_len, int32_t* len_out, int32_t* moved,
+                            hipStream_t st);
+hipError_t launch_kv_fork(const KvPoolArgs& pool, int32_t* table, int64_t ld, int cols, int rows, int page_size,
+                          const int32_t* src, const int32_t* dst, const int32_t* len, int n, hipStream_t st);
+hipError_t launch_kv_copy_pages(const KvStackArgs& c, const int32_t* pairs, int64_t n, hipStream_t st);
+hipError_t launch_kv_compact(const KvIndex& ix, const KvStackArgs& c, const int32_t* path, int64_t path_ld,
+                             const int32_t* count, int32_t* len_out, hipStream_t st);
 
 // Streaming read of bytes (a multiple of 16) at src; one word per block to sink.
 hipError_t launch_stream_read(const void* src, int64_t bytes, uint32_t* sink, int64_t sink_words, hipStream_t st);

@@ -557,6 +557,167 @@ qlin_status qlin_kv_attention(const void* q, qlin_dtype dtype, int64_t tokens, i
                               void* out, int64_t ldo, void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
+ * Trees of drafted tokens.  The new tokens of a sequence (qlin_kv_batch: at most
+ * 1024, max_q) are the nodes of a tree: node i's parent is the index of an earlier
+ * node of its sequence; any other value makes it a root.  Node 0 is the last token
+ * already taken, the others are drafted.  All nodes lie in the cache in their
+ * order, behind the cached tokens; a node's rotary position is the number of cached
+ * tokens plus its depth.  One step: qlin_tree_plan, then in each layer
+ * qlin_rope_append_kv (with these positions) and qlin_kv_attention_tree, a token
+ * sampled behind every node (qlin_sample), qlin_tree_accept, qlin_kv_compact.
+ *
+ * qlin_tree_plan -- parents int32 [tokens] to
+ *   mask      out uint32 [tokens][mask_ld]: bit j % 32 of word j / 32 of node i's row
+ *             is set where j is i or an ancestor of it; ceil(max_q / 32) words of
+ *             each node's row are written.  mask_ld >= ceil(max_q / 32).
+ *   positions out int32 [tokens]: rope rows for qlin_rope_append_kv.
+ * qlin_tree_accept -- the path from node 0 whose every token is the one sampled
+ *   behind its parent: from a node to the first of its children that holds
+ *   (draft) what was sampled behind it (sampled), while there is one.
+ *   draft, sampled  int32 [tokens] (draft at node 0 is not read).
+ *   path      out int32 [batch][path_ld]: the path's nodes in rising order, -1
+ *             behind them up to max_q.  path_ld >= max_q.
+ *   count     out int32 [batch]: nodes of the path (0 without new tokens).
+ *   token     out int32 [batch]: the token sampled behind its last node, -1 without.
+ * Of batch, q_start, kv_len, batch, max_q and max_kv are read.  Index arrays are
+ * 4-byte aligned.  One launch each; rows of no sequence stay as they are.
+ */
+#define QLIN_MAX_TREE_NODES 1024
+qlin_status qlin_tree_plan(const int32_t* parents, int64_t tokens, const qlin_kv_batch* batch, uint32_t* mask,
+                           int64_t mask_ld, int32_t* positions, void* stream);
+qlin_status qlin_tree_accept(const int32_t* parents, const int32_t* draft, const int32_t* sampled, int64_t tokens,
+                             const qlin_kv_batch* batch, int32_t* path, int64_t path_ld, int32_t* count,
+                             int32_t* token, void* stream);
+
+/*
+ * qlin_kv_attention_tree -- qlin_kv_attention for the nodes of a tree: node i sees
+ * every cached key, and of the new ones those whose bits its mask row has
+ * (qlin_tree_plan's, or any others: a row of zeros sees the cached keys only, and
+ * without those gives zeros; its own key is no exception).
+ *   mask     uint32 [tokens][mask_ld], 4-byte aligned, mask_ld >= ceil(max_q / 32).
+ *   batch    max_q at most QLIN_MAX_TREE_NODES; prefix_len must be NULL
+ *            (QLIN_ERR_UNSUPPORTED).
+ * Everything else, workspace, roundings and errors, as qlin_kv_attention.
+ */
+int64_t qlin_kv_attention_tree_workspace_bytes(int32_t heads_q, const qlin_kv_cache* cache,
+                                               const qlin_kv_batch* batch);
+qlin_status qlin_kv_attention_tree(const void* q, qlin_dtype dtype, int64_t tokens, int64_t ldq, int32_t heads_q,
+                                   const qlin_kv_cache* cache, const qlin_kv_batch* batch, const uint32_t* mask,
+                                   int64_t mask_ld, float sm_scale, float softcap, void* out, int64_t ldo,
+                                   void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * qlin_sample -- a token from each row of logits, by a given random number.
+ *   With t the row's temperature, w_i = exp((l_i - max l) / t), and the tokens in the
+ *   order of falling logits, the lowest index first among equal ones:
+ *     min_p   the tokens with w_i >= min_p stay;
+ *     top_k   the first top_k of them;
+ *     top_p   of those the shortest beginning whose sum of w reaches top_p of theirs
+ *             (one at least);
+ *     u       the token is the first of what is left at which the running sum of w
+ *             passes u times the whole sum M: u in [0, 1), u = 0 takes the largest.
+ *   logprob = log(w / M) of the token.
+ *   logits   [rows][ld], dtype F16/BF16/F32, vocab values in each row; rows 16-byte
+ *            aligned (ld a multiple of 8, of 4 for F32).
+ *   u        float [rows], read to 2^-48; values outside are cut to the range, NaN to 0.
+ *   temperature, top_p, min_p float [rows], top_k int32 [rows], each or NULL (1, 1, 0,
+ *            0: no filter).  A temperature that is not positive takes the largest
+ *            logit, the lowest index among equals (logprob 0).  top_k <= 0, top_p >= 1
+ *            or NaN, min_p <= 0 or NaN: no filter; top_p <= 0: the first token.
+ *   token    out int32 [rows];  logprob  out float [rows] or NULL.
+ *   A NaN among the logits counts as -infinity, which is never taken; a row of
+ *   nothing else gives token -1 and a NaN.  Several +infinities are equal.
+ *   Weights are rounded to 2^-44 of the largest and summed as integers: a token is
+ *   that of exact weights unless u or top_p lies within about 2^-40 of a border, and
+ *   the same row gives the same token in any call.
+ *   workspace  device memory, 16-byte aligned, contents overwritten, of at least
+ *            qlin_sample_workspace_bytes(rows, vocab) bytes (else
+ *            QLIN_ERR_WORKSPACE), or NULL with workspace_bytes 0: a row is then not
+ *            split over blocks, which is slower for few rows.  Calls (and replays of
+ *            captured calls) that can run at the same time need different ones.
+ * Preconditions: rows 0 .. 2^21; vocab 1 .. 2^18; ld >= vocab.  Outputs overlap no
+ * input.  The arrays of settings are 4-byte aligned.
+ */
+int64_t qlin_sample_workspace_bytes(int64_t rows, int64_t vocab);
+qlin_status qlin_sample(const void* logits, qlin_dtype dtype, int64_t rows, int64_t vocab, int64_t ld, const float* u,
+                        const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                        int32_t* token, float* logprob, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Pages of the cache.  One pool of page numbers serves every layer's cache and the
+ * rows of a page table [rows][table_ld], int32, of which table_cols entries belong
+ * to each row; a row of length n holds the pages of its first ceil(n / page_size)
+ * entries.
+ *
+ * qlin_kv_pool -- refs int32 [pages]: rows that hold the page, 0 where it is free;
+ *   free_bits uint32 [ceil(pages / 32)]: bit p % 32 of word p / 32 set where page p is
+ *   free.  16-byte aligned device memory of the caller, written by these calls.
+ * qlin_kv_pool_init -- all pages free.
+ * qlin_kv_resize -- every row's length from old_len to new_len (int32 [rows], cut to
+ *   0 .. table_cols * page_size).  First the pages behind the new lengths go back
+ *   (their entries become -1; a page is free when its last row leaves it).  Then, in
+ *   the order of the rows, a growing row takes the pages it needs, the free ones of
+ *   lowest number; where its last page is partly filled and other rows hold it too,
+ *   that page is replaced by a copy (a page that k growing rows hold is copied for all
+ *   but the last of them if nobody else holds it).  A row whose pages, with those of the rows
+ *   before it, are more than the free ones stays as it is.
+ *   len_out   out int32 [rows]: the new length, or the old one of a row that stayed.
+ *   moved     out int32 [rows][2]: the page copied from and the new one, or -1, -1.
+ *   caches    [layers] on the host, each layer's cache, of one shape: the copies are
+ *             made in all of them.  layers may be 0 (the caller makes them: `moved`).
+ *   rows at most 1024.
+ * qlin_kv_fork -- for i < n: row dst[i] gets the first ceil(len[i] / page_size)
+ *   entries of row src[i] and holds those pages too.  dst rows hold no pages before
+ *   (resize to 0), are different ones, and none of src is among them.  Entries that
+ *   name no page in use become -1.  n at most 2^20.
+ * qlin_kv_copy_pages -- pairs int32 [n][2]: page pairs[i][1] becomes a copy of page
+ *   pairs[i][0] (codes and scales, every head) in every cache.  A pair with a number
+ *   outside the pool copies nothing.  A page that is written stands in no other pair.
+ *
+ * Numbers that lie on the device cannot be refused: a page number outside the pool
+ * is no page, giving back a free page changes nothing, a row number outside the
+ * table forks nothing.  resize takes one launch, and one for each 32 layers.
+ */
+#define QLIN_MAX_POOL_ROWS 1024
+typedef struct {
+    int32_t* refs;
+    uint32_t* free_bits;
+    int64_t pages;
+} qlin_kv_pool;
+qlin_status qlin_kv_pool_init(const qlin_kv_pool* pool, void* stream);
+qlin_status qlin_kv_resize(const qlin_kv_pool* pool, const qlin_kv_cache* caches, int32_t layers, int32_t page_size,
+                           int32_t* page_table, int64_t table_ld, int64_t table_cols, int64_t rows,
+                           const int32_t* old_len, const int32_t* new_len, int32_t* len_out, int32_t* moved,
+                           void* stream);
+qlin_status qlin_kv_fork(const qlin_kv_pool* pool, int32_t page_size, int32_t* page_table, int64_t table_ld,
+                         int64_t table_cols, int64_t rows, const int32_t* src, const int32_t* dst,
+                         const int32_t* len, int64_t n, void* stream);
+qlin_status qlin_kv_copy_pages(const qlin_kv_cache* caches, int32_t layers, const int32_t* pairs, int64_t n,
+                               void* stream);
+
+/*
+ * qlin_kv_compact -- the keys and values of an accepted path to the places behind the
+ * cached tokens, in every layer's cache: the token of node path[b][i] goes to place
+ * (cached tokens of sequence b) + i, for i < count[b].
+ *   caches    [layers] on the host, each layer's cache, of one shape.
+ *   path      int32 [batch][path_ld], rising nodes (qlin_tree_accept); it ends before
+ *             a node that is not a later one of the sequence.  count int32 [batch].
+ *   kv_len_out out int32 [batch] (or NULL): cached tokens + path, the sequence's new
+ *             length.  The pages behind it still belong to its row (qlin_kv_resize).
+ * A page whose tokens change gets the largest scale of what it then holds, the tokens
+ * kept from before and those moved in; codes become rne(c * s_old / s), evaluated in
+ * float64.  A page of nodes that stay at their places does not change, nor does what
+ * lies behind the new length.  A node on no page counts as zeros.  A sequence with
+ * more new tokens than its length stays as it is.  Not to be called twice: the second
+ * call would move what the first has put there.
+ * Preconditions: max_q at most QLIN_MAX_TREE_NODES; batch x 32 x heads below 2^23 in
+ * one launch of 32 layers; the written pages belong to one sequence each.
+ */
+qlin_status qlin_kv_compact(const qlin_kv_cache* caches, int32_t layers, const qlin_kv_batch* batch,
+                            const int32_t* path, int64_t path_ld, const int32_t* count, int32_t* kv_len_out,
+                            void* stream);
+
+/*
  * qlin_stream_read -- measurement aid, not a step of the projection: reads
  * `bytes` bytes at src once with 16-byte loads spread over the whole device
  * and writes the xor of the words a workgroup read to sink (one uint32 per

@@ -26,6 +26,7 @@ Blocchi"; LoopQ abstract for plain RTN weights and the W4A16 weight-only form):
                   per block R_j = U_j H_b / sqrt(b) with U_j the eigenvectors
                   of the block's weight Gram matrix
   RMS norm        residual + norm + quantizer (layer_ref.py)
+  drafted trees   plans, attention, sampling, accepted paths, pages (decode_ref.py)
   per-step table  (Omega-QVLA "Scalatura delle Attivazioni DiT per Passo")
                   s_t[c] = max |rotated calibration activations| / qmax per
                   step; static codes v / s_t[c]; s_t folded into that step's
@@ -83,6 +84,15 @@ from .layer_ref import (  # noqa: F401
     rope,
     rope_append_kv,
     kv_attention,
+)
+from .decode_ref import (  # noqa: F401
+    Pool,
+    kv_attention_tree,
+    kv_compact,
+    sample,
+    tree_accept,
+    tree_parents,
+    tree_sees,
 )
 from .compare import (  # noqa: F401
     compare_codes,
