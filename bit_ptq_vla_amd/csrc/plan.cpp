@@ -170,10 +170,17 @@ int64_t composite_calib_work_bytes(int64_t n, int64_t k, int b) {
     return (chunks * k + k + k * b) * 8;
 }
 
-int64_t sample_workspace_bytes(int64_t rows, int64_t vocab) {
-    (void)rows;
-    (void)vocab;
-    return 0;
+SamplePlan plan_sample(int64_t rows, int64_t vocab, bool allow_split) {
+    SamplePlan p{1, static_cast<int>(vocab), 0};
+    const int64_t step = 4096, most = (vocab + 2 * step - 1) / (2 * step);
+    int64_t parts = allow_split && rows > 0 ? device_cus() / rows : 1;
+    parts = parts < most ? parts : most;
+    parts = parts < kMaxSampleParts ? parts : kMaxSampleParts;
+    if (parts < 2) return p;
+    p.size = static_cast<int>(((vocab + parts - 1) / parts + step - 1) / step * step);
+    p.parts = static_cast<int>((vocab + p.size - 1) / p.size);
+    p.ws_bytes = p.parts > 1 ? rows * p.parts * kSamplePartBytes : 0;
+    return p;
 }
 
 KvAttnPlan plan_kv_attention(int64_t batch, int64_t max_q, int64_t max_kv, int heads_q, int heads, int d,

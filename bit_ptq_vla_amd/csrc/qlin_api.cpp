@@ -841,7 +841,7 @@ qlin_status qlin_tree_accept(const int32_t* parents, const int32_t* draft, const
 
 int64_t qlin_sample_workspace_bytes(int64_t rows, int64_t vocab) {
     if (rows < 0 || rows > kMaxSampleRows || vocab < 1 || vocab > qlin::kMaxVocab) return -1;
-    return qlin::sample_workspace_bytes(rows, vocab);
+    return qlin::plan_sample(rows, vocab, true).ws_bytes;
 }
 
 qlin_status qlin_sample(const void* logits, qlin_dtype dtype, int64_t rows, int64_t vocab, int64_t ld, const float* u,
@@ -857,7 +857,7 @@ qlin_status qlin_sample(const void* logits, qlin_dtype dtype, int64_t rows, int6
     if (!aligned4(u) || !aligned4(temperature) || !aligned4(top_k) || !aligned4(top_p) || !aligned4(min_p) ||
         !aligned4(token) || !aligned4(logprob))
         return QLIN_ERR_ALIGN;
-    if (workspace && workspace_bytes < qlin::sample_workspace_bytes(rows, vocab)) return QLIN_ERR_WORKSPACE;
+    if (workspace && workspace_bytes < qlin::plan_sample(rows, vocab, true).ws_bytes) return QLIN_ERR_WORKSPACE;
     const Span outs[3] = {{token, rows * 4}, {logprob, rows * 4}, {workspace, workspace_bytes}};
     const Span ins[6] = {{logits, rows > 0 ? ((rows - 1) * ld + vocab) * size : 0}, {u, rows * 4},
                          {temperature, rows * 4}, {top_k, rows * 4}, {top_p, rows * 4}, {min_p, rows * 4}};

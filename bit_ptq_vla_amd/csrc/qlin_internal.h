@@ -135,6 +135,7 @@ hipError_t launch_tree_accept(const KvIndex& ix, const int32_t* parents, const i
 
 // A token from each row of logits (the arrays of settings may be null).
 constexpr int64_t kMaxVocab = 1 << 18;
+constexpr int kSampleBins = 46 * 32;
 struct SampleArgs {
     const void* logits;
     int64_t ld;
@@ -147,7 +148,13 @@ struct SampleArgs {
     int32_t* token;
     float* logprob;
 };
-int64_t sample_workspace_bytes(int64_t rows, int64_t vocab);
+constexpr int64_t kSamplePartBytes = 16 + kSampleBins * 12;
+constexpr int kMaxSampleParts = 64;
+struct SamplePlan {
+    int parts, size;          // blocks to a row, and the logits that each takes
+    int64_t ws_bytes;
+};
+SamplePlan plan_sample(int64_t rows, int64_t vocab, bool allow_split);
 hipError_t launch_sample(const SampleArgs& a, int dtype, void* ws, hipStream_t st);
 
 // Pages of the cache: the pool, a stack of layers' caches (as kernel arguments),

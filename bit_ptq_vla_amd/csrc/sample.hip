@@ -1,23 +1,31 @@
 // A token from each row of logits, for gfx950: temperature, min-p, top-k, top-p
 // and a given random number.
 //
-//   w_i = 2^-y_i, y_i = (max - l_i) log2(e) / t; in the order of falling logits
-//   (the lowest index first among equals) the kept tokens are a prefix, and the
-//   token is its first whose running mass passes u times the prefix's mass.
+//   w_i = exp((l_i - max) / t); in the order of falling logits (the lowest index
+//   first among equals) the kept tokens are a prefix, and the token is its first
+//   whose running mass passes u times the prefix's mass.
 //
-// Masses are integers in units of 2^-44 (at most 2^18 weights of at most 2^44:
-// below 2^62), so sums have no order: any split of a row over threads, and any
-// order of their atomics, gives the same token.  A weight is evaluated in float64
-// to 2^-46 of itself: the token is that of exact weights but for a u or a top-p
-// within about 2^-40 of a border.
+// With a = 32 log2(e) l / t a token lies in bin rint(a), 32 of them to a factor of
+// two, and its mass is 2^44 2^((a - rint(a)) / 32), an integer: bins do not depend on
+// the row's maximum, so one pass over the row fills them without knowing it, and
+// integer sums have no order: any split of a row over threads and blocks, and any
+// order of their atomics, gives the same token.  The 46 octaves below the largest bin
+// count (what lies lower weighs less than 2^-45 of it).  a - rint(a) is one fused
+// product in float64, exact but for its last rounding, and the mass is evaluated in
+// float64 to 2^-46 of itself.
 //
 // Each filter, and the token itself, is one question: the first element of the
-// order at which the running count, or mass, passes a target.  A histogram over y
-// (32 bins to an octave, 46 octaves: weights below 2^-45 count nothing) leaves one
-// bin; its few elements are gathered in LDS and sorted.  Where they are many (flat
-// rows, equal logits) histograms over their key, the logit as an ordered integer,
-// narrow them down; equal logits have equal weights, so among them the place is a
-// division.
+// order at which the running count, or mass, passes a target.  The bins' running
+// sums leave one bin; its keys (logits as ordered integers) are a range, found by a
+// search over keys, and the few elements in it are listed in LDS.  Where they are
+// many (flat rows, equal logits) histograms over the keys narrow them down; equal
+// logits have equal masses, so among them the place is a division.  Where the filters
+// leave few elements, those are listed once and every question is answered there, each
+// element at its rank; a min-p, or a small top-k (by a histogram of counts), tells so
+// before any mass is computed.
+//
+// A block takes a row, or a part of one where rows are few (the parts' bins then
+// meet in a second launch).
 
 #include "device_common.h"
 #include "qlin_internal.h"
@@ -26,407 +34,1113 @@ namespace qlin {
 
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
-constexpr int kBins = 46 * 32;           // level 0
-constexpr int kSub = 2048;               // bins of a further level
-constexpr int kList = 2048;              // elements that are sorted at once
-constexpr double kYEnd = 46.0;
+constexpr int kSlots = 2048;             // of the ring of bins
+constexpr int kBins = kSampleBins;       // 46 octaves
+constexpr int kSub = 2048;               // bins of a histogram over keys
+constexpr int kList = 1536;              // elements that are listed at once
+constexpr int kNear = 512;               // of them, that are all ranked
+constexpr int kFew = 64;                 // of them, that answer one question
 constexpr uint64_t kOne = 1ull << 44;
 
-struct Shared {
-    double exp2_tab[1024];               // 2^(-i / 1024)
-    uint64_t mass[kSub];                 // level 0: running sums, kept for every question
-    uint32_t count[kSub];
-    union {
-        struct {
-            uint64_t mass[kSub];
-            uint32_t count[kSub];
-        } sub;
-        uint64_t list[kList];
-    };
-    uint64_t part64[kWaves];
-    uint32_t part32[kWaves];
-    uint64_t found64[2];
-    uint32_t found32[4];
-};
+// A value that all lanes hold, in scalar registers.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgcn_readfirstlane(static_cast<int>(x)); }
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ float uniform(float x) { return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x))); }
+__device__ __forceinline__ uint64_t uniform(uint64_t x) {
+    return static_cast<uint64_t>(uniform(static_cast<uint32_t>(x >> 32))) << 32 | uniform(static_cast<uint32_t>(x));
+}
+__device__ __forceinline__ double uniform(double x) {
+    return __longlong_as_double(static_cast<long long>(uniform(static_cast<uint64_t>(__double_as_longlong(x)))));
+}
 
-// Logits as ordered integers; equal logits (the zeros too) have equal keys.  NaN is 0,
-// as -infinity: neither is ever taken.
+// Logits as ordered integers; equal logits (the zeros too) have equal keys.  NaN is
+// -infinity: neither is ever taken.
+constexpr uint32_t kKeyNone = 0x007FFFFFu;      // of -infinity
 __device__ __forceinline__ uint32_t key_of(float v) {
     const uint32_t b = __float_as_uint(v + 0.f);
-    if (v != v) return 0x007FFFFFu;
+    if (v != v) return kKeyNone;
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ float logit_of(uint32_t key) {
     return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
 }
-constexpr uint32_t kKeyNone = 0x007FFFFFu;      // of -infinity
 
-struct Row {
-    const char* at;
-    int vocab;
-    float top;          // the largest logit
-    double scale;       // log2(e) / t
-    uint64_t least;     // min-p as a mass
+struct Scale {
+    double c;           // 32 log2(e) / t
+    double top;         // kMagic + the largest bin
+    // The largest bin is so far from 0 (an infinite logit, a tiny temperature) that only
+    // the largest logit itself lies in the window: all else weighs nothing.
+    bool lone;
+    float top_logit;
 };
+constexpr double kMagic = 0x1.8p52;     // x + kMagic: rint(x) in the low bits of the significand
 
-__device__ __forceinline__ double y_of(const Row& r, float v) {
-    return v == r.top ? 0.0 : (static_cast<double>(r.top) - static_cast<double>(v)) * r.scale;
+// kMagic + the bin of a logit (below 2^51 either side).
+__device__ __forceinline__ double bin_at(const Scale& s, float v) { return fma(static_cast<double>(v), s.c, kMagic); }
+__device__ __forceinline__ int slot_of(double bin) {
+    return static_cast<int>(__double_as_longlong(bin)) & (kSlots - 1);
+}
+// 2^44 2^(f / 32), |f| <= 1/2, rounded to an integer: the exponential's series, what is
+// left out is below 2^-48 of it; the added 2^52 leaves the integer in the significand.
+struct Series {
+    double c5, c4, c3, c2, c1, c0;
+    __device__ __forceinline__ Series() {
+        constexpr double z = 0.69314718055994530942 / 32;
+        c0 = 0x1p52 + 0x1p44;
+        c1 = 0x1p44 * z;
+        c2 = 0x1p44 * z * z / 2;
+        c3 = 0x1p44 * z * z * z / 6;
+        c4 = 0x1p44 * z * z * z * z / 24;
+        c5 = 0x1p44 * z * z * z * z * z / 120;
+        // scalar registers: an addend of a product there needs no copy
+        asm("" : "+s"(c0), "+s"(c1), "+s"(c2), "+s"(c3), "+s"(c4));
+    }
+    __device__ __forceinline__ uint64_t operator()(double f) const {
+        const double p = fma(fma(fma(fma(fma(c5, f, c4), f, c3), f, c2), f, c1), f, c0);
+        return static_cast<uint64_t>(__double_as_longlong(p)) & 0xFFFFFFFFFFFFFull;
+    }
+};
+__device__ __forceinline__ uint64_t mass_in(const Series& series, const Scale& s, float v, double bin) {
+    return series(fma(static_cast<double>(v), s.c, kMagic - bin));
+}
+// Of a logit in the window.
+__device__ __forceinline__ uint64_t mass_of(const Scale& s, float v) {
+    return s.lone ? v == s.top_logit ? kOne : 0 : mass_in(Series(), s, v, bin_at(s, v));
+}
+// How far below the largest bin, to 63 octaves.
+__device__ __forceinline__ int depth_of(const Scale& s, float v) {
+    const double d = s.lone ? 0.0 : s.top - bin_at(s, v);
+    return static_cast<int>(d < 2047.0 ? d : 2047.0);
+}
+__device__ __forceinline__ void set_top(Scale& s, float v) {
+    s.top_logit = uniform(v);
+    s.top = uniform(bin_at(s, v));
+    s.lone = !(fabs(s.top - kMagic) < 0x1p40);
+    if (s.lone) s.top = kMagic;
 }
 
-// 2^-y in units of 2^-44, y in [0, kYEnd): 2^(-i / 1024) from the table times the
-// exponential's series to its fourth power (the rest is below 2^-59).
-__device__ __forceinline__ uint64_t mass_of(double y, const double* tab) {
-    const int n = static_cast<int>(y * 1024.0);
-    const double z = (y * 1024.0 - n) * -6.769015435155716e-4;      // -ln 2 / 1024
-    const double p = fma(z, fma(z, fma(z, fma(z, 1.0 / 24, 1.0 / 6), 0.5), 1.0), 1.0);
-    const double w = ldexp(tab[n & 1023] * p, 44 - (n >> 10));
-    return static_cast<uint64_t>(__double_as_longlong(w + 0x1p52)) & 0xFFFFFFFFFFFFFull;
+__device__ __forceinline__ bool counts(const SampleArgs& a, int row) {
+    return a.top_k && a.top_k[row] > 0 && a.top_k[row] < a.vocab;
+}
+
+__device__ __forceinline__ Scale scale_of(float temp) {
+    Scale sc{uniform(46.166241308446828384 / static_cast<double>(temp)), kMagic, false, 0.f};
+    if (sc.c < 1e-300) sc.c = 1e-300;               // (an infinite temperature: equal weights)
+    return sc;
 }
 
 template <int DT>
-__device__ __forceinline__ float load_one(const char* row, int i) {
-    if constexpr (DT == F32) return reinterpret_cast<const float*>(row)[i];
-    const uint16_t b = reinterpret_cast<const uint16_t*>(row)[i];
-    return DT == BF16 ? bf16_to_f32(b) : f16_bits_to_f32(b);
-}
-
-// f(index, logit) over the row, each thread's indices in rising order.
-template <int DT, typename F>
-__device__ __forceinline__ void scan_row(const Row& r, F f) {
-    const int full = r.vocab & ~7;
-    for (int i = 8 * threadIdx.x; i < full; i += 8 * kThreads) {
-        float v[8];
-        load8<DT>(r.at + static_cast<int64_t>(i) * (DT == F32 ? 4 : 2), v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f(i + j, v[j]);
-    }
-    if (full + static_cast<int>(threadIdx.x) < r.vocab) f(full + threadIdx.x, load_one<DT>(r.at, full + threadIdx.x));
-}
-
-template <typename T>
-__device__ __forceinline__ T wave_scan(T v) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const T o = __shfl_up(v, d, 64);
-        if (lane >= d) v += o;
-    }
-    return v;
-}
-
-// Inclusive sum over the block's threads.
-template <typename T>
-__device__ __forceinline__ T block_scan(T v, T* parts) {
-    v = wave_scan(v);
-    const int wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 63) parts[wave] = v;
-    __syncthreads();
-    T before = 0;
-    for (int w = 0; w < wave; ++w) before += parts[w];
-    __syncthreads();
-    return v + before;
-}
-
-__device__ __forceinline__ uint64_t block_max(uint64_t v, uint64_t* parts) {
-#pragma unroll
-    for (int d = 32; d; d /= 2) {
-        const uint64_t o = __shfl_xor(v, d, 64);
-        v = v > o ? v : o;
-    }
-    if ((threadIdx.x & 63) == 0) parts[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = parts[0];
-    for (int w = 1; w < kWaves; ++w) v = v > parts[w] ? v : parts[w];
-    __syncthreads();
-    return v;
-}
-
-// Histogram (mass, count)[n] to its running sums, n <= 2048.
-__device__ __forceinline__ void run_up(uint64_t* mass, uint32_t* count, int n, Shared& s) {
-    const int i = 2 * threadIdx.x;
-    const uint64_t m0 = i < n ? mass[i] : 0, m1 = i + 1 < n ? mass[i + 1] : 0;
-    const uint32_t c0 = i < n ? count[i] : 0, c1 = i + 1 < n ? count[i + 1] : 0;
-    const uint64_t m = block_scan<uint64_t>(m0 + m1, s.part64);
-    const uint32_t c = block_scan<uint32_t>(c0 + c1, s.part32);
-    if (i < n) {
-        mass[i] = m - m1;
-        count[i] = c - c1;
-    }
-    if (i + 1 < n) {
-        mass[i + 1] = m;
-        count[i + 1] = c;
-    }
-    __syncthreads();
-}
-
-// First bin whose running sum passes the target (some bin does).
-template <typename T>
-__device__ __forceinline__ int first_past(const T* run, int n, T target, Shared& s) {
-    for (int i = threadIdx.x; i < n; i += kThreads)
-        if (run[i] > target && (i == 0 || run[i - 1] <= target)) s.found32[0] = i;
-    __syncthreads();
-    const int b = s.found32[0];
-    __syncthreads();
-    return b;
-}
-
-// Where an order passes a target: the mass up to and with that element, and which it is.
-struct Place {
-    uint64_t mass;
-    uint32_t key;
-    int index;
-};
-
-// The first element at which the running count (BY_COUNT) or mass passes target.
-// The token's index is found only with INDEX.
-template <int DT, bool BY_COUNT, bool INDEX>
-__device__ Place pass(const Row& r, uint64_t target, Shared& s) {
-    int bin = BY_COUNT ? first_past<uint32_t>(s.count, kBins, static_cast<uint32_t>(target), s)
-                       : first_past<uint64_t>(s.mass, kBins, target, s);
-    uint64_t mass_before = bin ? s.mass[bin - 1] : 0;
-    uint32_t count_before = bin ? s.count[bin - 1] : 0;
-    uint32_t n = s.count[bin] - count_before;
-    const int bin0 = bin;
-    // of the bin's elements, those whose key lies in [lo, hi]
-    uint32_t lo = 0, hi = 0xFFFFFFFFu;
-    auto member = [&](float v, double& y) {
-        y = y_of(r, v);
-        if (!(y < kYEnd) || static_cast<int>(y * 32.0) != bin0) return false;
-        if (mass_of(y, s.exp2_tab) < r.least) return false;
-        const uint32_t k = key_of(v);
-        return k >= lo && k <= hi;
+struct Sampler {
+    struct Shared {
+        uint64_t mass[kSlots + 64];          // of a bin, in the ring
+        uint32_t count[kSlots + 64];
+        uint64_t run_mass[kBins];            // running sums from the largest bin down, in its units
+        uint32_t run_count[kBins];           // (where nothing counts: no fewer, about a hundredth more)
+        union {
+            struct {
+                uint64_t mass[kSub];
+                uint32_t count[kSub];
+            } sub;
+            struct {
+                uint64_t order[kList + 8];   // falling key, then rising index
+                uint64_t mass[kList + 8];
+                union {
+                    struct {
+                        uint64_t mass[kThreads];
+                        uint32_t count[kThreads];
+                        uint64_t few_order[kFew + 8], few_mass[kFew + 8];
+                    } part;
+                    struct {
+                        uint64_t order[kNear], ahead[kNear];
+                    } sorted;
+                };
+            } list;
+        };
+        uint64_t down[32];                   // 2^63 2^(-i / 32)
+        double up[32];                       // 2^(i / 32)
+        int offset[kMaxSampleParts];
+        uint64_t part64[kWaves];
+        uint32_t part32[kWaves];
+        uint64_t found64[2];
+        uint32_t found32[4];
     };
-    if (n > kList) {
-        // the range of their keys, then 2048 parts of it at a time
-        uint64_t top = 0, low = 0;
-        scan_row<DT>(r, [&](int, float v) {
-            double y;
-            if (member(v, y)) {
-                const uint64_t k = key_of(v), nk = 0xFFFFFFFFu - k;
-                top = top > k ? top : k;
-                low = low > nk ? low : nk;
+
+    // 16-byte words of a row in a thread's registers: element e of word j is index
+    // first + (1024 j + thread) N + e, -infinity past the end.
+    struct Chunk {
+        static constexpr int N = DT == F32 ? 4 : 8;
+        static constexpr int kWords = 4;
+        static constexpr int kSize = kThreads * N * kWords;
+        uint4 w[kWords];
+
+        __device__ __forceinline__ static int index(int first, int j, int e) {
+            return first + (kThreads * j + static_cast<int>(threadIdx.x)) * N + e;
+        }
+        // The word at element i, -infinity from the end on.
+        __device__ __forceinline__ static uint4 word_at(const char* row, int i, int end) {
+            constexpr uint32_t none = DT == F32 ? 0xFF800000u : DT == BF16 ? 0xFF80FF80u : 0xFC00FC00u;
+            if (i + N <= end) return *reinterpret_cast<const uint4*>(row + static_cast<int64_t>(i) * (16 / N));
+            uint32_t x[4] = {none, none, none, none};
+#pragma unroll
+            for (int e = 0; e < N - 1; ++e) {
+                if (i + e >= end) continue;
+                if constexpr (DT == F32) {
+                    x[e] = reinterpret_cast<const uint32_t*>(row)[i + e];
+                } else {
+                    const uint32_t b = reinterpret_cast<const uint16_t*>(row)[i + e];
+                    x[e / 2] = e & 1 ? (x[e / 2] & 0xFFFFu) | b << 16 : (x[e / 2] & 0xFFFF0000u) | b;
+                }
+            }
+            return make_uint4(x[0], x[1], x[2], x[3]);
+        }
+        __device__ __forceinline__ void load(const char* row, int first, int end) {
+#pragma unroll
+            for (int j = 0; j < kWords; ++j) w[j] = word_at(row, index(first, j, 0), end);
+        }
+        __device__ __forceinline__ static float value(uint4 word, int e) {
+            const uint32_t x[4] = {word.x, word.y, word.z, word.w};
+            if constexpr (DT == F32) return __uint_as_float(x[e]);
+            if constexpr (DT == BF16) return __uint_as_float(e & 1 ? x[e / 2] & 0xFFFF0000u : x[e / 2] << 16);
+            return f16_bits_to_f32(static_cast<uint16_t>(e & 1 ? x[e / 2] >> 16 : x[e / 2] & 0xFFFFu));
+        }
+        template <typename F>
+        __device__ __forceinline__ void words(F f) const {
+#pragma unroll
+            for (int j = 0; j < kWords; ++j) f(w[j]);
+        }
+    };
+
+    // A row, or a part of it.
+    struct Row {
+        const char* at;
+        int from, to;
+        __device__ __forceinline__ float value(int i) const {
+            if constexpr (DT == F32) return reinterpret_cast<const float*>(at)[i];
+            const uint16_t b = reinterpret_cast<const uint16_t*>(at)[i];
+            return DT == BF16 ? bf16_to_f32(b) : f16_bits_to_f32(b);
+        }
+        // f(index of its first element, word) for the thread's words, four more on their way:
+        // from the first on, or from the last, whose words a pass before left in the caches.
+        template <bool BACK, typename F>
+        __device__ __forceinline__ void words_to(F f) const {
+            constexpr int step = kThreads * Chunk::N;
+            const int n = (to - from + step - 1) / step;
+            auto at_step = [&](int k) { return Chunk::index(from + (BACK ? n - 1 - k : k) * step, 0, 0); };
+            auto word = [&](int k) { return Chunk::word_at(at, k < n ? at_step(k) : to, to); };
+            uint4 w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = word(j);
+            for (int k = 0; k < n; k += 4) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (k + j >= n) break;
+                    f(at_step(k + j), w[j]);
+                    w[j] = word(k + j + 4);          // (in place: a copy would wait for it)
+                }
+            }
+        }
+        template <typename F>
+        __device__ __forceinline__ void words(F f) const { words_to<false>(f); }
+        template <typename F>
+        __device__ __forceinline__ void words_back(F f) const { words_to<true>(f); }
+    };
+
+    // x of the lane that a DPP move names, 0 where there is none or the row is masked.
+    template <int CTRL, int ROWS>
+    static __device__ __forceinline__ uint32_t dpp(uint32_t x) {
+        return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), CTRL, ROWS, 0xF, false));
+    }
+    template <int CTRL, int ROWS>
+    static __device__ __forceinline__ uint64_t dpp(uint64_t x) {
+        return static_cast<uint64_t>(dpp<CTRL, ROWS>(static_cast<uint32_t>(x >> 32))) << 32 | dpp<CTRL, ROWS>(static_cast<uint32_t>(x));
+    }
+    // Inclusive sum over a wave's lanes: shifts within rows of 16, then the last lane of
+    // a row to the next one, and of the first half to the second.
+    template <typename T>
+    static __device__ __forceinline__ T wave_sum_up(T v) {
+        v += dpp<0x111, 0xF>(v);
+        v += dpp<0x112, 0xF>(v);
+        v += dpp<0x114, 0xF>(v);
+        v += dpp<0x118, 0xF>(v);
+        v += dpp<0x142, 0xA>(v);
+        v += dpp<0x143, 0xC>(v);
+        return v;
+    }
+
+    // Inclusive sum over the block's threads.
+    template <typename T>
+    static __device__ __forceinline__ T block_scan(T v, T* parts) {
+        v = wave_sum_up(v);
+        const int wave = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 63) parts[wave] = v;
+        __syncthreads();
+        T before = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves - 1; ++w) before += w < wave ? parts[w] : 0;
+        __syncthreads();
+        return v + before;
+    }
+
+    template <typename T>
+    static __device__ __forceinline__ T block_max(T v, T* parts) {
+        auto more = [](T a, T b) { return a > b ? a : b; };
+        v = more(v, dpp<0x111, 0xF>(v));
+        v = more(v, dpp<0x112, 0xF>(v));
+        v = more(v, dpp<0x114, 0xF>(v));
+        v = more(v, dpp<0x118, 0xF>(v));
+        v = more(v, dpp<0x142, 0xA>(v));
+        v = more(v, dpp<0x143, 0xC>(v));
+        if ((threadIdx.x & 63) == 63) parts[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = parts[0];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) v = more(v, parts[w]);
+        __syncthreads();
+        return uniform(v);
+    }
+
+    // Running sums of mass and count [kThreads * PER], from f(i, mass, count) to g(i, ..).
+    template <int PER, typename F, typename G>
+    static __device__ __forceinline__ void run_up(uint64_t* parts64, uint32_t* parts32, F f, G g) {
+        uint64_t m[PER], mass = 0;
+        uint32_t c[PER], count = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            f(PER * threadIdx.x + j, m[j], c[j]);
+            mass += m[j];
+            count += c[j];
+        }
+        uint64_t before = block_scan(mass, parts64) - mass;
+        uint32_t ahead = block_scan(count, parts32) - count;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            before += m[j];
+            ahead += c[j];
+            g(PER * threadIdx.x + j, before, ahead);
+        }
+        __syncthreads();
+    }
+
+    // First bin whose running sum passes the target (some bin does).
+    template <typename T>
+    static __device__ __forceinline__ int first_past(const T* run, int n, T target, Shared& s) {
+        for (int i = threadIdx.x; i < n; i += kThreads)
+            if (run[i] > target && (i == 0 || run[i - 1] <= target)) s.found32[0] = i;
+        __syncthreads();
+        const int b = uniform(s.found32[0]);
+        __syncthreads();
+        return b;
+    }
+
+    // The smallest key in (kKeyNone, top] for which holds() is true (it stays true from
+    // there on, and holds for top), by the 64 lanes of a wave.
+    template <typename F>
+    static __device__ __forceinline__ uint32_t first_key(uint32_t top, F holds) {
+        uint32_t lo = kKeyNone, hi = top;                // not at lo, at hi
+        while (hi - lo > 1) {
+            const uint32_t step = (hi - lo - 1) / 64 + 1;
+            const uint64_t at = static_cast<uint64_t>(lo) + static_cast<uint64_t>(step) * ((threadIdx.x & 63) + 1);
+            const uint64_t votes = __ballot(at >= hi || holds(static_cast<uint32_t>(at)));
+            const uint32_t n = __builtin_ctzll(votes);   // (the last lane is at hi or behind it)
+            const uint64_t next = static_cast<uint64_t>(lo) + static_cast<uint64_t>(step) * (n + 1);
+            lo += step * n;
+            hi = next < hi ? static_cast<uint32_t>(next) : hi;
+        }
+        return hi;
+    }
+
+    // m in units of a bin i below the largest, in those of the largest, and back.
+    static __device__ __forceinline__ uint64_t to_top(uint64_t m, int i, const Shared& s) {
+        return i == 0 ? m : __umul64hi(m, s.down[i & 31]) << 1 >> (i >> 5);      // m below 2^63
+    }
+    static __device__ __forceinline__ uint64_t from_top(uint64_t m, int i, uint64_t most, const Shared& s) {
+        if (i == 0) return m;
+        const double x = ldexp(static_cast<double>(m) * s.up[i & 31], i >> 5);   // (2^-52 of it is far below what bins round)
+        return x < static_cast<double>(most) ? static_cast<uint64_t>(x) : most;
+    }
+
+    // f(index) for the elements with keys from lo_key to hi_key.
+    template <typename F>
+    static __device__ __forceinline__ void in_range(const Row& row, uint32_t lo_key, uint32_t hi_key, F f) {
+        const float lo = logit_of(lo_key), hi = logit_of(hi_key);
+        auto in = [&](uint4 word, int e) {
+            const float v = Chunk::value(word, e);
+            return __builtin_amdgcn_fmed3f(v, lo, hi) == v;
+        };
+        row.words_back([&](int i0, uint4 word) {
+            bool any = false;
+#pragma unroll
+            for (int e = 0; e < Chunk::N; ++e) any |= in(word, e);
+            if (!__any(any)) return;
+            uint32_t bits = 0;
+#pragma unroll
+            for (int e = 0; e < Chunk::N; ++e) bits |= in(word, e) ? 1u << e : 0;
+            while (bits) {
+                f(i0 + __builtin_ctz(bits));
+                bits &= bits - 1;
             }
         });
-        hi = static_cast<uint32_t>(block_max(top, s.part64));
-        lo = 0xFFFFFFFFu - static_cast<uint32_t>(block_max(low, s.part64));
     }
-    while (n > kList) {
-        const uint32_t range = hi - lo;
-        const int shift = range < kSub ? 0 : 32 - __builtin_clz(range) - 11;
-        const uint32_t start = hi;
+
+    // How many of the n elements come before one, and their mass.  The arrays hold
+    // room for 7 more.
+    static __device__ __forceinline__ void rank_of(uint64_t mine, const uint64_t* order, const uint64_t* mass, uint32_t n, uint32_t& rank,
+                                            uint64_t& ahead) {
+        rank = 0;
+        ahead = 0;
+        for (uint32_t e0 = 0; e0 < n; e0 += 8) {
+            uint64_t o[8], m[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                o[e] = order[e0 + e];
+                m[e] = mass[e0 + e];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const bool first = o[e] < mine && e0 + e < n;
+                ahead += first ? m[e] : 0;
+                rank += first;
+            }
+        }
+    }
+
+    struct Range {
+        uint32_t lo, hi;
+    };
+    // Keys of the bin i below the largest.
+    static __device__ __forceinline__ Range keys_of(const Scale& sc, uint32_t top_key, int i, Shared& s) {
+        if (sc.lone) return {top_key, top_key};
+        const int wave = threadIdx.x >> 6;
+        if (wave < 2) {
+            const double bin = sc.top - i + wave;        // (behind bin 0's keys there are none)
+            const uint32_t k = first_key(top_key, [&](uint32_t key) { return bin_at(sc, logit_of(key)) >= bin; });
+            if ((threadIdx.x & 63) == 0) s.found32[wave] = k;
+        }
+        __syncthreads();
+        const Range range{uniform(s.found32[0]), i == 0 ? top_key : uniform(s.found32[1]) - 1};
+        __syncthreads();
+        return range;
+    }
+
+    // Mass and count of the elements with keys in the range.
+    static __device__ __forceinline__ void sum_of(const Row& row, const Scale& sc, Range range, Shared& s, uint64_t& mass,
+                                           uint32_t& count) {
+        uint64_t m = 0;
+        uint32_t n = 0;
+        in_range(row, range.lo, range.hi, [&](int i) {
+            m += mass_of(sc, row.value(i));
+            ++n;
+        });
+        m = block_scan(m, s.part64);
+        n = block_scan(n, s.part32);
+        if (threadIdx.x == kThreads - 1) {
+            s.found64[0] = m;
+            s.found32[0] = n;
+        }
+        __syncthreads();
+        mass = uniform(s.found64[0]);
+        count = uniform(s.found32[0]);
+        __syncthreads();
+    }
+
+    // Lists the elements with keys in the range: their orders and masses (in their bins'
+    // units).  Returns how many there are; past kList only some are listed.
+    static __device__ __forceinline__ uint32_t list_range(const Row& row, const Scale& sc, Range range, Shared& s) {
+        if (threadIdx.x == 0) s.found32[1] = 0;
+        __syncthreads();
+        in_range(row, range.lo, range.hi, [&](int i) {
+            const uint32_t n = atomicAdd(&s.found32[1], 1u);
+            if (n < kList) s.list.order[n] = static_cast<uint32_t>(i);
+        });
+        __syncthreads();
+        const uint32_t n = uniform(s.found32[1]);
+        for (uint32_t e = threadIdx.x; e < n && e < kList; e += kThreads) {
+            const uint32_t i = static_cast<uint32_t>(s.list.order[e]);
+            const float v = row.value(static_cast<int>(i));
+            s.list.order[e] = static_cast<uint64_t>(~key_of(v)) << 32 | i;
+            s.list.mass[e] = mass_of(sc, v);
+        }
+        __syncthreads();
+        return n;
+    }
+
+    // Of the list's n elements the one at which the running count or mass passes left:
+    // its order is in s.found64[1], the mass up to and with it in [0]; returns the mass
+    // of those left out before.  While there are many, 512 parts of their range at a time.
+    static __device__ __forceinline__ uint64_t of_list(bool by_count, uint64_t left, uint32_t n, Shared& s) {
+        const uint32_t t = threadIdx.x, all = n;
+        uint64_t lo = 0, hi = ~0ull, passed = 0;
+        while (n > kFew) {
+            uint64_t most = 0, least = 0;            // (the least by its complement)
+            for (uint32_t e = t; e < all; e += kThreads) {
+                const uint64_t o = s.list.order[e];
+                if (o < lo || o > hi) continue;
+                most = o > most ? o : most;
+                least = ~o > least ? ~o : least;
+            }
+            hi = block_max(most, s.part64);
+            lo = ~block_max(least, s.part64);
+            const uint64_t width = hi - lo;
+            const int shift = width < kThreads ? 0 : 64 - __builtin_clzll(width) - __builtin_ctz(kThreads);
+            s.list.part.mass[t] = 0;
+            s.list.part.count[t] = 0;
+            __syncthreads();
+            for (uint32_t e = t; e < all; e += kThreads) {
+                const uint64_t o = s.list.order[e];
+                if (o < lo || o > hi) continue;
+                const uint32_t b = static_cast<uint32_t>((o - lo) >> shift);
+                atomicAdd(reinterpret_cast<unsigned long long*>(&s.list.part.mass[b]), s.list.mass[e]);
+                atomicAdd(&s.list.part.count[b], 1u);
+            }
+            __syncthreads();
+            const uint64_t m = s.list.part.mass[t];
+            const uint32_t c = s.list.part.count[t];
+            const uint64_t mass = block_scan(m, s.part64);
+            const uint32_t count = block_scan(c, s.part32);
+            if (by_count ? count > left && count - c <= left : mass > left && mass - m <= left) {
+                s.found64[0] = mass - m;
+                s.found32[0] = count - c;
+                s.found32[2] = c;
+                s.found32[3] = t;
+            }
+            __syncthreads();
+            passed += uniform(s.found64[0]);
+            left -= by_count ? uniform(s.found32[0]) : uniform(s.found64[0]);
+            n = uniform(s.found32[2]);
+            lo += static_cast<uint64_t>(uniform(s.found32[3])) << shift;
+            const uint64_t part = (1ull << shift) - 1;
+            hi = hi - lo > part ? lo + part : hi;
+            __syncthreads();
+        }
+        if (t == 0) s.found32[0] = 0;
+        __syncthreads();
+        for (uint32_t e = t; e < all; e += kThreads) {
+            const uint64_t o = s.list.order[e];
+            if (o < lo || o > hi) continue;
+            const uint32_t at = atomicAdd(&s.found32[0], 1u);
+            s.list.part.few_order[at] = o;
+            s.list.part.few_mass[at] = s.list.mass[e];
+        }
+        __syncthreads();
+        if (t < n) {
+            const uint64_t mine = s.list.part.few_order[t], m = s.list.part.few_mass[t];
+            uint64_t ahead;
+            uint32_t rank;
+            rank_of(mine, s.list.part.few_order, s.list.part.few_mass, n, rank, ahead);
+            if (by_count ? rank == left : ahead <= left && left < ahead + m) {
+                s.found64[0] = ahead + m;
+                s.found64[1] = mine;
+            }
+        }
+        __syncthreads();
+        return passed;
+    }
+
+    // The part (of 2048) of the range in which the running count or mass passes left: the
+    // range becomes that part, and what comes before it in the range moves from left to
+    // passed (the mass).  Returns true where the part is a single key: nth is then the
+    // place among its elements, one their mass.
+    static __device__ __forceinline__ bool narrow(const Row& row, const Scale& sc, bool by_count, Range& range, uint64_t& left,
+                                           uint64_t& passed, uint32_t& nth, uint64_t& one, Shared& s) {
+        const uint32_t width = range.hi - range.lo;
+        const int shift = width < kSub ? 0 : 21 - __builtin_clz(width);
         for (int i = threadIdx.x; i < kSub; i += kThreads) {
             s.sub.mass[i] = 0;
             s.sub.count[i] = 0;
         }
         __syncthreads();
-        scan_row<DT>(r, [&](int, float v) {
-            double y;
-            if (member(v, y)) {
-                const uint32_t b = (start - key_of(v)) >> shift;
-                atomicAdd(reinterpret_cast<unsigned long long*>(&s.sub.mass[b]), mass_of(y, s.exp2_tab));
-                atomicAdd(&s.sub.count[b], 1u);
-            }
+        in_range(row, range.lo, range.hi, [&](int i) {
+            const float v = row.value(i);
+            const uint32_t b = (range.hi - key_of(v)) >> shift;
+            atomicAdd(reinterpret_cast<unsigned long long*>(&s.sub.mass[b]), mass_of(sc, v));
+            atomicAdd(&s.sub.count[b], 1u);
         });
         __syncthreads();
-        run_up(s.sub.mass, s.sub.count, kSub, s);
-        const int b = BY_COUNT ? first_past<uint32_t>(s.sub.count, kSub, static_cast<uint32_t>(target) - count_before, s)
-                               : first_past<uint64_t>(s.sub.mass, kSub, target - mass_before, s);
-        n = s.sub.count[b] - (b ? s.sub.count[b - 1] : 0);
-        const uint64_t here = s.sub.mass[b] - (b ? s.sub.mass[b - 1] : 0);
-        mass_before += b ? s.sub.mass[b - 1] : 0;
-        count_before += b ? s.sub.count[b - 1] : 0;
-        const uint32_t was_lo = lo;
-        hi = start - (static_cast<uint32_t>(b) << shift);
-        const uint32_t width = (1u << shift) - 1;
-        lo = hi - was_lo > width ? hi - width : was_lo;
+        run_up<kSub / kThreads>(
+            s.part64, s.part32,
+            [&](int i, uint64_t& m, uint32_t& c) {
+                m = s.sub.mass[i];
+                c = s.sub.count[i];
+            },
+            [&](int i, uint64_t m, uint32_t c) {
+                s.sub.mass[i] = m;
+                s.sub.count[i] = c;
+            });
+        const int b = by_count ? first_past(s.sub.count, kSub, static_cast<uint32_t>(left), s)
+                               : first_past(s.sub.mass, kSub, left, s);
+        const uint64_t mass_b = b ? uniform(s.sub.mass[b - 1]) : 0, mass_here = uniform(s.sub.mass[b]) - mass_b;
+        const uint32_t count_b = b ? uniform(s.sub.count[b - 1]) : 0, count_here = uniform(s.sub.count[b]) - count_b;
+        passed += mass_b;
+        left -= by_count ? count_b : mass_b;
+        const uint32_t hi = range.hi - (static_cast<uint32_t>(b) << shift), part = (1u << shift) - 1;
+        range.lo = hi - range.lo > part ? hi - part : range.lo;
+        range.hi = hi;
         __syncthreads();
-        if (shift == 0) {
-            // one key: equal weights (a weight of 0 passes no target)
-            const uint64_t w = here / n;
-            const uint32_t nth = BY_COUNT ? static_cast<uint32_t>(target) - count_before
-                                          : static_cast<uint32_t>((target - mass_before) / w);
-            Place p{mass_before + (nth + 1) * w, hi, -1};
-            if (INDEX) {
-                // the nth element of that key, 8192 elements at a time
-                uint32_t seen = 0;
-                const int full = r.vocab & ~7;
-                for (int i0 = 0; i0 < r.vocab; i0 += 8 * kThreads) {
-                    const int i = i0 + 8 * threadIdx.x;
-                    uint32_t bits = 0;
-                    if (i < full) {
-                        float v[8];
-                        load8<DT>(r.at + static_cast<int64_t>(i) * (DT == F32 ? 4 : 2), v);
+        if (range.lo != range.hi) return false;
+        one = mass_here / count_here;
+        nth = static_cast<uint32_t>(by_count ? left : left / one);
+        return true;
+    }
+
+    // Index of the nth element with that key.
+    static __device__ __forceinline__ int nth_of(const Row& row, uint32_t key, uint32_t nth, Shared& s) {
+        constexpr int N = Chunk::N;
+        uint32_t seen = 0;
+        row.words([&](int i0, uint4 word) {
+            if (seen > nth) return;
+            uint32_t bits = 0;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) bits |= key_of(v[j]) == hi ? 1u << j : 0;
-                    } else {
-                        for (int j = 0; j < 8 && i + j < r.vocab; ++j) bits |= key_of(load_one<DT>(r.at, i + j)) == hi ? 1u << j : 0;
+            for (int e = 0; e < N; ++e) bits |= key_of(Chunk::value(word, e)) == key ? 1u << e : 0;
+            const uint32_t here = __popc(bits), upto = seen + block_scan(here, s.part32);
+            if (nth >= upto - here && nth < upto) {
+                for (uint32_t k = upto - here; k < nth; ++k) bits &= bits - 1;
+                s.found32[1] = i0 + __builtin_ctz(bits);
+            }
+            if (threadIdx.x == kThreads - 1) s.found32[2] = upto;
+            __syncthreads();
+            seen = uniform(s.found32[2]);
+            __syncthreads();
+        });
+        const int i = uniform(static_cast<int>(s.found32[1]));
+        __syncthreads();
+        return i;
+    }
+
+    // floor(f * m), f in [0, 1) given in units of 2^-48; *exact: nothing was cut off.
+    static __device__ __forceinline__ uint64_t part_of(uint64_t f48, uint64_t m, bool* exact) {
+        const uint64_t hi = __umul64hi(f48, m), lo = f48 * m;
+        *exact = (lo & 0xFFFFFFFFFFFFull) == 0;
+        return hi << 16 | lo >> 48;
+    }
+
+    // Bins of the elements from row.from to row.to into s and the largest of them into
+    // sc; the largest key (kKeyNone: no element).
+    static __device__ __forceinline__ uint32_t fill_bins(const Row& row, bool with_count, Scale& sc, Shared& s) {
+        constexpr int N = Chunk::N;
+        for (int i = threadIdx.x; i < kSlots; i += kThreads) {
+            s.mass[i] = 0;
+            s.count[i] = 0;
+        }
+        uint32_t top_key = kKeyNone;
+        Chunk c;
+        c.load(row.at, row.from, row.to);
+        for (int from = row.from; from < row.to; from += Chunk::kSize) {
+            Chunk next;
+            next.load(row.at, from + Chunk::kSize, row.to);      // on its way meanwhile
+            float most = -__builtin_inff();
+            c.words([&](uint4 word) {
+#pragma unroll
+                for (int e = 0; e < N; ++e) most = fmaxf(most, Chunk::value(word, e));     // (a NaN is passed over)
+            });
+            const uint32_t k = block_max(key_of(most), s.part32);
+            if (k > top_key) {
+                const Scale was = sc;
+                set_top(sc, logit_of(k));
+                const double rise = sc.top - was.top;
+                if (top_key != kKeyNone) {
+                    if (sc.lone || was.lone || rise >= kSlots) {     // far above all before: the ring starts anew
+                        for (int i = threadIdx.x; i < kSlots; i += kThreads) {
+                            s.mass[i] = 0;
+                            s.count[i] = 0;
+                        }
+                    } else {                                         // slots between hold bins 64 octaves lower
+                        for (int i = threadIdx.x; i < static_cast<int>(rise); i += kThreads) {
+                            s.mass[slot_of(was.top + 1 + i)] = 0;
+                            s.count[slot_of(was.top + 1 + i)] = 0;
+                        }
                     }
-                    const uint32_t upto = seen + block_scan<uint32_t>(__popc(bits), s.part32);
-                    const uint32_t before = upto - __popc(bits);
-                    if (nth >= before && nth < upto) {
-                        for (uint32_t k = before; k < nth; ++k) bits &= bits - 1;
-                        s.found32[1] = i + __builtin_ctz(bits);
-                    }
-                    if (threadIdx.x == kThreads - 1) s.found32[2] = upto;
-                    __syncthreads();
-                    seen = s.found32[2];
-                    if (seen > nth) break;
-                    __syncthreads();
                 }
-                p.index = static_cast<int>(s.found32[1]);
+                top_key = k;
                 __syncthreads();
             }
-            return p;
+            if (top_key == kKeyNone) {
+                // nothing yet
+            } else if (sc.lone) {
+                c.words([&](uint4 word) {
+#pragma unroll
+                    for (int e = 0; e < N; ++e)
+                        if (Chunk::value(word, e) == sc.top_logit) {
+                            atomicAdd(reinterpret_cast<unsigned long long*>(&s.mass[slot_of(kMagic)]), kOne);
+                            if (with_count) atomicAdd(&s.count[slot_of(kMagic)], 1u);
+                        }
+                });
+            } else {
+                // (what lies below the window goes to slots of its own: no branch keeps the
+                // elements' arithmetic apart)
+                const double least = sc.top - kBins;
+                const int none = kSlots + static_cast<int>(threadIdx.x & 63);
+                const Series series;
+                c.words([&](uint4 word) {
+                    int slot[N];
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        const float v = Chunk::value(word, e);
+                        const double bin = bin_at(sc, v);
+                        slot[e] = bin > least ? slot_of(bin) : none;
+                        atomicAdd(reinterpret_cast<unsigned long long*>(&s.mass[slot[e]]), mass_in(series, sc, v, bin));
+                    }
+                    if (with_count) {
+#pragma unroll
+                        for (int e = 0; e < N; ++e) atomicAdd(&s.count[slot[e]], 1u);
+                    }
+                });
+            }
+            c = next;
         }
+        __syncthreads();
+        return top_key;
     }
 
-    // few: sorted by falling key, then rising index
-    if (threadIdx.x == 0) s.found32[1] = 0;
-    __syncthreads();
-    scan_row<DT>(r, [&](int i, float v) {
-        double y;
-        if (member(v, y)) s.list[atomicAdd(&s.found32[1], 1u)] = static_cast<uint64_t>(~key_of(v)) << 32 | static_cast<uint32_t>(i);
-    });
-    __syncthreads();
-    int pow2 = 64;
-    while (pow2 < static_cast<int>(n)) pow2 *= 2;
-    for (int i = n + threadIdx.x; i < pow2; i += kThreads) s.list[i] = ~0ull;
-    __syncthreads();
-    for (int k = 2; k <= pow2; k *= 2)
-        for (int j = k / 2; j; j /= 2) {
-            for (int e = threadIdx.x; e < pow2 / 2; e += kThreads) {
-                const int a = 2 * e - (e & (j - 1)), b = a + j;      // bit j of a is clear
-                const uint64_t x = s.list[a], z = s.list[b];
-                if ((x > z) == ((a & k) == 0)) {
-                    s.list[a] = z;
-                    s.list[b] = x;
+    // f in [0, 1) in units of 2^-48 (a NaN is 0).
+    static __device__ __forceinline__ uint64_t units_of(float f) {
+        return !(f > 0.f) ? 0 : f >= 1.f ? (1ull << 48) - 1 : static_cast<uint64_t>(static_cast<double>(f) * 0x1p48);
+    }
+    // The kept tokens are those before which less than top_p of the mass lies: the last
+    // is the first at which the running mass passes this.
+    static __device__ __forceinline__ uint64_t last_kept(float top_p, uint64_t mass) {
+        bool exact;
+        const uint64_t f = part_of(units_of(top_p), mass, &exact);
+        return exact && f ? f - 1 : f;
+    }
+
+    struct Settings {
+        float min_p, top_p, u;
+        uint32_t top_k;            // 2^32 - 1: none
+    };
+    static __device__ __forceinline__ Settings settings_of(const SampleArgs& a, int r) {
+        return {a.min_p ? a.min_p[r] : 0.f, a.top_p ? a.top_p[r] : 1.f, a.u[r],
+                counts(a, r) ? static_cast<uint32_t>(a.top_k[r]) : 0xFFFFFFFFu};
+    }
+
+    // The smallest key with w >= min_p.
+    static __device__ __forceinline__ uint32_t least_key(const Scale& sc, uint32_t top_key, float min_p, Shared& s) {
+        if (threadIdx.x < 64) {
+            const float top = logit_of(top_key);
+            const double least = -log2(static_cast<double>(min_p)) * 32.0;
+            const uint32_t k = first_key(top_key, [&](uint32_t key) {
+                const float v = logit_of(key);
+                return v == top || (static_cast<double>(top) - static_cast<double>(v)) * sc.c <= least;
+            });
+            if (threadIdx.x == 0) s.found32[3] = k;
+        }
+        __syncthreads();
+        const uint32_t k = uniform(s.found32[3]);
+        __syncthreads();
+        return k;
+    }
+
+    struct Token {
+        uint32_t key;
+        int index;
+        uint64_t mass;             // of all that was kept
+    };
+
+    // The list's n <= kNear elements, each at its rank, and the token.  All that the
+    // filters keep is among them; whole is the row's mass where the list may end before
+    // what top-p counts, else 0.
+    static __device__ __forceinline__ Token among_list(const Scale& sc, uint32_t n, const Settings& set, uint32_t least,
+                                                uint64_t whole, Shared& s) {
+        const uint32_t t = threadIdx.x;
+        uint64_t mine = 0;
+        if (t < n) {
+            mine = s.list.order[t];
+            s.list.mass[t] = to_top(s.list.mass[t], depth_of(sc, logit_of(~static_cast<uint32_t>(mine >> 32))), s);
+        }
+        __syncthreads();
+        if (t < n) {
+            uint64_t ahead;
+            uint32_t rank;
+            rank_of(mine, s.list.order, s.list.mass, n, rank, ahead);
+            s.list.sorted.order[rank] = mine;
+            s.list.sorted.ahead[rank] = ahead;
+            if (rank == n - 1) s.found64[0] = ahead + s.list.mass[t];
+        }
+        __syncthreads();
+        mine = t < n ? s.list.sorted.order[t] : ~0ull;
+        const uint64_t all = s.found64[0], ahead = t < n ? s.list.sorted.ahead[t] : all;
+        auto upto = [&](uint32_t kept) { return kept < n ? s.list.sorted.ahead[kept] : all; };
+        uint32_t kept = __syncthreads_count(t < n && ~static_cast<uint32_t>(mine >> 32) >= least);
+        kept = set.top_k < kept ? set.top_k : kept;
+        uint64_t mass = whole ? whole : upto(kept);
+        if (set.top_p < 1.f) {
+            kept = __syncthreads_count(t < kept && ahead <= last_kept(set.top_p, mass));
+            mass = upto(kept);
+        }
+        bool exact;
+        const uint64_t goal = part_of(units_of(set.u), mass, &exact);
+        const uint32_t at = __syncthreads_count(t < kept && upto(t + 1) <= goal);
+        mine = s.list.sorted.order[at];
+        return {~static_cast<uint32_t>(mine >> 32), static_cast<int>(static_cast<uint32_t>(mine)), mass};
+    }
+
+    static __device__ __forceinline__ void store_token(const SampleArgs& a, int r, const Scale& sc, const Token& token) {
+        if (threadIdx.x != 0) return;
+        a.token[r] = token.index;
+        if (!a.logprob) return;
+        const float v = logit_of(token.key);
+        const double share = static_cast<double>(mass_of(sc, v)) / static_cast<double>(token.mass);
+        const double y = log(share) - depth_of(sc, v) * (0.6931471805599453 / 32);
+        a.logprob[r] = static_cast<float>(y < 0.0 ? y : 0.0);
+    }
+
+    // The largest logit of a row.
+    static __device__ __forceinline__ uint32_t top_key_of(const Row& row, Shared& s) {
+        float most = -__builtin_inff();
+        row.words([&](int, uint4 word) {
+#pragma unroll
+            for (int e = 0; e < Chunk::N; ++e) most = fmaxf(most, Chunk::value(word, e));
+        });
+        return block_max(key_of(most), s.part32);
+    }
+
+    static __device__ __forceinline__ void store_largest(const SampleArgs& a, int r, uint64_t best) {
+        if (threadIdx.x != 0) return;
+        const bool none = static_cast<uint32_t>(best >> 32) == kKeyNone;
+        a.token[r] = none ? -1 : static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(best));
+        if (a.logprob) a.logprob[r] = none ? __builtin_nanf("") : 0.f;
+    }
+
+    // The smallest key that a small top-k can reach, from counts alone, over bins in fp32
+    // (rounding is monotonic, so they are stretches of the order).  False where those keys
+    // are too many.
+    static __device__ __forceinline__ bool reach_of(const Row& row, const Scale& sc, uint32_t top_key, uint32_t top_k, Shared& s,
+                                             uint32_t& from) {
+        constexpr int N = Chunk::N;
+        const float scale = static_cast<float>(sc.c), base = logit_of(top_key) * scale;
+        auto place = [&](float v) { return fmaf(-v, scale, base); };      // (no number for a NaN; what is not below kBins is left out)
+        for (int i = threadIdx.x; i < kSlots + 64; i += kThreads) s.count[i] = 0;
+        __syncthreads();
+        row.words([&](int, uint4 word) {
+            int slot[N];
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float d = place(Chunk::value(word, e));
+                slot[e] = d < static_cast<float>(kBins) ? static_cast<int>(fmaxf(d, 0.f)) : kSlots + static_cast<int>(threadIdx.x & 63);
+            }
+#pragma unroll
+            for (int e = 0; e < N; ++e) atomicAdd(&s.count[slot[e]], 1u);
+        });
+        __syncthreads();
+        run_up<kSlots / kThreads>(
+            s.part64, s.part32,
+            [&](int i, uint64_t& m, uint32_t& c) {
+                m = 0;
+                c = i < kBins ? s.count[i] : 0;
+            },
+            [&](int i, uint64_t, uint32_t c) {
+                if (i < kBins) s.run_count[i] = c;
+            });
+        if (s.run_count[kBins - 1] < top_k) return false;
+        const int reach = first_past(s.run_count, kBins, top_k - 1, s);
+        if (s.run_count[reach] > kNear) return false;
+        if (threadIdx.x < 64) {
+            const uint32_t k = first_key(top_key, [&](uint32_t key) { return place(logit_of(key)) < static_cast<float>(reach + 1); });
+            if (threadIdx.x == 0) s.found32[3] = k;
+        }
+        __syncthreads();
+        from = uniform(s.found32[3]);
+        __syncthreads();
+        return true;
+    }
+
+    // The row's token.  fill() brings its bins and largest logit; top_key and sc's top are
+    // known before only with `known`.
+    template <typename F>
+    static __device__ __forceinline__ void choose(const SampleArgs& a, int r, const Row& row, Scale& sc, uint32_t top_key,
+                                           bool known, Shared& s, F fill) {
+        const Settings set = settings_of(a, r);
+        const bool counting = set.top_k != 0xFFFFFFFFu;
+        uint32_t least = kKeyNone + 1;                   // keys from here on pass min-p
+        int least_bin = kBins;
+        int step = -1;                                   // what the list is for: all (-1), top-k, top-p, the token
+        bool filled = false;
+        Range range{0, 0};
+        if (set.min_p > 0.f || set.top_k <= kNear / 2) {
+            if (!known) {
+                top_key = top_key_of(row, s);
+                if (top_key != kKeyNone) set_top(sc, logit_of(top_key));
+            }
+            if (top_key == kKeyNone) {
+                store_largest(a, r, static_cast<uint64_t>(kKeyNone) << 32);
+                return;
+            }
+            range = {0, top_key};
+            if (set.min_p > 0.f) range.lo = least = least_key(sc, top_key, set.min_p, s);
+            else if (!reach_of(row, sc, top_key, set.top_k, s, range.lo)) range.lo = 0;
+        }
+        Token token{};
+        uint64_t mass = 0, whole = 0, before = 0, left = 0, passed = 0;
+        uint32_t all = 0;
+        int bin = 0;
+        while (true) {
+            if (!filled && (step >= 0 || range.lo == 0)) {
+                top_key = fill();
+                filled = true;
+                if (top_key == kKeyNone) {
+                    store_largest(a, r, static_cast<uint64_t>(kKeyNone) << 32);
+                    return;
+                }
+                run_up<kSlots / kThreads>(
+                    s.part64, s.part32,
+                    [&](int i, uint64_t& m, uint32_t& c) {
+                        m = 0;
+                        c = 0;
+                        if (i >= kBins) return;
+                        const uint64_t raw = s.mass[slot_of(sc.top - i)];
+                        m = to_top(raw, i, s);
+                        if (counting) {
+                            c = s.count[slot_of(sc.top - i)];
+                        } else {
+                            // masses are within 1.1% of 2^44
+                            const float n = static_cast<float>(raw) * 0x1p-44f;
+                            c = static_cast<uint32_t>(rintf(n) + floorf(n * (1.f / 45)));
+                        }
+                    },
+                    [&](int i, uint64_t m, uint32_t c) {
+                        if (i >= kBins) return;
+                        s.run_mass[i] = m;
+                        s.run_count[i] = c;
+                    });
+                mass = uniform(s.run_mass[kBins - 1]);
+                all = uniform(s.run_count[kBins - 1]);
+                if (set.min_p > 0.f) {
+                    const double below = uniform(sc.lone ? least == top_key ? 0.0 : kBins : sc.top - bin_at(sc, logit_of(least)));
+                    least_bin = below < kBins ? static_cast<int>(below) : kBins;
+                }
+                // the last bin that any of it can reach
+                int reach = least_bin < kBins ? least_bin : kBins - 1;
+                if (set.top_k <= all) {
+                    const int b = first_past(s.run_count, kBins, set.top_k - 1, s);
+                    reach = b < reach ? b : reach;
+                } else if (least_bin == kBins && set.top_p < 1.f) {
+                    reach = first_past(s.run_mass, kBins, last_kept(set.top_p, mass), s);
+                    whole = mass;
+                }
+                if (s.run_count[reach] <= kNear) {
+                    step = -1;
+                    range = {keys_of(sc, top_key, reach, s).lo, top_key};
+                } else {
+                    step = 0;
+                    if (least_bin < kBins) {
+                        uint64_t m;
+                        uint32_t n;
+                        sum_of(row, sc, {least, keys_of(sc, top_key, least_bin, s).hi}, s, m, n);
+                        mass = (least_bin ? uniform(s.run_mass[least_bin - 1]) : 0) + uniform(to_top(m, least_bin, s));
+                        all = (least_bin ? uniform(s.run_count[least_bin - 1]) : 0) + n;
+                    }
                 }
             }
-            __syncthreads();
+            if (step >= 0 && range.lo == 0) {
+                // the next question: its target, bin, and what of the target lies in the bin
+                uint64_t target;
+                if (step == 0) {
+                    if (set.top_k >= all) {
+                        step = 1;
+                        continue;
+                    }
+                    target = set.top_k - 1;
+                } else if (step == 1) {
+                    if (!(set.top_p < 1.f)) {
+                        step = 2;
+                        continue;
+                    }
+                    target = last_kept(set.top_p, mass);
+                } else {
+                    bool exact;
+                    target = part_of(units_of(set.u), mass, &exact);
+                }
+                bin = step == 0 ? first_past(s.run_count, kBins, static_cast<uint32_t>(target), s)
+                                : first_past(s.run_mass, kBins, target, s);
+                before = bin ? uniform(s.run_mass[bin - 1]) : 0;
+                left = step == 0 ? target - (bin ? uniform(s.run_count[bin - 1]) : 0)
+                                 : uniform(from_top(target - before, bin, s.mass[slot_of(sc.top - bin)] - 1, s));
+                passed = 0;
+                range = keys_of(sc, top_key, bin, s);
+            }
+            const uint32_t n = list_range(row, sc, range, s);
+            if (step < 0) {
+                if (n <= kNear) {
+                    token = among_list(sc, n, set, least, whole, s);
+                    break;
+                }
+                range.lo = 0;                            // too many after all
+                step = 0;
+                continue;
+            }
+            uint32_t nth;
+            uint64_t one, upto;
+            if (n <= kList) {
+                passed += of_list(step == 0, left, n, s);
+                upto = uniform(s.found64[0]);
+                token.key = ~uniform(static_cast<uint32_t>(s.found64[1] >> 32));
+                token.index = uniform(static_cast<int>(static_cast<uint32_t>(s.found64[1])));
+                __syncthreads();
+            } else {
+                if (!narrow(row, sc, step == 0, range, left, passed, nth, one, s)) continue;
+                upto = (nth + 1) * one;
+                token.key = range.hi;
+                if (step == 2) token.index = nth_of(row, range.hi, nth, s);
+            }
+            if (step == 2) {
+                token.mass = mass;
+                break;
+            }
+            mass = before + uniform(to_top(passed + upto, bin, s));
+            ++step;
+            range.lo = 0;
         }
-    const int i = 2 * threadIdx.x;
-    uint64_t w[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-        w[j] = i + j < static_cast<int>(n) ? mass_of(y_of(r, logit_of(~static_cast<uint32_t>(s.list[i + j] >> 32))), s.exp2_tab) : 0;
-    uint64_t run = mass_before + block_scan<uint64_t>(w[0] + w[1], s.part64) - w[0] - w[1];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const uint64_t next = run + w[j];
-        const bool here = BY_COUNT ? count_before + i + j == target : run <= target && next > target;
-        if (i + j < static_cast<int>(n) && here) {
-            s.found64[0] = next;
-            s.found64[1] = s.list[i + j];
-        }
-        run = next;
+        store_token(a, r, sc, token);
     }
-    __syncthreads();
-    Place p{s.found64[0], ~static_cast<uint32_t>(s.found64[1] >> 32), static_cast<int>(static_cast<uint32_t>(s.found64[1]))};
-    __syncthreads();
-    return p;
+
+    // The largest key of a row and the first element that has it.
+    static __device__ __forceinline__ uint64_t largest(const Row& row) {
+        uint64_t best = 0;
+        row.words([&](int i0, uint4 word) {
+#pragma unroll
+            for (int e = 0; e < Chunk::N; ++e) {
+                const uint64_t x = static_cast<uint64_t>(key_of(Chunk::value(word, e))) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(i0 + e));
+                best = x > best ? x : best;
+            }
+        });
+        return best;
+    }
+    static __device__ __forceinline__ void fill_tables(Shared& s) {
+        const int t = threadIdx.x;
+        if (t < 32) {
+            s.down[t] = static_cast<uint64_t>(exp2(-t / 32.0) * 0x1p63);
+            s.up[t] = exp2(t / 32.0);
+        }
+    }
+};
+
+__device__ __forceinline__ float temperature_of(const SampleArgs& a, int r) { return a.temperature ? a.temperature[r] : 1.f; }
+
+template <int DT>
+__device__ __forceinline__ const char* row_at(const SampleArgs& a, int r) {
+    return static_cast<const char*>(a.logits) + static_cast<int64_t>(r) * a.ld * (DT == F32 ? 4 : 2);
 }
 
-// floor(f * m), f in [0, 1) given in units of 2^-48; *exact: nothing was cut off.
-__device__ __forceinline__ uint64_t part_of(uint64_t f48, uint64_t m, bool* exact) {
-    const uint64_t hi = __umul64hi(f48, m), lo = f48 * m;
-    *exact = (lo & 0xFFFFFFFFFFFFull) == 0;
-    return hi << 16 | lo >> 48;
+// A block to a row.
+template <int DT>
+__global__ __launch_bounds__(kThreads, 4) void sample_kernel(SampleArgs a) {
+    using S = Sampler<DT>;
+    __shared__ typename S::Shared s;
+    const int r = blockIdx.x;
+    const typename S::Row row{row_at<DT>(a, r), 0, a.vocab};
+    const float temp = temperature_of(a, r);
+    if (!(temp > 0.f)) {
+        S::store_largest(a, r, S::block_max(S::largest(row), s.part64));
+        return;
+    }
+    S::fill_tables(s);
+    Scale sc = scale_of(temp);
+    S::choose(a, r, row, sc, kKeyNone, false, s, [&] { return S::fill_bins(row, counts(a, r), sc, s); });
+}
+
+// What a part of a row leaves for the second launch.
+struct Part {
+    uint64_t best;      // at temperature 0: the largest key and its first place; else the key only
+    double top;
+    uint64_t mass[kBins];
+    uint32_t count[kBins];
+};
+static_assert(sizeof(Part) == kSamplePartBytes && kSamplePartBytes % 16 == 0, "workspace of a part");
+
+// A block to a part of a row: its bins, from its own largest one down.
+template <int DT>
+__global__ __launch_bounds__(kThreads, 4) void sample_part_kernel(SampleArgs a, int parts, int size, Part* out) {
+    using S = Sampler<DT>;
+    __shared__ typename S::Shared s;
+    const int r = blockIdx.x / parts, p = blockIdx.x % parts, from = p * size;
+    const typename S::Row row{row_at<DT>(a, r), from, from + size < a.vocab ? from + size : a.vocab};
+    const float temp = temperature_of(a, r);
+    Part& o = out[blockIdx.x];
+    if (!(temp > 0.f)) {
+        const uint64_t best = S::block_max(S::largest(row), s.part64);
+        if (threadIdx.x == 0) o.best = best;
+        return;
+    }
+    Scale sc = scale_of(temp);
+    const bool counting = counts(a, r);
+    const uint32_t top = S::fill_bins(row, counting, sc, s);
+    if (threadIdx.x == 0) {
+        o.best = static_cast<uint64_t>(top) << 32;
+        o.top = sc.lone ? -__builtin_inf() : sc.top;
+    }
+    for (int i = threadIdx.x; i < kBins; i += kThreads) {
+        o.mass[i] = s.mass[slot_of(sc.top - i)];
+        if (counting) o.count[i] = s.count[slot_of(sc.top - i)];
+    }
+}
+
+// The parts of a row met.
+template <int DT>
+__global__ __launch_bounds__(kThreads, 4) void sample_join_kernel(SampleArgs a, int parts, const Part* in) {
+    using S = Sampler<DT>;
+    __shared__ typename S::Shared s;
+    const int r = blockIdx.x, t = threadIdx.x;
+    in += static_cast<int64_t>(r) * parts;
+    uint64_t best = 0;
+    for (int p = t; p < parts; p += kThreads) best = in[p].best > best ? in[p].best : best;
+    best = S::block_max(best, s.part64);
+    const float temp = temperature_of(a, r);
+    const uint32_t top = static_cast<uint32_t>(best >> 32);
+    if (!(temp > 0.f) || top == kKeyNone) {
+        S::store_largest(a, r, best);
+        return;
+    }
+    S::fill_tables(s);
+    const typename S::Row row{row_at<DT>(a, r), 0, a.vocab};
+    Scale sc = scale_of(temp);
+    set_top(sc, logit_of(top));
+    S::choose(a, r, row, sc, top, true, s, [&] {
+        // where the parts' bins lie below the row's (far below: at kBins)
+        const bool counting = counts(a, r);
+        for (int p = t; p < parts; p += kThreads) {
+            const uint32_t key = static_cast<uint32_t>(in[p].best >> 32);
+            const double below = sc.lone ? 0.0 : sc.top - in[p].top;       // (a lone part is far below)
+            s.offset[p] = key == kKeyNone || (sc.lone && key != top) || !(below < kBins) ? kBins : static_cast<int>(below);
+        }
+        __syncthreads();
+        for (int i = t; i < kBins; i += kThreads) {
+            uint64_t m = 0;
+            uint32_t c = 0;
+#pragma unroll 4
+            for (int p = 0; p < parts; ++p) {
+                const int at = i - s.offset[p];
+                const uint64_t pm = in[p].mass[at < 0 ? 0 : at];
+                m += at < 0 ? 0 : pm;
+                if (counting) c += at < 0 ? 0 : in[p].count[at];
+            }
+            s.mass[slot_of(sc.top - i)] = m;
+            s.count[slot_of(sc.top - i)] = c;
+        }
+        __syncthreads();
+        return top;
+    });
 }
 
 template <int DT>
-__global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
-    __shared__ Shared s;
-    const int row = blockIdx.x, t = threadIdx.x;
-    Row r;
-    r.at = static_cast<const char*>(a.logits) + static_cast<int64_t>(row) * a.ld * (DT == F32 ? 4 : 2);
-    r.vocab = a.vocab;
-
-    // the largest logit, and the first that has it
-    uint64_t best = 0;
-    uint32_t best_key = kKeyNone;
-    int best_at = 0;
-    scan_row<DT>(r, [&](int i, float v) {
-        const uint32_t k = key_of(v);
-        if (k > best_key) {
-            best_key = k;
-            best_at = i;
-        }
-    });
-    best = static_cast<uint64_t>(best_key) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(best_at));
-    best = block_max(best, s.part64);
-    best_key = static_cast<uint32_t>(best >> 32);
-    best_at = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(best));
-    if (best_key == kKeyNone) {
-        if (t == 0) {
-            a.token[row] = -1;
-            if (a.logprob) a.logprob[row] = __builtin_nanf("");
-        }
-        return;
+hipError_t launch_dt(const SampleArgs& a, void* ws, hipStream_t st) {
+    const SamplePlan plan = plan_sample(a.rows, a.vocab, ws != nullptr);
+    if (plan.parts == 1) {
+        sample_kernel<DT><<<dim3(static_cast<unsigned>(a.rows)), kThreads, 0, st>>>(a);
+        return hipGetLastError();
     }
-    const float temp = a.temperature ? a.temperature[row] : 1.f;
-    if (!(temp > 0.f)) {
-        if (t == 0) {
-            a.token[row] = best_at;
-            if (a.logprob) a.logprob[row] = 0.f;
-        }
-        return;
-    }
-    r.top = logit_of(best_key);
-    r.scale = 1.4426950408889634 / static_cast<double>(temp);
-    const float min_p = a.min_p ? a.min_p[row] : 0.f;
-    r.least = !(min_p > 0.f) ? 0 : min_p >= 1.f ? kOne : static_cast<uint64_t>(ceil(static_cast<double>(min_p) * 0x1p44));
-
-    for (int i = t; i < 1024; i += kThreads) s.exp2_tab[i] = exp2(-i / 1024.0);
-    for (int i = t; i < kBins; i += kThreads) {
-        s.mass[i] = 0;
-        s.count[i] = 0;
-    }
-    __syncthreads();
-    scan_row<DT>(r, [&](int, float v) {
-        const double y = y_of(r, v);
-        if (!(y < kYEnd)) return;            // (a NaN too)
-        const uint64_t w = mass_of(y, s.exp2_tab);
-        if (w < r.least) return;
-        const int b = static_cast<int>(y * 32.0);
-        atomicAdd(reinterpret_cast<unsigned long long*>(&s.mass[b]), w);
-        atomicAdd(&s.count[b], 1u);
-    });
-    __syncthreads();
-    run_up(s.mass, s.count, kBins, s);
-
-    uint64_t mass = s.mass[kBins - 1];
-    const uint32_t all = s.count[kBins - 1];
-    const float top_p = a.top_p ? a.top_p[row] : 1.f;
-    int64_t k = a.top_k ? a.top_k[row] : 0;
-    if (top_p <= 0.f) k = 1;
-    if (k > 0 && k < all) mass = pass<DT, true, false>(r, static_cast<uint64_t>(k - 1), s).mass;
-    bool exact;
-    if (top_p > 0.f && top_p < 1.f) {
-        // kept: the tokens before which less than top_p of the mass lies
-        const uint64_t f = part_of(static_cast<uint64_t>(static_cast<double>(top_p) * 0x1p48), mass, &exact);
-        mass = pass<DT, false, false>(r, exact && f ? f - 1 : f, s).mass;
-    }
-    const float u = a.u[row];
-    const uint64_t u48 = !(u > 0.f) ? 0 : u >= 1.f ? (1ull << 48) - 1 : static_cast<uint64_t>(static_cast<double>(u) * 0x1p48);
-    const Place p = pass<DT, false, true>(r, part_of(u48, mass, &exact), s);
-    if (t == 0) {
-        a.token[row] = p.index;
-        if (a.logprob)
-            a.logprob[row] = static_cast<float>(-y_of(r, logit_of(p.key)) * 0.6931471805599453 - log(static_cast<double>(mass) * 0x1p-44));
-    }
+    Part* parts = static_cast<Part*>(ws);
+    sample_part_kernel<DT><<<dim3(static_cast<unsigned>(a.rows * plan.parts)), kThreads, 0, st>>>(a, plan.parts, plan.size, parts);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    sample_join_kernel<DT><<<dim3(static_cast<unsigned>(a.rows)), kThreads, 0, st>>>(a, plan.parts, parts);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_sample(const SampleArgs& a, int dtype, void* ws, hipStream_t st) {
-    (void)ws;
-    const dim3 grid(static_cast<unsigned>(a.rows));
-    if (dtype == F16) sample_kernel<F16><<<grid, kThreads, 0, st>>>(a);
-    else if (dtype == BF16) sample_kernel<BF16><<<grid, kThreads, 0, st>>>(a);
-    else sample_kernel<F32><<<grid, kThreads, 0, st>>>(a);
-    return hipGetLastError();
+    return dtype == F16 ? launch_dt<F16>(a, ws, st) : dtype == BF16 ? launch_dt<BF16>(a, ws, st) : launch_dt<F32>(a, ws, st);
 }
 
 }  // namespace qlin
