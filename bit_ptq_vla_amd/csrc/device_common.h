@@ -181,6 +181,28 @@ __device__ __forceinline__ float wave_max(float v, int width) {
     return v;
 }
 
+// x of the lane that a DPP move names, 0 where there is none or the row is masked.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_u(uint32_t x) {
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), CTRL, ROWS, 0xF, false));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t dpp_u(uint64_t x) {
+    return static_cast<uint64_t>(dpp_u<CTRL, ROWS>(static_cast<uint32_t>(x >> 32))) << 32 | dpp_u<CTRL, ROWS>(static_cast<uint32_t>(x));
+}
+// Inclusive sum over a wave's lanes: shifts within rows of 16, then the last lane of
+// a row to the next one, and of the first half to the second.
+template <typename T>
+__device__ __forceinline__ T wave_sum_up(T v) {
+    v += dpp_u<0x111, 0xF>(v);
+    v += dpp_u<0x112, 0xF>(v);
+    v += dpp_u<0x114, 0xF>(v);
+    v += dpp_u<0x118, 0xF>(v);
+    v += dpp_u<0x142, 0xA>(v);
+    v += dpp_u<0x143, 0xC>(v);
+    return v;
+}
+
 // Exact GeLU, t * (1 + erf(t / sqrt 2)) / 2, in fp32 (device-library erff).
 __device__ __forceinline__ float gelu_erf(float t) {
     return 0.5f * t * (1.0f + erff(t * 0.70710678118654752440f));

@@ -247,28 +247,6 @@ struct Sampler {
         __device__ __forceinline__ void words_back(F f) const { words_to<true>(f); }
     };
 
-    // x of the lane that a DPP move names, 0 where there is none or the row is masked.
-    template <int CTRL, int ROWS>
-    static __device__ __forceinline__ uint32_t dpp(uint32_t x) {
-        return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), CTRL, ROWS, 0xF, false));
-    }
-    template <int CTRL, int ROWS>
-    static __device__ __forceinline__ uint64_t dpp(uint64_t x) {
-        return static_cast<uint64_t>(dpp<CTRL, ROWS>(static_cast<uint32_t>(x >> 32))) << 32 | dpp<CTRL, ROWS>(static_cast<uint32_t>(x));
-    }
-    // Inclusive sum over a wave's lanes: shifts within rows of 16, then the last lane of
-    // a row to the next one, and of the first half to the second.
-    template <typename T>
-    static __device__ __forceinline__ T wave_sum_up(T v) {
-        v += dpp<0x111, 0xF>(v);
-        v += dpp<0x112, 0xF>(v);
-        v += dpp<0x114, 0xF>(v);
-        v += dpp<0x118, 0xF>(v);
-        v += dpp<0x142, 0xA>(v);
-        v += dpp<0x143, 0xC>(v);
-        return v;
-    }
-
     // Inclusive sum over the block's threads.
     template <typename T>
     static __device__ __forceinline__ T block_scan(T v, T* parts) {
@@ -286,12 +264,12 @@ struct Sampler {
     template <typename T>
     static __device__ __forceinline__ T block_max(T v, T* parts) {
         auto more = [](T a, T b) { return a > b ? a : b; };
-        v = more(v, dpp<0x111, 0xF>(v));
-        v = more(v, dpp<0x112, 0xF>(v));
-        v = more(v, dpp<0x114, 0xF>(v));
-        v = more(v, dpp<0x118, 0xF>(v));
-        v = more(v, dpp<0x142, 0xA>(v));
-        v = more(v, dpp<0x143, 0xC>(v));
+        v = more(v, dpp_u<0x111, 0xF>(v));
+        v = more(v, dpp_u<0x112, 0xF>(v));
+        v = more(v, dpp_u<0x114, 0xF>(v));
+        v = more(v, dpp_u<0x118, 0xF>(v));
+        v = more(v, dpp_u<0x142, 0xA>(v));
+        v = more(v, dpp_u<0x143, 0xC>(v));
         if ((threadIdx.x & 63) == 63) parts[threadIdx.x >> 6] = v;
         __syncthreads();
         v = parts[0];
