@@ -823,23 +823,25 @@ QLIN_MAX_TREE_NODES = 1024
 QLIN_MAX_POOL_ROWS = 1024
 
 
-def _index(t: torch.Tensor, name: str, n: int, dev: torch.device) -> None:
-    """An int32 array of n values on dev."""
-    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+def _index(t: torch.Tensor, name: str, n: int, dev: torch.device) -> int:
+    """Address of an int32 array of n values on the device dev."""
+    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must hold {n} contiguous int32 values")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, the call on {dev}")
-    _dev_tensor(t, name)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    return t.data_ptr()
 
 
 def _index_rows(t: torch.Tensor, name: str, rows: int, cols: int, dev: torch.device) -> int:
     """Row pitch of a row-major int32 [rows][>= cols] tensor on dev."""
-    if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != rows or t.shape[1] < cols or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape = t.shape
+    if t.dtype is not torch.int32 or len(shape) != 2 or shape[0] != rows or shape[1] < cols or (shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be a row-major int32 [{rows}][>= {cols}] tensor")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, the call on {dev}")
-    _dev_tensor(t, name)
-    return t.stride(0) if rows > 1 else t.shape[1]
+    return t.stride(0) if rows > 1 else shape[1]
 
 
 def qlin_tree_plan(parents: torch.Tensor, batch: KvBatch, mask: Optional[torch.Tensor] = None,
@@ -849,17 +851,17 @@ def qlin_tree_plan(parents: torch.Tensor, batch: KvBatch, mask: Optional[torch.T
     nodes are the batch's new tokens; parents int32 [tokens]: an earlier node of
     the sequence, or -1."""
     dev, tokens = batch.device, parents.numel()
-    _index(parents, "parents", tokens, dev)
+    src = _index(parents, "parents", tokens, dev)
     words = -(-batch.max_q // 32)
     if mask is None:
         mask = torch.empty((tokens, words), dtype=torch.int32, device=dev)
     if positions is None:
         positions = torch.empty(tokens, dtype=torch.int32, device=dev)
     ld = _index_rows(mask, "mask", tokens, words, dev)
-    _index(positions, "positions", tokens, dev)
-    st = _on_device(load().qlin_tree_plan, dev, parents.data_ptr(), tokens, batch._ref, mask.data_ptr(), ld,
-                    positions.data_ptr(), _stream(dev))
-    _check(st, "qlin_tree_plan")
+    st = _on_device(load().qlin_tree_plan, dev, src, tokens, batch._ref, mask.data_ptr(), ld,
+                    _index(positions, "positions", tokens, dev), _stream(dev))
+    if st:
+        raise QlinError(st, "qlin_tree_plan")
     return mask, positions
 
 
@@ -870,19 +872,17 @@ def qlin_tree_accept(parents: torch.Tensor, draft: torch.Tensor, sampled: torch.
     tokens confirm, its length (int32 [batch]) and the token sampled behind it
     (int32 [batch]); parents, draft and sampled int32 [tokens]."""
     dev, tokens = batch.device, parents.numel()
-    for name, t in (("parents", parents), ("draft", draft), ("sampled", sampled)):
-        _index(t, name, tokens, dev)
+    up, new, got = _index(parents, "parents", tokens, dev), _index(draft, "draft", tokens, dev), _index(sampled, "sampled", tokens, dev)
     if out is None:
         i32 = dict(dtype=torch.int32, device=dev)
         out = (torch.empty((batch.batch, batch.max_q), **i32), torch.empty(batch.batch, **i32),
                torch.empty(batch.batch, **i32))
     path, count, token = out
     ld = _index_rows(path, "path", batch.batch, batch.max_q, dev)
-    _index(count, "count", batch.batch, dev)
-    _index(token, "token", batch.batch, dev)
-    st = _on_device(load().qlin_tree_accept, dev, parents.data_ptr(), draft.data_ptr(), sampled.data_ptr(), tokens,
-                    batch._ref, path.data_ptr(), ld, count.data_ptr(), token.data_ptr(), _stream(dev))
-    _check(st, "qlin_tree_accept")
+    st = _on_device(load().qlin_tree_accept, dev, up, new, got, tokens, batch._ref, path.data_ptr(), ld,
+                    _index(count, "count", batch.batch, dev), _index(token, "token", batch.batch, dev), _stream(dev))
+    if st:
+        raise QlinError(st, "qlin_tree_accept")
     return path, count, token
 
 
@@ -946,10 +946,10 @@ def qlin_sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[tor
     _dev_tensor(logits, "logits")
     vocab, size = logits.shape[1], logits.element_size()
     ld = logits.stride(0) if rows > 1 else -(-vocab * size // 16) * 16 // size
-    for name, t, dt in (("u", u, torch.float32), ("temperature", temperature, torch.float32),
-                        ("top_k", top_k, torch.int32), ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
-        if t is not None and (t.dtype != dt or t.numel() != rows or not t.is_contiguous() or t.device != dev):
-            raise ValueError(f"{name} must hold {rows} contiguous {dt} values on {dev}")
+    for name, t in (("u", u), ("temperature", temperature), ("top_k", top_k), ("top_p", top_p), ("min_p", min_p)):
+        if t is not None and (t.dtype is not (torch.int32 if t is top_k else torch.float32) or t.numel() != rows
+                              or not t.is_contiguous() or t.device != dev):
+            raise ValueError(f"{name} must hold {rows} contiguous {'int32' if t is top_k else 'float32'} values on {dev}")
     if out is None:
         out = (torch.empty(rows, dtype=torch.int32, device=dev), torch.empty(rows, dtype=torch.float32, device=dev))
     token, logprob = out
@@ -1022,7 +1022,8 @@ def qlin_kv_resize(pool: KvPool, stack: Optional[KvStack], page_table: torch.Ten
     receives the pages copied from and to."""
     dev, rows = pool.device, old_len.numel()
     if stack is not None:
-        _same_device(dev, caches=stack.caches[0].k)
+        if stack.device != dev:
+            raise ValueError(f"the caches are on {stack.device}, the call on {dev}")
         if page_size is not None and page_size != stack.page_size:
             raise ValueError(f"page_size {page_size}, the stack's pages hold {stack.page_size}")
         page_size = stack.page_size
@@ -1033,13 +1034,12 @@ def qlin_kv_resize(pool: KvPool, stack: Optional[KvStack], page_table: torch.Ten
         len_out = torch.empty(rows, dtype=torch.int32, device=dev)
     if moved is None:
         moved = torch.empty((rows, 2), dtype=torch.int32, device=dev)
-    for name, t, n in (("old_len", old_len, rows), ("new_len", new_len, rows), ("len_out", len_out, rows),
-                       ("moved", moved, 2 * rows)):
-        _index(t, name, n, dev)
     st = _on_device(load().qlin_kv_resize, dev, pool._ref, None if stack is None else stack._ref,
                     0 if stack is None else stack.layers, page_size, page_table.data_ptr(), ld, page_table.shape[1], rows,
-                    old_len.data_ptr(), new_len.data_ptr(), len_out.data_ptr(), moved.data_ptr(), _stream(dev))
-    _check(st, "qlin_kv_resize")
+                    _index(old_len, "old_len", rows, dev), _index(new_len, "new_len", rows, dev),
+                    _index(len_out, "len_out", rows, dev), _index(moved, "moved", 2 * rows, dev), _stream(dev))
+    if st:
+        raise QlinError(st, "qlin_kv_resize")
     return len_out
 
 
@@ -1049,11 +1049,11 @@ def qlin_kv_fork(pool: KvPool, page_table: torch.Tensor, src: torch.Tensor, dst:
     tokens of rows src too (int32 [n] each; dst rows hold none before)."""
     dev, n = pool.device, src.numel()
     ld = _index_rows(page_table, "page_table", page_table.shape[0], 0, dev)
-    for name, t in (("src", src), ("dst", dst), ("length", length)):
-        _index(t, name, n, dev)
     st = _on_device(load().qlin_kv_fork, dev, pool._ref, page_size, page_table.data_ptr(), ld, page_table.shape[1],
-                    page_table.shape[0], src.data_ptr(), dst.data_ptr(), length.data_ptr(), n, _stream(dev))
-    _check(st, "qlin_kv_fork")
+                    page_table.shape[0], _index(src, "src", n, dev), _index(dst, "dst", n, dev),
+                    _index(length, "length", n, dev), n, _stream(dev))
+    if st:
+        raise QlinError(st, "qlin_kv_fork")
 
 
 def qlin_kv_copy_pages(stack: KvStack, pairs: torch.Tensor) -> None:
@@ -1077,11 +1077,11 @@ def qlin_kv_compact(stack: KvStack, batch: KvBatch, path: torch.Tensor, count: t
     ld = _index_rows(path, "path", batch.batch, batch.max_q, dev)
     if kv_len_out is None:
         kv_len_out = torch.empty(batch.batch, dtype=torch.int32, device=dev)
-    _index(count, "count", batch.batch, dev)
-    _index(kv_len_out, "kv_len_out", batch.batch, dev)
     st = _on_device(load().qlin_kv_compact, dev, stack._ref, stack.layers, batch._ref, path.data_ptr(), ld,
-                    count.data_ptr(), kv_len_out.data_ptr(), _stream(dev))
-    _check(st, "qlin_kv_compact")
+                    _index(count, "count", batch.batch, dev), _index(kv_len_out, "kv_len_out", batch.batch, dev),
+                    _stream(dev))
+    if st:
+        raise QlinError(st, "qlin_kv_compact")
     return kv_len_out
 
 

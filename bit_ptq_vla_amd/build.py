@@ -16,7 +16,7 @@ import tempfile
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libqlin.so")
-SOURCES = ["act_quant.hip", "norm_quant.hip", "rope_append.hip", "kv_attention.hip",
+SOURCES = ["act_quant.hip", "norm_quant.hip", "rope_append.hip", "kv_attention.hip", "kv_tree_attention.hip",
            "kv_pages.hip", "tree.hip", "sample.hip",
            "gemm_i8.hip", "gemv_w4a16.hip", "skinny_w4a16.hip",
            "skinny_int.hip", "composite.hip", "plan.cpp",

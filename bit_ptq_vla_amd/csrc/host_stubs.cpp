@@ -96,8 +96,14 @@ hipError_t launch_rope_table(float*, int64_t, int, double, double, hipStream_t) 
 }
 
 hipError_t launch_kv_attention(const KvAttnPlan&, const void*, int, int64_t, int, const KvIndex&, const int8_t*,
-                               const int8_t*, const float*, const float*, int, int, float, float, const uint32_t*,
-                               int64_t, void*, int64_t, void*, hipStream_t) {
+                               const int8_t*, const float*, const float*, int, int, float, float, void*, int64_t,
+                               void*, hipStream_t) {
+    return hipErrorNoBinaryForGpu;
+}
+
+hipError_t launch_kv_attention_tree(const KvAttnPlan&, const void*, int, int64_t, int, const KvIndex&, const int8_t*,
+                                    const int8_t*, const float*, const float*, int, int, float, float,
+                                    const uint32_t*, int64_t, void*, int64_t, void*, hipStream_t) {
     return hipErrorNoBinaryForGpu;
 }
 

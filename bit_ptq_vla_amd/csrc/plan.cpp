@@ -183,10 +183,32 @@ SamplePlan plan_sample(int64_t rows, int64_t vocab, bool allow_split) {
     return p;
 }
 
+// The rest of a plan: `heads` (sequence, kv head) pairs of row_tiles tiles each, and
+// `rows` rows of partial results.  Few tiles: their keys are split while that gives no
+// more blocks than CUs, 256 keys at least to a block.  Two blocks to a CU, us: 131101
+// keys of 8 heads 58, one 55; 8 x 50 rows of 8 heads over 866 keys 20 and 15; a part of
+// a second one (24 requests of 8 heads, 4097 keys, 384 blocks) 50, none (192) 42.
+static void split_keys(KvAttnPlan& p, int64_t heads, int64_t row_tiles, int64_t rows, int64_t max_kv, int d,
+                       bool allow_split) {
+    p.row_tiles = static_cast<int>(row_tiles);
+    const int64_t units = heads * row_tiles;
+    int64_t splits = 1;
+    if (allow_split && units > 0) {
+        const int64_t want = device_cus() / units, most = (max_kv + 255) / 256;
+        splits = want < most ? want : most;
+        splits = splits < 1 ? 1 : splits;
+    }
+    const int64_t keys = ((max_kv + splits - 1) / splits + 255) / 256 * 256;
+    p.split_keys = static_cast<int>(keys < 256 ? 256 : keys);
+    p.splits = splits == 1 ? 1 : static_cast<int>((max_kv + p.split_keys - 1) / p.split_keys);
+    p.blocks = units * p.splits;
+    p.ws_bytes = p.splits > 1 ? p.splits * rows * (d + 2) * 4 : 0;
+}
+
 KvAttnPlan plan_kv_attention(int64_t batch, int64_t max_q, int64_t max_kv, int heads_q, int heads, int d,
                              bool allow_split) {
     KvAttnPlan p;
-    const int64_t rows = max_q * (heads_q / heads), cus = device_cus();
+    const int64_t rows = max_q * (heads_q / heads);
     // Blocks of 128 (256-wide heads) or 256 rows pay once the call is long, counted
     // in 16-row tiles times keys, and fill at least a quarter of theirs.  Measured,
     // us for 16-row blocks / for these, bf16:
@@ -197,25 +219,33 @@ KvAttnPlan plan_kv_attention(int64_t batch, int64_t max_q, int64_t max_kv, int h
     // and with less than a quarter: 81 / 88 (128 wide, 32 x 8 heads, 64 rows), 57 / 69 (256 wide, 32 rows).
     const int64_t least = d == 256 ? 3 << 17 : d == 128 ? 1 << 20 : 5 << 19;
     p.many = rows > (d == 256 ? 32 : 64) && max_kv > 0 && batch * heads * ((rows + 15) / 16) > least / max_kv;
+    p.tile = 16;
     const int64_t per = !p.many ? 16 : d == 256 ? 128 : 256;
-    p.row_tiles = static_cast<int>((rows + per - 1) / per);
-    const int64_t units = batch * heads * p.row_tiles;
     p.lds_bytes = static_cast<int>(4 * (rows < 16 ? rows : 16) * (d + 6) * 4);
-    // Few tiles: their keys are split while that gives no more blocks than CUs, 256
-    // keys at least to a block.  Two blocks to a CU, us: 131101 keys of 8 heads 58,
-    // one 55; 8 x 50 rows of 8 heads over 866 keys 20 and 15; a part of a second
-    // one (24 requests of 8 heads, 4097 keys, 384 blocks) 50, none (192) 42.
-    int64_t splits = 1;
-    if (allow_split && units > 0) {
-        const int64_t want = cus / units, most = (max_kv + 255) / 256;
-        splits = want < most ? want : most;
-        splits = splits < 1 ? 1 : splits;
-    }
-    const int64_t keys = ((max_kv + splits - 1) / splits + 255) / 256 * 256;
-    p.split_keys = static_cast<int>(keys < 256 ? 256 : keys);
-    p.splits = splits == 1 ? 1 : static_cast<int>((max_kv + p.split_keys - 1) / p.split_keys);
-    p.blocks = units * p.splits;
-    p.ws_bytes = p.splits > 1 ? p.splits * batch * max_q * heads_q * (d + 2) * 4 : 0;
+    split_keys(p, batch * heads, (rows + per - 1) / per, batch * max_q * heads_q, max_kv, d, allow_split);
+    return p;
+}
+
+KvAttnPlan plan_kv_attention_tree(int64_t batch, int64_t max_q, int64_t max_kv, int heads_q, int heads, int d,
+                                  bool allow_split) {
+    KvAttnPlan p;
+    const int64_t rows = max_q * (heads_q / heads), tiles = batch * heads * ((rows + 15) / 16);
+    // By the call's work in 16-row tiles times keys.  Measured, us for blocks of 16 rows,
+    // of 32, and of 256 (128 of a 256-wide head), bf16:
+    //   64 wide:   0.5 M 14 / 17 / 25, 1.1 M 20 / 20 / 37, 2.2 M 31 / 28 / 37, 4.4 M 57 / 55 / 50, 17 M 185 / 146 / 125
+    //   128 wide:  0.5 M 19 / 21 / 34, 0.7 M 21 / 18 / 40, 1.1 M 31 / 26 / 43, 2.4 M 59 / 39 / 55, 4.5 M 109 / 73 / 64,
+    //              17 M 372 / 221 / 170
+    //   256 wide:  0.5 M 34 / 56 / 46, 0.7 M 44 / 52 / 47, 1.1 M 68 / 84 / 60, 1.6 M 123 / 130 / 63, 4.5 M 258 / 320 / 142
+    // The large blocks' matrix products run for all of their rows: a quarter filled
+    // (64 x 16 nodes over 4096 keys, 8.4 M) they take 328 where blocks of 32 take 126.
+    const int64_t many = d == 256 ? 800000 : d == 128 ? 3500000 : 4500000, wide = d == 128 ? 600000 : 1000000;
+    p.many = rows > (d == 256 ? 32 : 128) && max_kv > 0 && tiles > many / max_kv;
+    p.tile = d < 256 && rows > 16 && max_kv > 0 && tiles > wide / max_kv ? 32 : 16;
+    const int64_t per = !p.many ? p.tile : d == 256 ? 128 : 256;
+    p.lds_bytes = static_cast<int>(4 * (rows < 16 ? rows : 16) * (d + 6) * 4);
+    split_keys(p, batch * heads, (rows + per - 1) / per, batch * max_q * heads_q, max_kv, d, allow_split);
+    // (eight units at a time: see the kernel's order of blocks)
+    if (!p.many && p.row_tiles > 0) p.blocks = (p.blocks / p.row_tiles + 7) / 8 * 8 * p.row_tiles;
     return p;
 }
 

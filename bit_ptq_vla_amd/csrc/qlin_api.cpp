@@ -322,10 +322,10 @@ qlin::KvStackArgs stack_args(const qlin_kv_cache* c, int32_t layers, int32_t at)
 }
 
 // Checks and launch of the two attention entry points (tree: with a mask).
-int64_t attention_bytes(int32_t heads_q, const qlin_kv_cache* cache, const qlin_kv_batch* batch) {
+int64_t attention_bytes(int32_t heads_q, const qlin_kv_cache* cache, const qlin_kv_batch* batch, bool tree) {
     if (kv_check(cache, batch, 0, heads_q) != QLIN_OK) return -1;
-    const qlin::KvAttnPlan plan = qlin::plan_kv_attention(batch->batch, batch->max_q, batch->max_kv, heads_q,
-                                                          cache->heads, cache->head_dim, true);
+    const qlin::KvAttnPlan plan = (tree ? qlin::plan_kv_attention_tree : qlin::plan_kv_attention)(
+        batch->batch, batch->max_q, batch->max_kv, heads_q, cache->heads, cache->head_dim, true);
     return plan.blocks > kMaxAttnBlocks ? -1 : plan.ws_bytes;
 }
 
@@ -345,8 +345,8 @@ qlin_status attention(const void* q, qlin_dtype dtype, int64_t tokens, int64_t l
     if (ldq % 8 != 0 || ldq < wide || ldo % 8 != 0 || ldo < wide || workspace_bytes < 0) return QLIN_ERR_SHAPE;
     if (!workspace && workspace_bytes > 0) return QLIN_ERR_NULL;
     if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return QLIN_ERR_ALIGN;
-    const qlin::KvAttnPlan plan = qlin::plan_kv_attention(batch->batch, batch->max_q, batch->max_kv, heads_q,
-                                                          cache->heads, cache->head_dim, workspace != nullptr);
+    const qlin::KvAttnPlan plan = (mask ? qlin::plan_kv_attention_tree : qlin::plan_kv_attention)(
+        batch->batch, batch->max_q, batch->max_kv, heads_q, cache->heads, cache->head_dim, workspace != nullptr);
     if (plan.blocks > kMaxAttnBlocks) return QLIN_ERR_SHAPE;
     if (workspace && workspace_bytes < plan.ws_bytes) return QLIN_ERR_WORKSPACE;
     const int64_t codes = cache->pages * cache->heads * cache->page_size * cache->head_dim;
@@ -360,9 +360,14 @@ qlin_status attention(const void* q, qlin_dtype dtype, int64_t tokens, int64_t l
     if (tokens == 0 || batch->batch == 0 || batch->max_q == 0) return QLIN_OK;
     st = check_device();
     if (st != QLIN_OK) return st;
+    if (mask)
+        return map_err(qlin::launch_kv_attention_tree(plan, q, dtype, ldq, heads_q, kv_index(cache, batch, tokens),
+                                                      cache->k, cache->v, cache->k_scale, cache->v_scale, cache->heads,
+                                                      cache->head_dim, sm_scale, softcap, mask, mask_ld, out, ldo,
+                                                      workspace, as_stream(stream)));
     return map_err(qlin::launch_kv_attention(plan, q, dtype, ldq, heads_q, kv_index(cache, batch, tokens), cache->k,
                                              cache->v, cache->k_scale, cache->v_scale, cache->heads, cache->head_dim,
-                                             sm_scale, softcap, mask, mask_ld, out, ldo, workspace, as_stream(stream)));
+                                             sm_scale, softcap, out, ldo, workspace, as_stream(stream)));
 }
 
 // Checks and launch of the two residual + RMS norm entry points (bits 0: the
@@ -754,7 +759,7 @@ qlin_status qlin_rope_append_kv(const void* qkv, qlin_dtype dtype, int64_t token
 }
 
 int64_t qlin_kv_attention_workspace_bytes(int32_t heads_q, const qlin_kv_cache* cache, const qlin_kv_batch* batch) {
-    return attention_bytes(heads_q, cache, batch);
+    return attention_bytes(heads_q, cache, batch, false);
 }
 
 qlin_status qlin_kv_attention(const void* q, qlin_dtype dtype, int64_t tokens, int64_t ldq, int32_t heads_q,
@@ -767,7 +772,7 @@ qlin_status qlin_kv_attention(const void* q, qlin_dtype dtype, int64_t tokens, i
 int64_t qlin_kv_attention_tree_workspace_bytes(int32_t heads_q, const qlin_kv_cache* cache,
                                                const qlin_kv_batch* batch) {
     if (!batch || batch->prefix_len || batch->max_q > qlin::kMaxTreeNodes) return -1;
-    return attention_bytes(heads_q, cache, batch);
+    return attention_bytes(heads_q, cache, batch, true);
 }
 
 qlin_status qlin_kv_attention_tree(const void* q, qlin_dtype dtype, int64_t tokens, int64_t ldq, int32_t heads_q,

@@ -109,12 +109,12 @@ hipError_t launch_rope_append(const void* qkv, int dtype, int64_t ld, int heads_
                               hipStream_t st);
 hipError_t launch_rope_table(float* table, int64_t positions, int rot, double base, double stretch, hipStream_t st);
 
-// Attention over the paged cache (mask: the new tokens are the nodes of a tree,
-// mask_ld words to a row; else nullptr).  The plan: query-row tiles, and how many
+// Attention over the paged cache.  The plan: query-row tiles, and how many
 // blocks share a tile's keys (split_keys each; their partials, ws_bytes, are
 // joined by a second kernel).
 struct KvAttnPlan {
-    bool many;                // 256 query rows (128 of a 256-wide head) to a block; else 16
+    bool many;                // 256 query rows (128 of a 256-wide head) to a block; else
+    int tile;                 // 16 of them (of a tree 16, 32 or 64)
     int lds_bytes;            // of the 16-row blocks
     int row_tiles, splits, split_keys;
     int64_t blocks, ws_bytes;
@@ -123,8 +123,15 @@ KvAttnPlan plan_kv_attention(int64_t batch, int64_t max_q, int64_t max_kv, int h
                              bool allow_split);
 hipError_t launch_kv_attention(const KvAttnPlan& plan, const void* q, int dtype, int64_t ldq, int heads_q,
                                const KvIndex& ix, const int8_t* k, const int8_t* v, const float* ks, const float* vs,
-                               int heads, int d, float sm_scale, float cap, const uint32_t* mask, int64_t mask_ld,
-                               void* out, int64_t ldo, void* ws, hipStream_t st);
+                               int heads, int d, float sm_scale, float cap, void* out, int64_t ldo, void* ws,
+                               hipStream_t st);
+// The same for the nodes of a tree (mask_ld words of mask to a row).
+KvAttnPlan plan_kv_attention_tree(int64_t batch, int64_t max_q, int64_t max_kv, int heads_q, int heads, int d,
+                                  bool allow_split);
+hipError_t launch_kv_attention_tree(const KvAttnPlan& plan, const void* q, int dtype, int64_t ldq, int heads_q,
+                                    const KvIndex& ix, const int8_t* k, const int8_t* v, const float* ks,
+                                    const float* vs, int heads, int d, float sm_scale, float cap, const uint32_t* mask,
+                                    int64_t mask_ld, void* out, int64_t ldo, void* ws, hipStream_t st);
 
 // Trees of drafted tokens: masks and positions from parents, the confirmed path.
 constexpr int kMaxTreeNodes = 1024;

@@ -141,6 +141,30 @@ def test_attention(case, bound):
     check(one, x, c, table, start, kv, hq, sees, d ** -0.5, cap, dtype)
 
 
+@pytest.mark.parametrize("max_kv", [1 << 16, 1 << 19, 1 << 22])
+@pytest.mark.parametrize("case", [CASES[i] for i in (2, 4, 5, 6, 7, 9, 10, 11, 12)],
+                         ids=lambda c: f"{c[0]}-{c[1]}-{c[2]}-{c[3]}-p{c[4]}-cap{c[5]}-{len(c[6])}")
+def test_attention_under_far_bounds(case, max_kv):
+    """The kernels for more rows are chosen by the bound: blocks of 32 and of 256 rows
+    on short sequences, with and without split keys."""
+    dtype, hq, hkv, d, page, cap, seqs = case
+    c, table, start, kv, parents, x, batch = setup(case)
+    wide = np.zeros((len(seqs), max_kv // page), dtype=np.int32)
+    wide[:, :table.shape[1]] = table
+    batch = q.KvBatch(i32(wide), i32(start), i32(kv), max_q=batch.max_q, max_kv=max_kv)
+    sees = make_sees(parents, start, max(1, batch.max_q))
+    mask, _ = q.qlin_tree_plan(i32(parents), batch)
+    for split in (True, False):
+        out = torch.full_like(x, 5.0)
+        work = q.kv_attention_tree_workspace(c.cache, batch, hq) if split else None
+        q._check(q.load().qlin_kv_attention_tree(x.data_ptr(), q._TORCH_TO_QLIN[x.dtype], len(x), x.stride(0), hq,
+                                                 c.cache._ref, batch._ref, mask.data_ptr(), mask.shape[1], d ** -0.5, cap,
+                                                 out.data_ptr(), out.stride(0), q._ptr(work),
+                                                 0 if work is None else work.numel(), q._stream(x.device)), "tree")
+        torch.cuda.synchronize()
+        check(out, x, c, table, start, kv, hq, sees, d ** -0.5, cap, dtype)
+
+
 @pytest.mark.parametrize("case", [CASES[2], CASES[6], CASES[9]], ids=["16", "50", "130"])
 def test_chain_gives_the_bits_of_causal_attention(case):
     """Where every key behind a query is masked either way, the products are the same."""
