@@ -475,11 +475,12 @@ class DecoderLayer:
                            for name, (n, k) in self.shapes.items()}
         return self._ws[m]
 
-    def step(self, x, residual, batch, attn_workspace=None, evs=None):
+    def step(self, x, residual, batch, attn_workspace=None, evs=None, tree=None):
         """residual [m][hidden] += x (the previous layer's output) and, behind
         the attention, the attention branch; returns the MLP branch [m][hidden]
         (a buffer of this layer).  batch holds the m new tokens; evs: 11 events
-        around the launches."""
+        around the launches; tree: (mask, positions) where the new tokens are
+        the nodes of trees (qlin_tree_plan)."""
         if batch.max_kv > self.rope.shape[0]:
             # (the append would turn the tokens behind the table's last row by that row)
             raise ValueError(f"the layer's rotary table of {self.rope.shape[0]} positions does not hold max_kv = {batch.max_kv}")
@@ -499,9 +500,13 @@ class DecoderLayer:
         mark(1)
         gemm("qkv", a, qkv)
         mark(2)
-        q.qlin_rope_append_kv(qkv, self.cache, batch, self.heads, self.rope, q_out=qr)
+        q.qlin_rope_append_kv(qkv, self.cache, batch, self.heads, self.rope, positions=None if tree is None else tree[1],
+                              q_out=qr)
         mark(3)
-        q.qlin_kv_attention(qr, self.cache, batch, self.heads, out=ctx, workspace=attn_workspace)
+        if tree is None:
+            q.qlin_kv_attention(qr, self.cache, batch, self.heads, out=ctx, workspace=attn_workspace)
+        else:
+            q.qlin_kv_attention_tree(qr, self.cache, batch, self.heads, tree[0], out=ctx, workspace=attn_workspace)
         mark(4)
         q.qlin_rotate_quant_act(ctx, bits=8, out=cq)
         mark(5)
@@ -516,3 +521,101 @@ class DecoderLayer:
         gemm("down", hq, y)
         mark(10)
         return y
+
+
+class TreeDecoder:
+    """A few decoder layers that check a tree of drafted tokens in each of a
+    batch of sequences, over one pool of pages: growth of the rows, tree plan,
+    layers, final norm and vocabulary projection (W8A8), a token sampled behind
+    every node, the accepted path, its compaction in every layer's cache, and
+    the rejected nodes' pages given back.  Nothing goes through the host, so
+    that step() can be captured into a graph.
+
+    Every sequence has `nodes` nodes a step, the first of them the last token
+    taken (`last`), and room for `tokens` tokens.
+    """
+
+    def __init__(self, dev, layers: int, batch: int, nodes: int, tokens: int, vocab: int, page_size: int = 16,
+                 hidden: int = 256, heads: int = 4, heads_kv: int = 2, head_dim: int = 64, ffn: int = 512,
+                 dtype: str = "f16", seed: int = 3):
+        import torch
+
+        import bit_ptq_vla_amd as q
+        from bit_ptq_vla_amd import synth
+
+        if vocab % 8:
+            raise ValueError("the vocabulary is a multiple of 8")
+        self.q, self.batch, self.nodes, self.vocab, self.hidden = q, batch, nodes, vocab, hidden
+        cols = -(-(tokens + nodes) // page_size)
+        m = batch * nodes
+        tdt = {"f16": torch.float16, "bf16": torch.bfloat16}[dtype]
+        # a page of every row's table at most, so that growth is always granted
+        self.layers = [DecoderLayer(dev, max(m, batch * tokens), batch * cols, page_size, positions=cols * page_size,
+                                    hidden=hidden, heads=heads, heads_kv=heads_kv, head_dim=head_dim, ffn=ffn, dtype=dtype,
+                                    seed=seed + i) for i in range(layers)]
+        self.stack = q.KvStack([x.cache for x in self.layers])
+        self.pool = q.KvPool.empty(batch * cols, dev)
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.table = torch.full((batch, cols), -1, **i32)
+        self.embed = synth.device_normal(seed, f"tree_decoder/embed/{vocab}x{hidden}", (vocab, hidden), dev, dtype=dtype)
+        w = synth.device_normal(seed, f"tree_decoder/head/{vocab}x{hidden}", (vocab, hidden), dev, std=hidden ** -0.5)
+        self.head = q.qlin_quantize_weights(w, bits=8)
+        self.gamma = torch.ones(hidden, device=dev)
+        self.len, self.grown, self.kept = (torch.zeros(batch, **i32) for _ in range(3))
+        self.want = torch.zeros(batch, **i32)
+        self.last = torch.zeros(batch, **i32)
+        self.moved = torch.empty((batch, 2), **i32)
+        self.max_kv = cols * page_size
+        self.starts = torch.arange(0, m + 1, nodes, **i32)
+        self.kv = q.KvBatch(self.table, self.starts, self.grown, max_q=nodes, max_kv=self.max_kv)
+        self.mask = torch.empty((m, -(-nodes // 32)), **i32)
+        self.positions = torch.empty(m, **i32)
+        self.attn = q.kv_attention_tree_workspace(self.layers[0].cache, self.kv, heads)
+        self.residual = torch.empty((m, hidden), dtype=tdt, device=dev)
+        self.zero = torch.zeros((m, hidden), dtype=tdt, device=dev)
+        self.codes = (torch.empty((m, hidden), dtype=torch.int8, device=dev), torch.empty(m, dtype=torch.float32, device=dev))
+        self.logits = torch.empty((m, vocab), dtype=tdt, device=dev)
+        self.head_ws = q.gemm_workspace(q.QLIN_W8A8, m, vocab, hidden, dev)
+        self.token, self.logprob = torch.empty(m, **i32), torch.empty(m, dtype=torch.float32, device=dev)
+        self.sample_ws = q.sample_workspace(m, vocab, dev)
+        self.path = (torch.empty((batch, nodes), **i32), torch.empty(batch, **i32), self.last)
+
+    def prompt(self, tokens, lengths):
+        """The cached tokens of each sequence: rows of tokens (int32, on the
+        device) of the given lengths, the last token taken behind them not
+        included."""
+        import torch
+
+        q = self.q
+        new = torch.tensor(lengths, dtype=torch.int32, device=tokens.device)
+        q.qlin_kv_resize(self.pool, self.stack, self.table, self.len, new, len_out=self.grown, moved=self.moved)
+        starts = torch.cat([new.new_zeros(1), new.cumsum(0).to(torch.int32)])
+        batch = q.KvBatch(self.table, starts, self.grown, max_q=max(lengths), max_kv=self.max_kv)
+        residual = self.embed.index_select(0, tokens)
+        x = torch.zeros_like(residual)
+        for layer in self.layers:
+            x = layer.step(x, residual, batch)
+        self.len.copy_(self.grown)
+
+    def step(self, parents, draft, u, **sampling):
+        """One step: parents int32 [batch * nodes]; draft int32 [batch * nodes],
+        whose entries at the first nodes are the last tokens taken; u float32
+        [batch * nodes].  Returns (path, count, token): self.last becomes the
+        token sampled behind each path, self.len counts its tokens."""
+        import torch
+
+        q = self.q
+        torch.add(self.len, self.nodes, out=self.want)
+        q.qlin_kv_resize(self.pool, self.stack, self.table, self.len, self.want, len_out=self.grown, moved=self.moved)
+        q.qlin_tree_plan(parents, self.kv, mask=self.mask, positions=self.positions)
+        torch.index_select(self.embed, 0, draft, out=self.residual)
+        x = self.zero
+        for layer in self.layers:
+            x = layer.step(x, self.residual, self.kv, attn_workspace=self.attn, tree=(self.mask, self.positions))
+        q.qlin_add_rmsnorm_quant(x, self.gamma, self.residual, bits=8, out=self.codes)
+        q.qlin_gemm_w8a8(*self.codes, *self.head, self.hidden, out=self.logits, workspace=self.head_ws)
+        q.qlin_sample(self.logits, u, out=(self.token, self.logprob), workspace=self.sample_ws, **sampling)
+        q.qlin_tree_accept(parents, draft, self.token, self.kv, out=self.path)
+        q.qlin_kv_compact(self.stack, self.kv, self.path[0], self.path[1], kv_len_out=self.kept)
+        q.qlin_kv_resize(self.pool, self.stack, self.table, self.grown, self.kept, len_out=self.len, moved=self.moved)
+        return self.path
