@@ -13,6 +13,13 @@ namespace {
 // A wave holds all of the rows, so that a step's codes are read and expanded to fp16
 // once for NQ products with 16 queries each: expanding them (20 vector instructions to
 // 16 codes) costs as much as the softmax of 16 rows.
+//
+// Bound by latency where there is little (16 nodes over 816 keys of 32 heads, 7 MB: 11
+// us, a join among them), by the vector units' issue where there is much: 64 trees of up
+// to 16 nodes over up to 4080 keys, 8 heads of 128 for 32 (421 MB) take 127 us, 3.3 TB/s;
+// a step of 32 rows and 64 keys is about 800 vector instructions, which keep the SIMDs
+// 63% busy, the matrix units 20%.  Blocks of 16 rows whose row tiles did not share an L2
+// took 212; a wave with 64 rows spills.
 template <int DT, int D, bool CAP, int NQ>
 __global__ __launch_bounds__(256, D < 256 ? 2 : 1) void kv_attn_tree_kernel(AttnParams p) {
     constexpr int NWV = 4;

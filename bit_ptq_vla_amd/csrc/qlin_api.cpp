@@ -246,7 +246,9 @@ qlin::KvIndex kv_index(const qlin_kv_cache* c, const qlin_kv_batch* b, int64_t t
             b->max_kv, c->page_size};
 }
 
-// Rows of qlin_sample (a block of 1024 threads each, of the 2^32 a launch holds).
+static_assert(QLIN_MAX_TREE_NODES == qlin::kMaxTreeNodes && QLIN_MAX_POOL_ROWS == qlin::kMaxPoolRows, "bounds of the header");
+
+// Rows of qlin_sample (a block of 512 threads each, of the 2^32 a launch holds).
 constexpr int64_t kMaxSampleRows = 1 << 21;
 
 // Shared checks of the tree calls, which read a batch's lengths only.

@@ -676,7 +676,9 @@ qlin_status qlin_sample(const void* logits, qlin_dtype dtype, int64_t rows, int6
  *
  * Numbers that lie on the device cannot be refused: a page number outside the pool
  * is no page, giving back a free page changes nothing, a row number outside the
- * table forks nothing.  resize takes one launch, and one for each 32 layers.
+ * table forks nothing.  resize takes one launch, and one for each 32 layers.  Calls on
+ * one pool, one table or the same pages run one after the other: in one stream, or
+ * ordered by events.
  */
 #define QLIN_MAX_POOL_ROWS 1024
 typedef struct {
@@ -705,8 +707,8 @@ qlin_status qlin_kv_copy_pages(const qlin_kv_cache* caches, int32_t layers, cons
  *   kv_len_out out int32 [batch] (or NULL): cached tokens + path, the sequence's new
  *             length.  The pages behind it still belong to its row (qlin_kv_resize).
  * A page whose tokens change gets the largest scale of what it then holds, the tokens
- * kept from before and those moved in; codes become rne(c * s_old / s), evaluated in
- * float64.  A page of nodes that stay at their places does not change, nor does what
+ * kept from before and those moved in; codes become rne(c * s_old / s), as the exact
+ * quotient rounds.  A page of nodes that stay at their places does not change, nor does what
  * lies behind the new length.  A node on no page counts as zeros.  A sequence with
  * more new tokens than its length stays as it is.  Not to be called twice: the second
  * call would move what the first has put there.
