@@ -349,9 +349,9 @@ __device__ __forceinline__ uint4 follow16(uint4 w, float was, float now) {
 // Bound by the chain page table, scales, codes, stores at five waves to a SIMD, and by
 // what shares the moved codes' cache lines: 64 paths of 8 of 32 nodes in 16 layers of 8
 // heads of 128 (29 MB of moved codes; some 60 MB are read and 48 written, with the tokens
-// whose page's scale
-// rises) take 38 us, one path of 5 of 16 in 32 layers of 32 heads 8.  A wave for a head's
-// k and v takes 35 and 8, a wave for 64 dimensions 60 and 7: each repeats the chain.
+// whose page's scale rises) take 38 us, one path of 5 of 16 in 32 layers of 32 heads 8.
+// A wave for a head's k and v takes 35 and 8, a wave for 64 dimensions of v 60 and 7:
+// each wave repeats the chain.
 __global__ __launch_bounds__(256) void compact_kernel(KvIndex ix, KvStackArgs c, const int32_t* path, int64_t path_ld,
                                                       const int32_t* count, int32_t* len_out, int groups) {
     __shared__ int16_t node[kMaxTreeNodes];
