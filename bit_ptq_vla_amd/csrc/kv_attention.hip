@@ -266,7 +266,7 @@ __global__ __launch_bounds__(256) void kv_attn_rows16_kernel(AttnParams p) {
 template <int DT, int D, bool CAP>
 hipError_t launch_cap(const AttnParams& p, const KvAttnPlan& plan, hipStream_t st) {
     const hipError_t e =
-        plan.many ? launch_lds(kv_attn_phase_kernel<DT, D, CAP, false>, plan.blocks, 512, 2 * 2 * 64 * D * 2, p, st)
+        plan.many ? launch_lds(kv_attn_phase_kernel<DT, D, CAP>, plan.blocks, 512, 2 * 2 * 64 * D * 2, p, st)
                   : launch_lds(kv_attn_rows16_kernel<DT, D, CAP>, plan.blocks, 256, plan.lds_bytes, p, st);
     return e != hipSuccess ? e : launch_join<DT, D>(p, st);
 }

@@ -36,6 +36,8 @@ struct AttnParams {
     float* part_ml;    // [splits][batch * max_q][heads_q][2]
     const uint32_t* mask;   // [tokens][mask_ld] of a tree, or nullptr
     int64_t mask_ld;
+    uint32_t even;          // blocks that share a tree's steps evenly, or 0
+    uint32_t* shares;       // [64] running sums of the sequences' steps
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -161,35 +163,29 @@ __device__ __forceinline__ int key_row(int j) {
 // compute K Q, the softmax and the cap in both waves of a pair, and one block fits
 // a CU: prompts of up to 816 tokens, 8 x 8 capped heads, are two uneven rounds of
 // blocks, 28.6 GFLOP in 110 us with neither unit busy half of the time.
-template <int DT, int D, bool CAP, bool TREE>
-__global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
+//
+// One block's rows r0 .. of a (sequence, kv head) against the keys k0 .. k1 - 1 (k0 a
+// multiple of 64); part(row, number) is where a row's partial result goes, -1: the
+// result is whole.
+template <int D>
+constexpr int kPhaseRows = D == 256 ? 128 : 256;
+
+template <int DT, int D, bool CAP, bool TREE, typename F>
+__device__ __forceinline__ void phase_unit(const AttnParams& p, char* lds, const KvSeq& s, int b, int h, int r0, int k0,
+                                           int k1, F part_of) {
     constexpr int TPB = 512;
     constexpr int HV = D == 256 ? 2 : 1;
-    constexpr int ROWS = 32 * 8 / HV;
+    constexpr int ROWS = kPhaseRows<D>;
     constexpr int NS = D / 16;            // k steps of S
     constexpr int ND = D / 32 / HV;       // 32-dimension tiles of the wave's output
     constexpr int NC = D * 4 / TPB > 0 ? D * 4 / TPB : 1;   // 16-byte pieces of k (and of v) a thread stages
     constexpr int AHEAD = D == 256 ? 3 : 6;
     constexpr bool PART = D * 4 < TPB;    // only the first D * 4 threads stage
     constexpr int KB = 64 * D * 2;        // bytes of one operand of a step in LDS
-    extern __shared__ __attribute__((aligned(16))) char lds[];
     typedef float f16v __attribute__((ext_vector_type(16)));
 
-    int64_t u = blockIdx.x;
-    const int h = static_cast<int>(u % p.heads);
-    u /= p.heads;
-    const int sp = static_cast<int>(u % p.splits);
-    u /= p.splits;
-    const int b = static_cast<int>(u % p.ix.batch);
-    const int rt = p.row_tiles - 1 - static_cast<int>(u / p.ix.batch);   // the longest first
-    const KvSeq s = kv_seq(p.ix, b);
-    const int rows = s.n * p.group, r0 = rt * ROWS;
-    if (r0 >= rows) return;
+    const int rows = s.n * p.group;
     const int last = (r0 + ROWS < rows ? r0 + ROWS : rows) - 1;
-    const int vis_hi = row_of<TREE>(p, s, b, h, last).vis;
-    const int k0 = sp * p.split_keys;
-    if (sp > 0 && k0 >= vis_hi) return;
-    const int k1 = k0 + p.split_keys < vis_hi ? k0 + p.split_keys : vis_hi;
     const int steps = k1 > k0 ? (k1 - k0 + 63) >> 6 : 0;
 
     const int tid = threadIdx.x, lane = tid & 63;
@@ -493,7 +489,8 @@ __global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
     if (rw + c >= rows) return;
     // element i of tile d is dimension 32 (half ND + d) + 8 (i / 4) + 4 hf + i % 4 of query c
     const int d0 = 32 * ND * half + 4 * hf;
-    if (p.splits == 1) {
+    const int64_t at = part_of(row, rw + c - r0);
+    if (at < 0) {
         const float inv = l > 0.f ? vo / l : 0.f;
         char* dst = static_cast<char*>(p.out) + (row.token * p.ldo + static_cast<int64_t>(row.head) * D + d0) * 2;
 #pragma unroll
@@ -511,7 +508,6 @@ __global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
                 *reinterpret_cast<uint2*>(dst + (32 * d + 2 * i) * 2) = w;
             }
     } else {
-        const int64_t at = ((static_cast<int64_t>(sp) * p.ix.batch * p.ix.max_q + row.slot) * p.heads_q + row.head);
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
@@ -523,6 +519,30 @@ __global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
             p.part_ml[2 * at + 1] = l;
         }
     }
+}
+
+template <int DT, int D, bool CAP>
+__global__ __launch_bounds__(512, 2) void kv_attn_phase_kernel(AttnParams p) {
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    int64_t u = blockIdx.x;
+    const int h = static_cast<int>(u % p.heads);
+    u /= p.heads;
+    const int sp = static_cast<int>(u % p.splits);
+    u /= p.splits;
+    const int b = static_cast<int>(u % p.ix.batch);
+    const int rt = p.row_tiles - 1 - static_cast<int>(u / p.ix.batch);   // the longest first
+    const KvSeq s = kv_seq(p.ix, b);
+    const int rows = s.n * p.group, r0 = rt * kPhaseRows<D>;
+    if (r0 >= rows) return;
+    const int last = (r0 + kPhaseRows<D> < rows ? r0 + kPhaseRows<D> : rows) - 1;
+    const int vis_hi = row_of<false>(p, s, b, h, last).vis;
+    const int k0 = sp * p.split_keys;
+    if (sp > 0 && k0 >= vis_hi) return;
+    const int k1 = k0 + p.split_keys < vis_hi ? k0 + p.split_keys : vis_hi;
+    phase_unit<DT, D, CAP, false>(p, lds, s, b, h, r0, k0, k1, [&](const Row& row, int) -> int64_t {
+        if (p.splits == 1) return -1;
+        return (static_cast<int64_t>(sp) * p.ix.batch * p.ix.max_q + row.slot) * p.heads_q + row.head;
+    });
 }
 
 // Joins the splits of each (token, head).  GROUPS == 1: D / 8 lanes to each, the
@@ -587,7 +607,7 @@ inline AttnParams attn_params(const KvAttnPlan& plan, const void* q, int64_t ldq
                               float sm_scale, float cap, const uint32_t* mask, int64_t mask_ld, void* out, int64_t ldo,
                               void* ws) {
     AttnParams p{ix, q, ldq, k, v, ks, vs, out, ldo, heads_q, heads, heads_q / heads, sm_scale, cap, plan.row_tiles,
-                 plan.splits, plan.split_keys, nullptr, nullptr, mask, mask_ld};
+                 plan.splits, plan.split_keys, nullptr, nullptr, mask, mask_ld, 0, nullptr};
     if (plan.splits > 1) {
         p.part_o = static_cast<float*>(ws);
         p.part_ml = p.part_o + static_cast<int64_t>(plan.splits) * ix.batch * ix.max_q * heads_q * d;

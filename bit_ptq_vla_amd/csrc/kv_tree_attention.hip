@@ -286,13 +286,153 @@ __global__ __launch_bounds__(256, D < 256 ? 2 : 1) void kv_attn_tree_kernel(Attn
     }
 }
 
+// ---- many rows ---------------------------------------------------------------
+
+// The blocks deal the call's steps (64 keys of one block of rows, "unit") evenly: all
+// units' steps in a row, sequence by sequence, are cut into p.even shares of one length,
+// whatever the sequences' lengths are, so that all CUs end together.  A share covers the
+// end of a unit, whole ones, and the beginning of another; what is not whole leaves
+// partial results, 2 slots of rows to a block: one for a unit that the share does not
+// begin with.
+struct Shares {
+    uint32_t even, total;
+    __device__ __forceinline__ uint32_t from(uint32_t j) const {
+        return static_cast<uint32_t>(static_cast<uint64_t>(j) * total / even);
+    }
+    // The share that a step lies in: the last one that begins no later.
+    __device__ __forceinline__ uint32_t of(uint32_t step) const { return ((step + 1) * even - 1) / total; }   // (below 2^31)
+};
+template <int D>
+__device__ __forceinline__ int units_of(const AttnParams& p, const KvSeq& s) {       // of a head
+    return (s.n * p.group + kPhaseRows<D> - 1) / kPhaseRows<D>;
+}
+__device__ __forceinline__ uint32_t steps_of(const KvSeq& s) { return s.kv > 0 ? (s.kv + 63) >> 6 : 1; }
+
+// 4 trees of up to 256 nodes over up to 16100 keys, 8 heads of 128 for 32, capped (176
+// GFLOP): EVEN_US us, each sequence cut at the same length 403.
+template <int DT, int D, bool CAP>
+__global__ __launch_bounds__(512, 2) void kv_attn_tree_phase_kernel(AttnParams p) {
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    constexpr int ROWS = kPhaseRows<D>;
+    uint32_t* upto = reinterpret_cast<uint32_t*>(lds + 2 * 2 * 64 * D * 2);     // [64] running sums
+    uint32_t* steps = upto + 64;
+    uint32_t at = 0, end = 1, share = 0, begin = 0;
+    if (p.even) {
+        if (threadIdx.x < 64) {
+            const int b = threadIdx.x;
+            uint32_t n = 0, w = 0;
+            if (b < p.ix.batch) {
+                const KvSeq s = kv_seq(p.ix, b);
+                n = steps_of(s);
+                w = n * static_cast<uint32_t>(units_of<D>(p, s)) * static_cast<uint32_t>(p.heads);
+            }
+            w = wave_sum_up(w);
+            upto[b] = w;
+            steps[b] = n;
+            if (blockIdx.x == 0) p.shares[b] = w;
+        }
+        __syncthreads();
+        const Shares shares{p.even, upto[63]};
+        // consecutive shares, often of one head's keys, to one XCD
+        share = p.even % 8 ? blockIdx.x : blockIdx.x % 8 * (p.even / 8) + blockIdx.x / 8;
+        at = begin = __builtin_amdgcn_readfirstlane(shares.from(share));
+        end = __builtin_amdgcn_readfirstlane(shares.from(share + 1));
+        if (at >= end) return;
+    }
+    do {
+        int b, h, rt, k0, k1;
+        int64_t slot = -1;
+        KvSeq s;
+        if (p.even) {
+            b = __builtin_ctzll(__ballot(upto[threadIdx.x & 63] > at));
+            s = kv_seq(p.ix, b);
+            const uint32_t n = __builtin_amdgcn_readfirstlane(steps[b]);
+            const uint32_t off = at - (b > 0 ? __builtin_amdgcn_readfirstlane(upto[b - 1]) : 0), unit = off / n;
+            const uint32_t step = off - unit * n, left = end - at, len = n - step < left ? n - step : left;
+            const int units = units_of<D>(p, s);
+            h = static_cast<int>(unit) / units;
+            rt = static_cast<int>(unit) % units;
+            k0 = 64 * static_cast<int>(step);
+            k1 = s.kv - k0 > 64 * static_cast<int>(len) ? k0 + 64 * static_cast<int>(len) : s.kv;
+            if (len < n) slot = (2 * static_cast<int64_t>(share) + (at > begin ? 1 : 0)) * ROWS;
+            at += len;
+        } else {
+            at = end;
+            h = static_cast<int>(blockIdx.x % p.heads);
+            b = static_cast<int>(blockIdx.x / p.heads % p.ix.batch);
+            rt = static_cast<int>(blockIdx.x / p.heads / p.ix.batch);
+            s = kv_seq(p.ix, b);
+            if (rt * ROWS >= s.n * p.group) return;
+            k0 = 0;
+            k1 = s.kv;
+        }
+        phase_unit<DT, D, CAP, true>(p, lds, s, b, h, rt * ROWS, k0, k1,
+                                     [&](const Row&, int r) -> int64_t { return slot < 0 ? -1 : slot + r; });
+        if (at < end) __syncthreads();
+    } while (at < end);
+}
+
+// Joins the partial results of the rows whose units lie in several shares, D / 8 lanes
+// to each row.
+template <int DT, int D>
+__global__ __launch_bounds__(256) void kv_attn_tree_join_kernel(AttnParams p) {
+    constexpr int LANES = D / 8, ROWS = kPhaseRows<D>;
+    const int64_t u = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / LANES;
+    const int64_t at = u / p.heads_q;
+    const int head = static_cast<int>(u % p.heads_q), d = threadIdx.x % LANES * 8;
+    const int b = static_cast<int>(at / p.ix.max_q), i = static_cast<int>(at % p.ix.max_q);
+    if (b >= p.ix.batch) return;
+    const KvSeq s = kv_seq(p.ix, b);
+    if (i >= s.n) return;
+    const Shares shares{p.even, p.shares[63]};
+    const int r = i * p.group + head % p.group;
+    const uint32_t n = steps_of(s), unit = head / p.group * units_of<D>(p, s) + r / ROWS;
+    const uint32_t from = (b > 0 ? p.shares[b - 1] : 0) + unit * n;
+    const uint32_t first = shares.of(from), last = shares.of(from + n - 1);
+    if (first == last) return;                // the result is there
+    float m = kNegInf, sum = 0.f, f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (uint32_t j = first; j <= last; ++j) {
+        const uint32_t begin = shares.from(j);
+        if (begin == shares.from(j + 1)) continue;            // (fewer steps than shares)
+        const int64_t part = (2 * static_cast<int64_t>(j) + (from > begin ? 1 : 0)) * ROWS + r % ROWS;
+        const float ms = p.part_ml[2 * part], ls = p.part_ml[2 * part + 1];
+        float v[8];
+        load8<F32>(p.part_o + part * D + d, v);
+        const float mn = fmaxf(m, ms), base = mn > kNegInf ? mn : 0.f;
+        const float a = __builtin_amdgcn_exp2f(m - base), c = __builtin_amdgcn_exp2f(ms - base);
+        sum = sum * a + ls * c;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = f[e] * a + v[e] * c;
+        m = mn;
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] *= inv;
+    store8<DT>(static_cast<char*>(p.out) + ((s.row0 + i) * p.ldo + static_cast<int64_t>(head) * D + d) * 2, f);
+}
 
 template <int DT, int D, bool CAP>
-hipError_t launch_cap(const AttnParams& p, const KvAttnPlan& plan, hipStream_t st) {
+hipError_t launch_many(AttnParams p, const KvAttnPlan& plan, void* ws, hipStream_t st) {
+    if (plan.even) {
+        p.even = static_cast<uint32_t>(plan.even);
+        p.shares = static_cast<uint32_t*>(ws);
+        p.part_o = static_cast<float*>(ws) + 64;
+        p.part_ml = p.part_o + 2 * static_cast<int64_t>(plan.even) * kPhaseRows<D> * D;
+    }
+    const hipError_t e =
+        launch_lds(kv_attn_tree_phase_kernel<DT, D, CAP>, plan.blocks, 512, 2 * 2 * 64 * D * 2 + 512, p, st);
+    if (e != hipSuccess || !plan.even) return e;
+    const int64_t lanes = static_cast<int64_t>(p.ix.batch) * p.ix.max_q * p.heads_q * (D / 8);
+    kv_attn_tree_join_kernel<DT, D><<<dim3(static_cast<unsigned>((lanes + 255) / 256)), 256, 0, st>>>(p);
+    return hipGetLastError();
+}
+
+
+template <int DT, int D, bool CAP>
+hipError_t launch_cap(const AttnParams& p, const KvAttnPlan& plan, void* ws, hipStream_t st) {
+    if (plan.many) return launch_many<DT, D, CAP>(p, plan, ws, st);
     hipError_t e;
-    if (plan.many)
-        e = launch_lds(kv_attn_phase_kernel<DT, D, CAP, true>, plan.blocks, 512, 2 * 2 * 64 * D * 2, p, st);
-    else if (D == 256 || plan.tile == 16)        // (32 rows of a 256-wide head do not fit a wave's registers)
+    if (D == 256 || plan.tile == 16)        // (32 rows of a 256-wide head do not fit a wave's registers)
         e = launch_lds(kv_attn_tree_kernel<DT, D, CAP, 1>, plan.blocks, 256, plan.lds_bytes, p, st);
     else
         e = launch_lds(kv_attn_tree_kernel<DT, D, CAP, D == 256 ? 1 : 2>, plan.blocks, 256, plan.lds_bytes, p, st);
@@ -300,11 +440,11 @@ hipError_t launch_cap(const AttnParams& p, const KvAttnPlan& plan, hipStream_t s
 }
 
 template <int DT>
-hipError_t launch_dt(const AttnParams& p, const KvAttnPlan& plan, int d, hipStream_t st) {
+hipError_t launch_dt(const AttnParams& p, const KvAttnPlan& plan, int d, void* ws, hipStream_t st) {
     const bool cap = p.cap > 0.f;
-    if (d == 64) return cap ? launch_cap<DT, 64, true>(p, plan, st) : launch_cap<DT, 64, false>(p, plan, st);
-    if (d == 128) return cap ? launch_cap<DT, 128, true>(p, plan, st) : launch_cap<DT, 128, false>(p, plan, st);
-    return cap ? launch_cap<DT, 256, true>(p, plan, st) : launch_cap<DT, 256, false>(p, plan, st);
+    if (d == 64) return cap ? launch_cap<DT, 64, true>(p, plan, ws, st) : launch_cap<DT, 64, false>(p, plan, ws, st);
+    if (d == 128) return cap ? launch_cap<DT, 128, true>(p, plan, ws, st) : launch_cap<DT, 128, false>(p, plan, ws, st);
+    return cap ? launch_cap<DT, 256, true>(p, plan, ws, st) : launch_cap<DT, 256, false>(p, plan, ws, st);
 }
 
 }  // namespace
@@ -315,7 +455,7 @@ hipError_t launch_kv_attention_tree(const KvAttnPlan& plan, const void* q, int d
                                     int64_t mask_ld, void* out, int64_t ldo, void* ws, hipStream_t st) {
     const AttnParams p =
         attn_params(plan, q, ldq, heads_q, ix, k, v, ks, vs, heads, d, sm_scale, cap, mask, mask_ld, out, ldo, ws);
-    return dtype == F16 ? launch_dt<F16>(p, plan, d, st) : launch_dt<BF16>(p, plan, d, st);
+    return dtype == F16 ? launch_dt<F16>(p, plan, d, ws, st) : launch_dt<BF16>(p, plan, d, ws, st);
 }
 
 }  // namespace qlin

@@ -190,6 +190,7 @@ SamplePlan plan_sample(int64_t rows, int64_t vocab, bool allow_split) {
 // a second one (24 requests of 8 heads, 4097 keys, 384 blocks) 50, none (192) 42.
 static void split_keys(KvAttnPlan& p, int64_t heads, int64_t row_tiles, int64_t rows, int64_t max_kv, int d,
                        bool allow_split) {
+    p.even = 0;
     p.row_tiles = static_cast<int>(row_tiles);
     const int64_t units = heads * row_tiles;
     int64_t splits = 1;
@@ -226,6 +227,8 @@ KvAttnPlan plan_kv_attention(int64_t batch, int64_t max_q, int64_t max_kv, int h
     return p;
 }
 
+constexpr int64_t kEvenRounds = 4;
+
 KvAttnPlan plan_kv_attention_tree(int64_t batch, int64_t max_q, int64_t max_kv, int heads_q, int heads, int d,
                                   bool allow_split) {
     KvAttnPlan p;
@@ -243,7 +246,17 @@ KvAttnPlan plan_kv_attention_tree(int64_t batch, int64_t max_q, int64_t max_kv, 
     p.tile = d < 256 && rows > 16 && max_kv > 0 && tiles > wide / max_kv ? 32 : 16;
     const int64_t per = !p.many ? p.tile : d == 256 ? 128 : 256;
     p.lds_bytes = static_cast<int>(4 * (rows < 16 ? rows : 16) * (d + 6) * 4);
-    split_keys(p, batch * heads, (rows + per - 1) / per, batch * max_q * heads_q, max_kv, d, allow_split);
+    split_keys(p, batch * heads, (rows + per - 1) / per, batch * max_q * heads_q, max_kv, d, allow_split && !p.many);
+    if (p.many && allow_split) {
+        // One block to a CU, all of them with the same number of steps (64 keys of a
+        // block of rows); a wave knows the lengths of 64 sequences.
+        const int64_t cus = device_cus();
+        if (batch <= 64 && p.blocks < kEvenRounds * cus && p.blocks * (max_kv / 64 + 1) < (int64_t{1} << 31) / cus) {
+            p.even = static_cast<int>(cus);
+            p.blocks = cus;
+            p.ws_bytes = 256 + 2 * cus * per * (d + 2) * 4;
+        }
+    }
     // (eight units at a time: see the kernel's order of blocks)
     if (!p.many && p.row_tiles > 0) p.blocks = (p.blocks / p.row_tiles + 7) / 8 * 8 * p.row_tiles;
     return p;

@@ -117,6 +117,7 @@ struct KvAttnPlan {
     int tile;                 // 16 of them (of a tree 16, 32 or 64)
     int lds_bytes;            // of the 16-row blocks
     int row_tiles, splits, split_keys;
+    int even;                 // blocks that share a tree's work evenly (many), or 0
     int64_t blocks, ws_bytes;
 };
 KvAttnPlan plan_kv_attention(int64_t batch, int64_t max_q, int64_t max_kv, int heads_q, int heads, int d,
