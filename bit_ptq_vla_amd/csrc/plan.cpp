@@ -227,8 +227,6 @@ KvAttnPlan plan_kv_attention(int64_t batch, int64_t max_q, int64_t max_kv, int h
     return p;
 }
 
-constexpr int64_t kEvenRounds = 4;
-
 KvAttnPlan plan_kv_attention_tree(int64_t batch, int64_t max_q, int64_t max_kv, int heads_q, int heads, int d,
                                   bool allow_split) {
     KvAttnPlan p;
@@ -249,9 +247,14 @@ KvAttnPlan plan_kv_attention_tree(int64_t batch, int64_t max_q, int64_t max_kv, 
     split_keys(p, batch * heads, (rows + per - 1) / per, batch * max_q * heads_q, max_kv, d, allow_split && !p.many);
     if (p.many && allow_split) {
         // One block to a CU, all of them with the same number of steps (64 keys of a
-        // block of rows); a wave knows the lengths of 64 sequences.
+        // block of rows); a wave knows the lengths of 64 sequences.  us for a block to
+        // each block of rows / for even shares, 128 wide, 256 nodes of 8 x 4 heads over
+        // 3000 keys, lengths alike: 0.5 blocks to a CU 136 / 99, 1 151 / 149, 1.1 261 /
+        // 194, 1.5 262 / 233, 2 284 / 287, 2.5 399 / 370, 3 422 / 428, 3.9 567 / 584;
+        // lengths between 1500 and 3000: 125 / 87, 134 / 138, 170 / 150, 211 / 185, 228 /
+        // 236, 287 / 283, 333 / 346, 450 / 458; 256 wide: 0.75 326 / 277, 1.5 505 / 516.
         const int64_t cus = device_cus();
-        if (batch <= 64 && p.blocks < kEvenRounds * cus && p.blocks * (max_kv / 64 + 1) < (int64_t{1} << 31) / cus) {
+        if (batch <= 64 && p.blocks < 3 * cus && p.blocks * (max_kv / 64 + 1) < (int64_t{1} << 31) / cus) {
             p.even = static_cast<int>(cus);
             p.blocks = cus;
             p.ws_bytes = 256 + 2 * cus * per * (d + 2) * 4;
