@@ -29,9 +29,9 @@
 //
 // Bound by the pass that fills the bins, about 25 vector instructions and an LDS atomic
 // (two with a top-k) to a logit, and behind it by a chain of scans and barriers, 10 to 20
-// us: 1024 rows of 32003 bf16 logits with mixed filters (66 MB) take 84 us, 256 of
+// us: 1024 rows of 32003 bf16 logits with mixed filters (66 MB) take 82 us, 256 of
 // 257152 fp32 logits without any (263 MB, read again for the last bin) 130, one of 32000
-// 29.
+// 28.
 
 #include "device_common.h"
 #include "qlin_internal.h"
@@ -727,23 +727,38 @@ struct Sampler {
     static __device__ __forceinline__ Token among_list(const Scale& sc, uint32_t n, const Settings& set, uint32_t least,
                                                 uint64_t whole, Shared& s) {
         const uint32_t t = threadIdx.x;
-        uint64_t mine = 0;
-        if (t < n) {
-            mine = s.list.order[t];
-            s.list.mass[t] = to_top(s.list.mass[t], depth_of(sc, logit_of(~static_cast<uint32_t>(mine >> 32))), s);
+        // ranks: where there are fewer elements than threads, several threads to each
+        const uint32_t width = n > 1 ? 1u << (32 - __builtin_clz(n - 1)) : 1, share = (n * width + kThreads - 1) / kThreads;
+        const uint32_t e = t & (width - 1), from = t / width * share, to = from + share < n ? from + share : n;
+        uint64_t mine = e < n ? s.list.order[e] : 0, m = 0;
+        if (t < n) m = to_top(s.list.mass[t], depth_of(sc, logit_of(~static_cast<uint32_t>(mine >> 32))), s);
+        if (t < 8) s.list.order[n + t] = ~0ull;
+        s.count[t] = 0;
+        __syncthreads();
+        if (e < n) {
+            uint32_t rank = 0;
+            for (uint32_t j0 = from; j0 < to; j0 += 8) {
+                uint64_t o[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = s.list.order[j0 + j];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) rank += o[j] < mine && j0 + j < to;
+            }
+            atomicAdd(&s.count[e], rank);
         }
         __syncthreads();
         if (t < n) {
-            uint64_t ahead;
-            uint32_t rank;
-            rank_of(mine, s.list.order, s.list.mass, n, rank, ahead);
-            s.list.sorted.order[rank] = mine;
-            s.list.sorted.ahead[rank] = ahead;
-            if (rank == n - 1) s.found64[0] = ahead + s.list.mass[t];
+            s.list.sorted.order[s.count[t]] = mine;
+            s.list.sorted.ahead[s.count[t]] = m;
         }
         __syncthreads();
         mine = t < n ? s.list.sorted.order[t] : ~0ull;
-        const uint64_t all = s.found64[0], ahead = t < n ? s.list.sorted.ahead[t] : all;
+        m = t < n ? s.list.sorted.ahead[t] : 0;
+        const uint64_t behind = block_scan(m, s.part64), ahead = behind - m;       // (the mass up to and with it)
+        if (t < n) s.list.sorted.ahead[t] = ahead;
+        if (t == n - 1) s.found64[0] = behind;
+        __syncthreads();
+        const uint64_t all = s.found64[0];
         auto upto = [&](uint32_t kept) { return kept < n ? s.list.sorted.ahead[kept] : all; };
         uint32_t kept = __syncthreads_count(t < n && ~static_cast<uint32_t>(mine >> 32) >= least);
         kept = set.top_k < kept ? set.top_k : kept;
@@ -754,7 +769,7 @@ struct Sampler {
         }
         bool exact;
         const uint64_t goal = part_of(units_of(set.u), mass, &exact);
-        const uint32_t at = __syncthreads_count(t < kept && upto(t + 1) <= goal);
+        const uint32_t at = __syncthreads_count(t < kept && behind <= goal);
         mine = s.list.sorted.order[at];
         return {~static_cast<uint32_t>(mine >> 32), static_cast<int>(static_cast<uint32_t>(mine)), mass};
     }
