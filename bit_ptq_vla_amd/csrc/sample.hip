@@ -29,8 +29,8 @@
 //
 // Bound by the pass that fills the bins, about 25 vector instructions and an LDS atomic
 // (two with a top-k) to a logit, and behind it by a chain of scans and barriers, 10 to 20
-// us: 1024 rows of 32003 bf16 logits with mixed filters (66 MB) take 82 us, 256 of
-// 257152 fp32 logits without any (263 MB, read again for the last bin) 130, one of 32000
+// us: 1024 rows of 32003 bf16 logits with mixed filters (66 MB) take 59 us, 256 of
+// 257152 fp32 logits without any (263 MB, read again for the last bin) 128, one of 32000
 // 28.
 
 #include "device_common.h"
@@ -49,6 +49,14 @@ constexpr int kList = 1536;              // elements that are listed at once
 constexpr int kNear = 512;               // of them, that are all ranked
 constexpr int kFew = 64;                 // of them, that answer one question
 constexpr uint64_t kOne = 1ull << 44;
+
+// The thread's number, new to the compiler at every use: it would otherwise compute what
+// follows from it for all the phases of a row at once, and spill 70 registers.
+__device__ __forceinline__ int thread() {
+    int t = threadIdx.x;
+    asm volatile("" : "+v"(t));
+    return t;
+}
 
 // A value that all lanes hold, in scalar registers.
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __builtin_amdgcn_readfirstlane(static_cast<int>(x)); }
@@ -182,7 +190,7 @@ struct Sampler {
         uint4 w[kWords];
 
         __device__ __forceinline__ static int index(int first, int j, int e) {
-            return first + (kThreads * j + static_cast<int>(threadIdx.x)) * N + e;
+            return first + (kThreads * j + thread()) * N + e;
         }
         // The word at element i, -infinity from the end on.
         __device__ __forceinline__ static uint4 word_at(const char* row, int i, int end) {
@@ -257,8 +265,8 @@ struct Sampler {
     template <typename T>
     static __device__ __forceinline__ T block_scan(T v, T* parts) {
         v = wave_sum_up(v);
-        const int wave = threadIdx.x >> 6;
-        if ((threadIdx.x & 63) == 63) parts[wave] = v;
+        const int wave = thread() >> 6;
+        if ((thread() & 63) == 63) parts[wave] = v;
         __syncthreads();
         T before = 0;
 #pragma unroll
@@ -276,7 +284,7 @@ struct Sampler {
         v = more(v, dpp_u<0x118, 0xF>(v));
         v = more(v, dpp_u<0x142, 0xA>(v));
         v = more(v, dpp_u<0x143, 0xC>(v));
-        if ((threadIdx.x & 63) == 63) parts[threadIdx.x >> 6] = v;
+        if ((thread() & 63) == 63) parts[thread() >> 6] = v;
         __syncthreads();
         v = parts[0];
 #pragma unroll
@@ -292,7 +300,7 @@ struct Sampler {
         uint32_t c[PER], count = 0;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            f(PER * threadIdx.x + j, m[j], c[j]);
+            f(PER * thread() + j, m[j], c[j]);
             mass += m[j];
             count += c[j];
         }
@@ -302,7 +310,7 @@ struct Sampler {
         for (int j = 0; j < PER; ++j) {
             before += m[j];
             ahead += c[j];
-            g(PER * threadIdx.x + j, before, ahead);
+            g(PER * thread() + j, before, ahead);
         }
         __syncthreads();
     }
@@ -310,7 +318,7 @@ struct Sampler {
     // First bin whose running sum passes the target (some bin does).
     template <typename T>
     static __device__ __forceinline__ int first_past(const T* run, int n, T target, Shared& s) {
-        for (int i = threadIdx.x; i < n; i += kThreads)
+        for (int i = thread(); i < n; i += kThreads)
             if (run[i] > target && (i == 0 || run[i - 1] <= target)) s.found32[0] = i;
         __syncthreads();
         const int b = uniform(s.found32[0]);
@@ -325,7 +333,7 @@ struct Sampler {
         uint32_t lo = kKeyNone, hi = top;                // not at lo, at hi
         while (hi - lo > 1) {
             const uint32_t step = (hi - lo - 1) / 64 + 1;
-            const uint64_t at = static_cast<uint64_t>(lo) + static_cast<uint64_t>(step) * ((threadIdx.x & 63) + 1);
+            const uint64_t at = static_cast<uint64_t>(lo) + static_cast<uint64_t>(step) * ((thread() & 63) + 1);
             const uint64_t votes = __ballot(at >= hi || holds(static_cast<uint32_t>(at)));
             const uint32_t n = __builtin_ctzll(votes);   // (the last lane is at hi or behind it)
             const uint64_t next = static_cast<uint64_t>(lo) + static_cast<uint64_t>(step) * (n + 1);
@@ -396,11 +404,11 @@ struct Sampler {
     // Keys of the bin i below the largest.
     static __device__ __forceinline__ Range keys_of(const Scale& sc, uint32_t top_key, int i, Shared& s) {
         if (sc.lone) return {top_key, top_key};
-        const int wave = threadIdx.x >> 6;
+        const int wave = thread() >> 6;
         if (wave < 2) {
             const double bin = sc.top - i + wave;        // (behind bin 0's keys there are none)
             const uint32_t k = first_key(top_key, [&](uint32_t key) { return bin_at(sc, logit_of(key)) >= bin; });
-            if ((threadIdx.x & 63) == 0) s.found32[wave] = k;
+            if ((thread() & 63) == 0) s.found32[wave] = k;
         }
         __syncthreads();
         const Range range{uniform(s.found32[0]), i == 0 ? top_key : uniform(s.found32[1]) - 1};
@@ -419,7 +427,7 @@ struct Sampler {
         });
         m = block_scan(m, s.part64);
         n = block_scan(n, s.part32);
-        if (threadIdx.x == kThreads - 1) {
+        if (thread() == kThreads - 1) {
             s.found64[0] = m;
             s.found32[0] = n;
         }
@@ -432,7 +440,7 @@ struct Sampler {
     // Lists the elements with keys in the range: their orders and masses (in their bins'
     // units).  Returns how many there are; past kList only some are listed.
     static __device__ __forceinline__ uint32_t list_range(const Row& row, const Scale& sc, Range range, Shared& s) {
-        if (threadIdx.x == 0) s.found32[1] = 0;
+        if (thread() == 0) s.found32[1] = 0;
         __syncthreads();
         in_range(row, range.lo, range.hi, [&](int i) {
             const uint32_t n = atomicAdd(&s.found32[1], 1u);
@@ -440,7 +448,7 @@ struct Sampler {
         });
         __syncthreads();
         const uint32_t n = uniform(s.found32[1]);
-        for (uint32_t e = threadIdx.x; e < n && e < kList; e += kThreads) {
+        for (uint32_t e = thread(); e < n && e < kList; e += kThreads) {
             const uint32_t i = static_cast<uint32_t>(s.list.order[e]);
             const float v = row.value(static_cast<int>(i));
             s.list.order[e] = static_cast<uint64_t>(~key_of(v)) << 32 | i;
@@ -454,7 +462,7 @@ struct Sampler {
     // its order is in s.found64[1], the mass up to and with it in [0]; returns the mass
     // of those left out before.  While there are many, 512 parts of their range at a time.
     static __device__ __forceinline__ uint64_t of_list(bool by_count, uint64_t left, uint32_t n, Shared& s) {
-        const uint32_t t = threadIdx.x, all = n;
+        const uint32_t t = thread(), all = n;
         uint64_t lo = 0, hi = ~0ull, passed = 0;
         while (n > kFew) {
             uint64_t most = 0, least = 0;            // (the least by its complement)
@@ -530,7 +538,7 @@ struct Sampler {
                                            uint64_t& passed, uint32_t& nth, uint64_t& one, Shared& s) {
         const uint32_t width = range.hi - range.lo;
         const int shift = width < kSub ? 0 : 21 - __builtin_clz(width);
-        for (int i = threadIdx.x; i < kSub; i += kThreads) {
+        for (int i = thread(); i < kSub; i += kThreads) {
             s.sub.mass[i] = 0;
             s.sub.count[i] = 0;
         }
@@ -582,7 +590,7 @@ struct Sampler {
                 for (uint32_t k = upto - here; k < nth; ++k) bits &= bits - 1;
                 s.found32[1] = i0 + __builtin_ctz(bits);
             }
-            if (threadIdx.x == kThreads - 1) s.found32[2] = upto;
+            if (thread() == kThreads - 1) s.found32[2] = upto;
             __syncthreads();
             seen = uniform(s.found32[2]);
             __syncthreads();
@@ -603,7 +611,7 @@ struct Sampler {
     // sc; the largest key (kKeyNone: no element).
     static __device__ __forceinline__ uint32_t fill_bins(const Row& row, bool with_count, Scale& sc, Shared& s) {
         constexpr int N = Chunk::N;
-        for (int i = threadIdx.x; i < kSlots; i += kThreads) {
+        for (int i = thread(); i < kSlots; i += kThreads) {
             s.mass[i] = 0;
             s.count[i] = 0;
         }
@@ -625,12 +633,12 @@ struct Sampler {
                 const double rise = sc.top - was.top;
                 if (top_key != kKeyNone) {
                     if (sc.lone || was.lone || rise >= kSlots) {     // far above all before: the ring starts anew
-                        for (int i = threadIdx.x; i < kSlots; i += kThreads) {
+                        for (int i = thread(); i < kSlots; i += kThreads) {
                             s.mass[i] = 0;
                             s.count[i] = 0;
                         }
                     } else {                                         // slots between hold bins 64 octaves lower
-                        for (int i = threadIdx.x; i < static_cast<int>(rise); i += kThreads) {
+                        for (int i = thread(); i < static_cast<int>(rise); i += kThreads) {
                             s.mass[slot_of(was.top + 1 + i)] = 0;
                             s.count[slot_of(was.top + 1 + i)] = 0;
                         }
@@ -654,7 +662,7 @@ struct Sampler {
                 // (what lies below the window goes to slots of its own: no branch keeps the
                 // elements' arithmetic apart)
                 const double least = sc.top - kBins;
-                const int none = kSlots + static_cast<int>(threadIdx.x & 63);
+                const int none = kSlots + static_cast<int>(thread() & 63);
                 const Series series;
                 c.words([&](uint4 word) {
                     int slot[N];
@@ -700,14 +708,14 @@ struct Sampler {
 
     // The smallest key with w >= min_p.
     static __device__ __forceinline__ uint32_t least_key(const Scale& sc, uint32_t top_key, float min_p, Shared& s) {
-        if (threadIdx.x < 64) {
+        if (thread() < 64) {
             const float top = logit_of(top_key);
             const double least = -log2(static_cast<double>(min_p)) * 32.0;
             const uint32_t k = first_key(top_key, [&](uint32_t key) {
                 const float v = logit_of(key);
                 return v == top || (static_cast<double>(top) - static_cast<double>(v)) * sc.c <= least;
             });
-            if (threadIdx.x == 0) s.found32[3] = k;
+            if (thread() == 0) s.found32[3] = k;
         }
         __syncthreads();
         const uint32_t k = uniform(s.found32[3]);
@@ -726,7 +734,7 @@ struct Sampler {
     // what top-p counts, else 0.
     static __device__ __forceinline__ Token among_list(const Scale& sc, uint32_t n, const Settings& set, uint32_t least,
                                                 uint64_t whole, Shared& s) {
-        const uint32_t t = threadIdx.x;
+        const uint32_t t = thread();
         // ranks: where there are fewer elements than threads, several threads to each
         const uint32_t width = n > 1 ? 1u << (32 - __builtin_clz(n - 1)) : 1, share = (n * width + kThreads - 1) / kThreads;
         const uint32_t e = t & (width - 1), from = t / width * share, to = from + share < n ? from + share : n;
@@ -775,7 +783,7 @@ struct Sampler {
     }
 
     static __device__ __forceinline__ void store_token(const SampleArgs& a, int r, const Scale& sc, const Token& token) {
-        if (threadIdx.x != 0) return;
+        if (thread() != 0) return;
         a.token[r] = token.index;
         if (!a.logprob) return;
         const float v = logit_of(token.key);
@@ -795,7 +803,7 @@ struct Sampler {
     }
 
     static __device__ __forceinline__ void store_largest(const SampleArgs& a, int r, uint64_t best) {
-        if (threadIdx.x != 0) return;
+        if (thread() != 0) return;
         const bool none = static_cast<uint32_t>(best >> 32) == kKeyNone;
         a.token[r] = none ? -1 : static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(best));
         if (a.logprob) a.logprob[r] = none ? __builtin_nanf("") : 0.f;
@@ -809,14 +817,14 @@ struct Sampler {
         constexpr int N = Chunk::N;
         const float scale = static_cast<float>(sc.c), base = logit_of(top_key) * scale;
         auto place = [&](float v) { return fmaf(-v, scale, base); };      // (no number for a NaN; what is not below kBins is left out)
-        for (int i = threadIdx.x; i < kSlots + 64; i += kThreads) s.count[i] = 0;
+        for (int i = thread(); i < kSlots + 64; i += kThreads) s.count[i] = 0;
         __syncthreads();
         row.words([&](int, uint4 word) {
             int slot[N];
 #pragma unroll
             for (int e = 0; e < N; ++e) {
                 const float d = place(Chunk::value(word, e));
-                slot[e] = d < static_cast<float>(kBins) ? static_cast<int>(fmaxf(d, 0.f)) : kSlots + static_cast<int>(threadIdx.x & 63);
+                slot[e] = d < static_cast<float>(kBins) ? static_cast<int>(fmaxf(d, 0.f)) : kSlots + static_cast<int>(thread() & 63);
             }
 #pragma unroll
             for (int e = 0; e < N; ++e) atomicAdd(&s.count[slot[e]], 1u);
@@ -834,9 +842,9 @@ struct Sampler {
         if (s.run_count[kBins - 1] < top_k) return false;
         const int reach = first_past(s.run_count, kBins, top_k - 1, s);
         if (s.run_count[reach] > kNear) return false;
-        if (threadIdx.x < 64) {
+        if (thread() < 64) {
             const uint32_t k = first_key(top_key, [&](uint32_t key) { return place(logit_of(key)) < static_cast<float>(reach + 1); });
-            if (threadIdx.x == 0) s.found32[3] = k;
+            if (thread() == 0) s.found32[3] = k;
         }
         __syncthreads();
         from = uniform(s.found32[3]);
@@ -1006,7 +1014,7 @@ struct Sampler {
         return best;
     }
     static __device__ __forceinline__ void fill_tables(Shared& s) {
-        const int t = threadIdx.x;
+        const int t = thread();
         if (t < 32) {
             s.down[t] = static_cast<uint64_t>(exp2(-t / 32.0) * 0x1p63);
             s.up[t] = exp2(t / 32.0);
@@ -1058,17 +1066,17 @@ __global__ __launch_bounds__(kThreads, 4) void sample_part_kernel(SampleArgs a, 
     Part& o = out[blockIdx.x];
     if (!(temp > 0.f)) {
         const uint64_t best = S::block_max(S::largest(row), s.part64);
-        if (threadIdx.x == 0) o.best = best;
+        if (thread() == 0) o.best = best;
         return;
     }
     Scale sc = scale_of(temp);
     const bool counting = counts(a, r);
     const uint32_t top = S::fill_bins(row, counting, sc, s);
-    if (threadIdx.x == 0) {
+    if (thread() == 0) {
         o.best = static_cast<uint64_t>(top) << 32;
         o.top = sc.lone ? -__builtin_inf() : sc.top;
     }
-    for (int i = threadIdx.x; i < kBins; i += kThreads) {
+    for (int i = thread(); i < kBins; i += kThreads) {
         o.mass[i] = s.mass[slot_of(sc.top - i)];
         if (counting) o.count[i] = s.count[slot_of(sc.top - i)];
     }
@@ -1079,7 +1087,7 @@ template <int DT>
 __global__ __launch_bounds__(kThreads, 4) void sample_join_kernel(SampleArgs a, int parts, const Part* in) {
     using S = Sampler<DT>;
     __shared__ typename S::Shared s;
-    const int r = blockIdx.x, t = threadIdx.x;
+    const int r = blockIdx.x, t = thread();
     in += static_cast<int64_t>(r) * parts;
     uint64_t best = 0;
     for (int p = t; p < parts; p += kThreads) best = in[p].best > best ? in[p].best : best;
