@@ -192,19 +192,22 @@ struct Sampler {
         __device__ __forceinline__ static int index(int first, int j, int e) {
             return first + (kThreads * j + thread()) * N + e;
         }
-        // The word at element i, -infinity from the end on.
+        // The word at element i, -infinity from the end on.  (One word of a row lies across its
+        // end: only its wave goes through the loads of single elements, each with a wait.)
         __device__ __forceinline__ static uint4 word_at(const char* row, int i, int end) {
             constexpr uint32_t none = DT == F32 ? 0xFF800000u : DT == BF16 ? 0xFF80FF80u : 0xFC00FC00u;
             if (i + N <= end) return *reinterpret_cast<const uint4*>(row + static_cast<int64_t>(i) * (16 / N));
             uint32_t x[4] = {none, none, none, none};
+            if (i < end) {
 #pragma unroll
-            for (int e = 0; e < N - 1; ++e) {
-                if (i + e >= end) continue;
-                if constexpr (DT == F32) {
-                    x[e] = reinterpret_cast<const uint32_t*>(row)[i + e];
-                } else {
-                    const uint32_t b = reinterpret_cast<const uint16_t*>(row)[i + e];
-                    x[e / 2] = e & 1 ? (x[e / 2] & 0xFFFFu) | b << 16 : (x[e / 2] & 0xFFFF0000u) | b;
+                for (int e = 0; e < N - 1; ++e) {
+                    if (i + e >= end) continue;
+                    if constexpr (DT == F32) {
+                        x[e] = reinterpret_cast<const uint32_t*>(row)[i + e];
+                    } else {
+                        const uint32_t b = reinterpret_cast<const uint16_t*>(row)[i + e];
+                        x[e / 2] = e & 1 ? (x[e / 2] & 0xFFFFu) | b << 16 : (x[e / 2] & 0xFFFF0000u) | b;
+                    }
                 }
             }
             return make_uint4(x[0], x[1], x[2], x[3]);
@@ -218,6 +221,14 @@ struct Sampler {
             if constexpr (DT == F32) return __uint_as_float(x[e]);
             if constexpr (DT == BF16) return __uint_as_float(e & 1 ? x[e / 2] & 0xFFFF0000u : x[e / 2] << 16);
             return f16_bits_to_f32(static_cast<uint16_t>(e & 1 ? x[e / 2] >> 16 : x[e / 2] & 0xFFFFu));
+        }
+        // The same for an element that is known late.
+        __device__ __forceinline__ static float value_late(uint4 word, int e) {
+            const int at = e / (N / 4);
+            const uint32_t lo = at & 1 ? word.y : word.x, hi = at & 1 ? word.w : word.z, x = at & 2 ? hi : lo;
+            if constexpr (DT == F32) return __uint_as_float(x);
+            if constexpr (DT == BF16) return __uint_as_float(e & 1 ? x & 0xFFFF0000u : x << 16);
+            return f16_bits_to_f32(static_cast<uint16_t>(e & 1 ? x >> 16 : x & 0xFFFFu));
         }
         template <typename F>
         __device__ __forceinline__ void words(F f) const {
@@ -239,19 +250,19 @@ struct Sampler {
         // from the first on, or from the last, whose words a pass before left in the caches.
         template <bool BACK, typename F>
         __device__ __forceinline__ void words_to(F f) const {
-            constexpr int step = kThreads * Chunk::N;
+            constexpr int step = kThreads * Chunk::N, AHEAD = 4;
             const int n = (to - from + step - 1) / step;
             auto at_step = [&](int k) { return Chunk::index(from + (BACK ? n - 1 - k : k) * step, 0, 0); };
             auto word = [&](int k) { return Chunk::word_at(at, k < n ? at_step(k) : to, to); };
-            uint4 w[4];
+            uint4 w[AHEAD];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = word(j);
-            for (int k = 0; k < n; k += 4) {
+            for (int j = 0; j < AHEAD; ++j) w[j] = word(j);
+            for (int k = 0; k < n; k += AHEAD) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < AHEAD; ++j) {
                     if (k + j >= n) break;
                     f(at_step(k + j), w[j]);
-                    w[j] = word(k + j + 4);          // (in place: a copy would wait for it)
+                    w[j] = word(k + j + AHEAD);      // (in place: a copy would wait for it)
                 }
             }
         }
@@ -353,7 +364,7 @@ struct Sampler {
         return x < static_cast<double>(most) ? static_cast<uint64_t>(x) : most;
     }
 
-    // f(index) for the elements with keys from lo_key to hi_key.
+    // f(index, value) for the elements with keys from lo_key to hi_key.
     template <typename F>
     static __device__ __forceinline__ void in_range(const Row& row, uint32_t lo_key, uint32_t hi_key, F f) {
         const float lo = logit_of(lo_key), hi = logit_of(hi_key);
@@ -370,7 +381,8 @@ struct Sampler {
 #pragma unroll
             for (int e = 0; e < Chunk::N; ++e) bits |= in(word, e) ? 1u << e : 0;
             while (bits) {
-                f(i0 + __builtin_ctz(bits));
+                const int e = __builtin_ctz(bits);
+                f(i0 + e, Chunk::value_late(word, e));
                 bits &= bits - 1;
             }
         });
@@ -421,8 +433,8 @@ struct Sampler {
                                            uint32_t& count) {
         uint64_t m = 0;
         uint32_t n = 0;
-        in_range(row, range.lo, range.hi, [&](int i) {
-            m += mass_of(sc, row.value(i));
+        in_range(row, range.lo, range.hi, [&](int, float v) {
+            m += mass_of(sc, v);
             ++n;
         });
         m = block_scan(m, s.part64);
@@ -442,18 +454,14 @@ struct Sampler {
     static __device__ __forceinline__ uint32_t list_range(const Row& row, const Scale& sc, Range range, Shared& s) {
         if (thread() == 0) s.found32[1] = 0;
         __syncthreads();
-        in_range(row, range.lo, range.hi, [&](int i) {
+        in_range(row, range.lo, range.hi, [&](int i, float v) {
             const uint32_t n = atomicAdd(&s.found32[1], 1u);
-            if (n < kList) s.list.order[n] = static_cast<uint32_t>(i);
+            if (n < kList) s.list.order[n] = static_cast<uint64_t>(~key_of(v)) << 32 | static_cast<uint32_t>(i);
         });
         __syncthreads();
         const uint32_t n = uniform(s.found32[1]);
-        for (uint32_t e = thread(); e < n && e < kList; e += kThreads) {
-            const uint32_t i = static_cast<uint32_t>(s.list.order[e]);
-            const float v = row.value(static_cast<int>(i));
-            s.list.order[e] = static_cast<uint64_t>(~key_of(v)) << 32 | i;
-            s.list.mass[e] = mass_of(sc, v);
-        }
+        for (uint32_t e = thread(); e < n && e < kList; e += kThreads)
+            s.list.mass[e] = mass_of(sc, logit_of(~static_cast<uint32_t>(s.list.order[e] >> 32)));
         __syncthreads();
         return n;
     }
@@ -543,8 +551,7 @@ struct Sampler {
             s.sub.count[i] = 0;
         }
         __syncthreads();
-        in_range(row, range.lo, range.hi, [&](int i) {
-            const float v = row.value(i);
+        in_range(row, range.lo, range.hi, [&](int, float v) {
             const uint32_t b = (range.hi - key_of(v)) >> shift;
             atomicAdd(reinterpret_cast<unsigned long long*>(&s.sub.mass[b]), mass_of(sc, v));
             atomicAdd(&s.sub.count[b], 1u);
