@@ -145,6 +145,8 @@ __device__ __forceinline__ Scale scale_of(float temp) {
     return sc;
 }
 
+__device__ const uint4 kNoWord{};        // (of a row that is shorter than a word)
+
 template <int DT>
 struct Sampler {
     struct Shared {
@@ -182,7 +184,7 @@ struct Sampler {
     };
 
     // 16-byte words of a row in a thread's registers: element e of word j is index
-    // first + (1024 j + thread) N + e, -infinity past the end.
+    // first + (512 j + thread) N + e, -infinity past the end.
     struct Chunk {
         static constexpr int N = DT == F32 ? 4 : 8;
         static constexpr int kWords = 4;
@@ -192,11 +194,11 @@ struct Sampler {
         __device__ __forceinline__ static int index(int first, int j, int e) {
             return first + (kThreads * j + thread()) * N + e;
         }
-        // The word at element i, -infinity from the end on.  (One word of a row lies across its
-        // end: only its wave goes through the loads of single elements, each with a wait.)
-        __device__ __forceinline__ static uint4 word_at(const char* row, int i, int end) {
+        // The word at element i, of which all that lies below end was loaded if that was all of
+        // it; -infinity from the end on.
+        __device__ __forceinline__ static uint4 ended(uint4 loaded, const char* row, int i, int end) {
             constexpr uint32_t none = DT == F32 ? 0xFF800000u : DT == BF16 ? 0xFF80FF80u : 0xFC00FC00u;
-            if (i + N <= end) return *reinterpret_cast<const uint4*>(row + static_cast<int64_t>(i) * (16 / N));
+            if (i + N <= end) return loaded;
             uint32_t x[4] = {none, none, none, none};
             if (i < end) {
 #pragma unroll
@@ -212,9 +214,18 @@ struct Sampler {
             }
             return make_uint4(x[0], x[1], x[2], x[3]);
         }
-        __device__ __forceinline__ void load(const char* row, int first, int end) {
+        // (loads that every thread makes, whatever the row's end: behind one that may not be
+        // made, all that are on their way would be waited for)
+        template <typename R>
+        __device__ __forceinline__ void load(const R& row, int first) {
 #pragma unroll
-            for (int j = 0; j < kWords; ++j) w[j] = word_at(row, index(first, j, 0), end);
+            for (int j = 0; j < kWords; ++j) w[j] = row.word((index(first, j, 0) - row.from) / N);
+        }
+        template <typename R>
+        __device__ __forceinline__ void end(const R& row, int first) {
+            if (first + kSize <= row.to) return;
+#pragma unroll
+            for (int j = 0; j < kWords; ++j) w[j] = ended(w[j], row.at, index(first, j, 0), row.to);
         }
         __device__ __forceinline__ static float value(uint4 word, int e) {
             const uint32_t x[4] = {word.x, word.y, word.z, word.w};
@@ -241,28 +252,35 @@ struct Sampler {
     struct Row {
         const char* at;
         int from, to;
-        __device__ __forceinline__ float value(int i) const {
-            if constexpr (DT == F32) return reinterpret_cast<const float*>(at)[i];
-            const uint16_t b = reinterpret_cast<const uint16_t*>(at)[i];
-            return DT == BF16 ? bf16_to_f32(b) : f16_bits_to_f32(b);
+        const uint4* whole;          // its whole words, and how many follow the first
+        uint32_t more;
+        __device__ __forceinline__ Row(const char* at_, int from_, int to_) : at(at_), from(from_), to(to_) {
+            const bool any = to - from >= Chunk::N;
+            whole = any ? reinterpret_cast<const uint4*>(at + static_cast<int64_t>(from) * (16 / Chunk::N)) : &kNoWord;
+            more = any ? (to - from) / Chunk::N - 1 : 0;
+        }
+        // The word of that number, the last whole one behind it.
+        __device__ __forceinline__ uint4 word(int number) const {
+            const uint32_t n = static_cast<uint32_t>(number);
+            return whole[n < more ? n : more];
         }
         // f(index of its first element, word) for the thread's words, four more on their way:
         // from the first on, or from the last, whose words a pass before left in the caches.
         template <bool BACK, typename F>
         __device__ __forceinline__ void words_to(F f) const {
             constexpr int step = kThreads * Chunk::N, AHEAD = 4;
-            const int n = (to - from + step - 1) / step;
-            auto at_step = [&](int k) { return Chunk::index(from + (BACK ? n - 1 - k : k) * step, 0, 0); };
-            auto word = [&](int k) { return Chunk::word_at(at, k < n ? at_step(k) : to, to); };
+            const int n = (to - from + step - 1) / step, t = thread();
+            auto number = [&](int k) { return (BACK ? n - 1 - k : k) * kThreads + t; };
             uint4 w[AHEAD];
 #pragma unroll
-            for (int j = 0; j < AHEAD; ++j) w[j] = word(j);
+            for (int j = 0; j < AHEAD; ++j) w[j] = word(number(j));
             for (int k = 0; k < n; k += AHEAD) {
 #pragma unroll
                 for (int j = 0; j < AHEAD; ++j) {
                     if (k + j >= n) break;
-                    f(at_step(k + j), w[j]);
-                    w[j] = word(k + j + AHEAD);      // (in place: a copy would wait for it)
+                    const int i = from + number(k + j) * Chunk::N;
+                    f(i, Chunk::ended(w[j], at, i, to));
+                    w[j] = word(number(k + j + AHEAD));      // (in place: a copy would wait for it)
                 }
             }
         }
@@ -624,10 +642,11 @@ struct Sampler {
         }
         uint32_t top_key = kKeyNone;
         Chunk c;
-        c.load(row.at, row.from, row.to);
+        c.load(row, row.from);
         for (int from = row.from; from < row.to; from += Chunk::kSize) {
             Chunk next;
-            next.load(row.at, from + Chunk::kSize, row.to);      // on its way meanwhile
+            next.load(row, from + Chunk::kSize);                 // on its way meanwhile
+            c.end(row, from);
             float most = -__builtin_inff();
             c.words([&](uint4 word) {
 #pragma unroll
@@ -1042,7 +1061,7 @@ __global__ __launch_bounds__(kThreads, 4) void sample_kernel(SampleArgs a) {
     using S = Sampler<DT>;
     __shared__ typename S::Shared s;
     const int r = blockIdx.x;
-    const typename S::Row row{row_at<DT>(a, r), 0, a.vocab};
+    const typename S::Row row(row_at<DT>(a, r), 0, a.vocab);
     const float temp = temperature_of(a, r);
     if (!(temp > 0.f)) {
         S::store_largest(a, r, S::block_max(S::largest(row), s.part64));
@@ -1068,7 +1087,7 @@ __global__ __launch_bounds__(kThreads, 4) void sample_part_kernel(SampleArgs a, 
     using S = Sampler<DT>;
     __shared__ typename S::Shared s;
     const int r = blockIdx.x / parts, p = blockIdx.x % parts, from = p * size;
-    const typename S::Row row{row_at<DT>(a, r), from, from + size < a.vocab ? from + size : a.vocab};
+    const typename S::Row row(row_at<DT>(a, r), from, from + size < a.vocab ? from + size : a.vocab);
     const float temp = temperature_of(a, r);
     Part& o = out[blockIdx.x];
     if (!(temp > 0.f)) {
@@ -1106,7 +1125,7 @@ __global__ __launch_bounds__(kThreads, 4) void sample_join_kernel(SampleArgs a, 
         return;
     }
     S::fill_tables(s);
-    const typename S::Row row{row_at<DT>(a, r), 0, a.vocab};
+    const typename S::Row row(row_at<DT>(a, r), 0, a.vocab);
     Scale sc = scale_of(temp);
     set_top(sc, logit_of(top));
     S::choose(a, r, row, sc, top, true, s, [&] {
