@@ -29,9 +29,9 @@
 //
 // Bound by the pass that fills the bins, about 25 vector instructions and an LDS atomic
 // (two with a top-k) to a logit, and behind it by a chain of scans and barriers, 10 to 20
-// us: 1024 rows of 32003 bf16 logits with mixed filters (66 MB) take 59 us, 256 of
-// 257152 fp32 logits without any (263 MB, read again for the last bin) 128, one of 32000
-// 28.
+// us: 1024 rows of 32003 bf16 logits with mixed filters (66 MB) take 50 us, 256 of
+// 257152 fp32 logits without any (263 MB, read again for the last bin) 129, one of 32000
+// 26.
 
 #include "device_common.h"
 #include "qlin_internal.h"
@@ -145,7 +145,11 @@ __device__ __forceinline__ Scale scale_of(float temp) {
     return sc;
 }
 
-__device__ const uint4 kNoWord{};        // (of a row that is shorter than a word)
+// A word of memory behind a pointer that is known to be global: a load that might go
+// anywhere waits for all that are on their way.
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef const __attribute__((address_space(1))) u4* GlobalWords;
+__device__ const u4 kNoWord = {0, 0, 0, 0};        // (of a row that is shorter than a word)
 
 template <int DT>
 struct Sampler {
@@ -252,36 +256,43 @@ struct Sampler {
     struct Row {
         const char* at;
         int from, to;
-        const uint4* whole;          // its whole words, and how many follow the first
+        GlobalWords whole;           // its whole words, and how many follow the first
         uint32_t more;
         __device__ __forceinline__ Row(const char* at_, int from_, int to_) : at(at_), from(from_), to(to_) {
             const bool any = to - from >= Chunk::N;
-            whole = any ? reinterpret_cast<const uint4*>(at + static_cast<int64_t>(from) * (16 / Chunk::N)) : &kNoWord;
+            whole = any ? (GlobalWords)(at + static_cast<int64_t>(from) * (16 / Chunk::N)) : (GlobalWords)&kNoWord;
             more = any ? (to - from) / Chunk::N - 1 : 0;
         }
         // The word of that number, the last whole one behind it.
         __device__ __forceinline__ uint4 word(int number) const {
             const uint32_t n = static_cast<uint32_t>(number);
-            return whole[n < more ? n : more];
+            const u4 w = whole[n < more ? n : more];
+            return make_uint4(w[0], w[1], w[2], w[3]);
         }
-        // f(index of its first element, word) for the thread's words, four more on their way:
+        // f(index of its first element, word) for the thread's words, two more on their way:
         // from the first on, or from the last, whose words a pass before left in the caches.
+        // (In pairs that start together: one load at a time, four ahead, read 263 MB again in
+        // 40 us where this takes 30.)
         template <bool BACK, typename F>
         __device__ __forceinline__ void words_to(F f) const {
-            constexpr int step = kThreads * Chunk::N, AHEAD = 4;
+            constexpr int step = kThreads * Chunk::N, AHEAD = 2;
             const int n = (to - from + step - 1) / step, t = thread();
             auto number = [&](int k) { return (BACK ? n - 1 - k : k) * kThreads + t; };
-            uint4 w[AHEAD];
+            uint4 w[AHEAD], next[AHEAD];
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j) w[j] = word(number(j));
             for (int k = 0; k < n; k += AHEAD) {
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j) next[j] = word(number(k + j + AHEAD));
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int j = 0; j < AHEAD; ++j) {
                     if (k + j >= n) break;
                     const int i = from + number(k + j) * Chunk::N;
                     f(i, Chunk::ended(w[j], at, i, to));
-                    w[j] = word(number(k + j + AHEAD));      // (in place: a copy would wait for it)
                 }
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j) w[j] = next[j];
             }
         }
         template <typename F>
