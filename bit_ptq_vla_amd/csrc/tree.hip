@@ -8,8 +8,8 @@
 // lane to a node, for its mask words from the last to the first (parents come
 // before their children, so a walk meets the bits in falling order), and down
 // from node 0 by one lane.  The time is a launch and a chain of loads, walk and
-// stores: a plan and an accepted path take 12.1 us for one tree of 16 nodes, 12.3
-// for 64 of 256, two launches' 6.6 and what the calls cost on the host.
+// stores: a plan and an accepted path take 12 to 13 us for one tree of 16 nodes
+// as for 64 of 256, two launches' 6.6 and what the calls cost on the host.
 
 #include <hip/hip_runtime.h>
 
