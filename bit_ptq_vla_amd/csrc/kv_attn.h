@@ -32,7 +32,7 @@ struct AttnParams {
     int heads_q, heads, group;
     float sm_scale, cap;
     int row_tiles, splits, split_keys;
-    float* part_o;     // [splits][batch * max_q][heads_q][D]
+    float* part_o;     // [splits][batch * max_q][heads_q][D]; with even: [2 even][rows of a block][D]
     float* part_ml;    // [splits][batch * max_q][heads_q][2]
     const uint32_t* mask;   // [tokens][mask_ld] of a tree, or nullptr
     int64_t mask_ld;
