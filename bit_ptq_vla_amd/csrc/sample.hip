@@ -1135,8 +1135,12 @@ __global__ __launch_bounds__(kThreads, 4) void sample_join_kernel(SampleArgs a, 
         S::store_largest(a, r, best);
         return;
     }
-    S::fill_tables(s);
     const typename S::Row row(row_at<DT>(a, r), 0, a.vocab);
+    // the row's first 128 KB, a line to a load, on their way to this XCD's cache
+    uint4 line[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) line[j] = row.word(8 * (kThreads * j + t));
+    S::fill_tables(s);
     Scale sc = scale_of(temp);
     set_top(sc, logit_of(top));
     S::choose(a, r, row, sc, top, true, s, [&] {
@@ -1148,22 +1152,33 @@ __global__ __launch_bounds__(kThreads, 4) void sample_join_kernel(SampleArgs a, 
             s.offset[p] = key == kKeyNone || (sc.lone && key != top) || !(below < kBins) ? kBins : static_cast<int>(below);
         }
         __syncthreads();
-        for (int i = t; i < kBins; i += kThreads) {
-            uint64_t m = 0;
-            uint32_t c = 0;
+        // (loads that every thread makes: those of all bins are out together)
+        constexpr int kEach = (kBins + kThreads - 1) / kThreads;
+        uint64_t m[kEach] = {};
+        uint32_t c[kEach] = {};
 #pragma unroll 4
-            for (int p = 0; p < parts; ++p) {
-                const int at = i - s.offset[p];
+        for (int p = 0; p < parts; ++p) {
+            const int below = s.offset[p];
+#pragma unroll
+            for (int j = 0; j < kEach; ++j) {
+                const int i = t + kThreads * j, at = i < kBins ? i - below : -1;
                 const uint64_t pm = in[p].mass[at < 0 ? 0 : at];
-                m += at < 0 ? 0 : pm;
-                if (counting) c += at < 0 ? 0 : in[p].count[at];
+                m[j] += at < 0 ? 0 : pm;
+                if (counting) c[j] += at < 0 ? 0 : in[p].count[at];
             }
-            s.mass[slot_of(sc.top - i)] = m;
-            s.count[slot_of(sc.top - i)] = c;
+        }
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+            const int i = t + kThreads * j;
+            if (i >= kBins) continue;
+            s.mass[slot_of(sc.top - i)] = m[j];
+            s.count[slot_of(sc.top - i)] = c[j];
         }
         __syncthreads();
         return top;
     });
+#pragma unroll
+    for (int j = 0; j < 2; ++j) asm volatile("" ::"v"(line[j].x));
 }
 
 template <int DT>
