@@ -355,11 +355,16 @@ struct Sampler {
         __syncthreads();
     }
 
-    // First bin whose running sum passes the target (some bin does).
-    template <typename T>
-    static __device__ __forceinline__ int first_past(const T* run, int n, T target, Shared& s) {
-        for (int i = thread(); i < n; i += kThreads)
-            if (run[i] > target && (i == 0 || run[i - 1] <= target)) s.found32[0] = i;
+    // First of the N bins whose running sum passes the target (some bin does).
+    template <int N, typename T>
+    static __device__ __forceinline__ int first_past(const T* run, T target, Shared& s) {
+        const int t = thread();
+#pragma unroll
+        for (int j = 0; j < (N + kThreads - 1) / kThreads; ++j) {
+            const int i = t + kThreads * j, at = i < N ? i : N - 1;
+            const T before = run[at > 0 ? at - 1 : 0];
+            if (i < N && run[at] > target && (i == 0 || before <= target)) s.found32[0] = i;
+        }
         __syncthreads();
         const int b = uniform(s.found32[0]);
         __syncthreads();
@@ -596,8 +601,8 @@ struct Sampler {
                 s.sub.mass[i] = m;
                 s.sub.count[i] = c;
             });
-        const int b = by_count ? first_past(s.sub.count, kSub, static_cast<uint32_t>(left), s)
-                               : first_past(s.sub.mass, kSub, left, s);
+        const int b = by_count ? first_past<kSub>(s.sub.count, static_cast<uint32_t>(left), s)
+                               : first_past<kSub>(s.sub.mass, left, s);
         const uint64_t mass_b = b ? uniform(s.sub.mass[b - 1]) : 0, mass_here = uniform(s.sub.mass[b]) - mass_b;
         const uint32_t count_b = b ? uniform(s.sub.count[b - 1]) : 0, count_here = uniform(s.sub.count[b]) - count_b;
         passed += mass_b;
@@ -877,7 +882,7 @@ struct Sampler {
                 if (i < kBins) s.run_count[i] = c;
             });
         if (s.run_count[kBins - 1] < top_k) return false;
-        const int reach = first_past(s.run_count, kBins, top_k - 1, s);
+        const int reach = first_past<kBins>(s.run_count, top_k - 1, s);
         if (s.run_count[reach] > kNear) return false;
         if (thread() < 64) {
             const uint32_t k = first_key(top_key, [&](uint32_t key) { return place(logit_of(key)) < static_cast<float>(reach + 1); });
@@ -956,10 +961,10 @@ struct Sampler {
                 // the last bin that any of it can reach
                 int reach = least_bin < kBins ? least_bin : kBins - 1;
                 if (set.top_k <= all) {
-                    const int b = first_past(s.run_count, kBins, set.top_k - 1, s);
+                    const int b = first_past<kBins>(s.run_count, set.top_k - 1, s);
                     reach = b < reach ? b : reach;
                 } else if (least_bin == kBins && set.top_p < 1.f) {
-                    reach = first_past(s.run_mass, kBins, last_kept(set.top_p, mass), s);
+                    reach = first_past<kBins>(s.run_mass, last_kept(set.top_p, mass), s);
                     whole = mass;
                 }
                 if (s.run_count[reach] <= kNear) {
@@ -995,8 +1000,8 @@ struct Sampler {
                     bool exact;
                     target = part_of(units_of(set.u), mass, &exact);
                 }
-                bin = step == 0 ? first_past(s.run_count, kBins, static_cast<uint32_t>(target), s)
-                                : first_past(s.run_mass, kBins, target, s);
+                bin = step == 0 ? first_past<kBins>(s.run_count, static_cast<uint32_t>(target), s)
+                                : first_past<kBins>(s.run_mass, target, s);
                 before = bin ? uniform(s.run_mass[bin - 1]) : 0;
                 left = step == 0 ? target - (bin ? uniform(s.run_count[bin - 1]) : 0)
                                  : uniform(from_top(target - before, bin, s.mass[slot_of(sc.top - bin)] - 1, s));
