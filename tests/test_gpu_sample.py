@@ -205,3 +205,16 @@ def test_frequencies_follow_the_weights():
     share = np.bincount(token, minlength=5) / n
     assert np.all(np.abs(share - w) <= 2.0 / n)
     assert np.allclose(np.exp(logprob.astype(np.float64)), w[token], rtol=1e-6)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+def test_a_small_top_k_behind_a_min_p_that_keeps_many(dtype):
+    """Rows of which min-p keeps thousands and top-k a few, ties among them."""
+    x, g = draw(9, 6000, dtype, 77, std=0.6)
+    x[3] = (x[3] * 4).round() / 4
+    x[4] = 0.25
+    top_k = np.array([1, 2, 37, 100, 250, 256, 200, 255, 16])
+    min_p = np.array([0.01, 0.02, 0.005, 0.01, 0.5, 0.01, 0.002, 0.03, 0.01])
+    top_p = np.array([1.0, 0.9, 0.8, 0.7, 0.6, 0.95, 1.0, 0.5, 0.99])
+    for shift in range(3):
+        check(x, g.random(9), top_k=top_k, min_p=min_p, top_p=np.roll(top_p, shift), temperature=np.full(9, 0.9 + 0.2 * shift))
