@@ -18,7 +18,7 @@ namespace {
 // us, a join among them), by the vector units' issue where there is much: 64 trees of up
 // to 16 nodes over up to 4080 keys, 8 heads of 128 for 32 (421 MB) take 127 us, 3.3 TB/s;
 // a step of 32 rows and 64 keys is about 800 vector instructions, which keep the SIMDs
-// 63% busy, the matrix units 20%.  Blocks of 16 rows whose row tiles did not share an L2
+// 50 to 63% busy, the matrix units 15 to 20%.  Blocks of 16 rows whose row tiles did not share an L2
 // took 212; a wave with 64 rows spills.
 template <int DT, int D, bool CAP, int NQ>
 __global__ __launch_bounds__(256, D < 256 ? 2 : 1) void kv_attn_tree_kernel(AttnParams p) {

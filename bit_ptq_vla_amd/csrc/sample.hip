@@ -29,9 +29,9 @@
 //
 // Bound by the pass that fills the bins, about 25 vector instructions and an LDS atomic
 // (two with a top-k) to a logit, and behind it by a chain of scans and barriers, 10 to 20
-// us: 1024 rows of 32003 bf16 logits with mixed filters (66 MB) take 50 us, 256 of
+// us: 1024 rows of 32003 bf16 logits with mixed filters (66 MB) take 48 us, 256 of
 // 257152 fp32 logits without any (263 MB, read again for the last bin) 130, one of 32000
-// 24.
+// 26.
 
 #include "device_common.h"
 #include "qlin_internal.h"
