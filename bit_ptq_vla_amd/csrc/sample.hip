@@ -35,6 +35,7 @@
 
 #include "device_common.h"
 #include "qlin_internal.h"
+#include "sample_keys.h"
 
 namespace qlin {
 
@@ -67,18 +68,6 @@ __device__ __forceinline__ uint64_t uniform(uint64_t x) {
 }
 __device__ __forceinline__ double uniform(double x) {
     return __longlong_as_double(static_cast<long long>(uniform(static_cast<uint64_t>(__double_as_longlong(x)))));
-}
-
-// Logits as ordered integers; equal logits (the zeros too) have equal keys.  NaN is
-// -infinity: neither is ever taken.
-constexpr uint32_t kKeyNone = 0x007FFFFFu;      // of -infinity
-__device__ __forceinline__ uint32_t key_of(float v) {
-    const uint32_t b = __float_as_uint(v + 0.f);
-    if (v != v) return kKeyNone;
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ float logit_of(uint32_t key) {
-    return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
 }
 
 struct Scale {
@@ -444,9 +433,7 @@ struct Sampler {
         }
     }
 
-    struct Range {
-        uint32_t lo, hi;
-    };
+    using Range = KeyRange;
     // Keys of the bin i below the largest.
     static __device__ __forceinline__ Range keys_of(const Scale& sc, uint32_t top_key, int i, Shared& s) {
         if (sc.lone) return {top_key, top_key};
@@ -607,9 +594,7 @@ struct Sampler {
         const uint32_t count_b = b ? uniform(s.sub.count[b - 1]) : 0, count_here = uniform(s.sub.count[b]) - count_b;
         passed += mass_b;
         left -= by_count ? count_b : mass_b;
-        const uint32_t hi = range.hi - (static_cast<uint32_t>(b) << shift), part = (1u << shift) - 1;
-        range.lo = hi - range.lo > part ? hi - part : range.lo;
-        range.hi = hi;
+        range = part_of_range(range, shift, static_cast<uint32_t>(b));
         __syncthreads();
         if (range.lo != range.hi) return false;
         one = mass_here / count_here;

@@ -218,3 +218,29 @@ def test_a_small_top_k_behind_a_min_p_that_keeps_many(dtype):
     top_p = np.array([1.0, 0.9, 0.8, 0.7, 0.6, 0.95, 1.0, 0.5, 0.99])
     for shift in range(3):
         check(x, g.random(9), top_k=top_k, min_p=min_p, top_p=np.roll(top_p, shift), temperature=np.full(9, 0.9 + 0.2 * shift))
+
+
+@pytest.mark.parametrize("vocab", [40, 1500, 5000])
+@pytest.mark.parametrize("top", [255, 256, 511, 2 ** 19 + 255])
+def test_zeros_among_denormals(vocab, top):
+    """Elements at and around zero, whose weights are equal and whose order is that of
+    their bits: the parts that the row is narrowed to end at, above and right below zero."""
+    g = np.random.default_rng(vocab + top)
+    rows = 9
+    steps = g.integers(-300, 256, (rows, vocab))
+    steps[:, ::3] = 0
+    steps[3] = g.integers(-300, 1, vocab)
+    steps[4] = g.integers(-2 ** 22, 256, vocab)
+    steps[5] = np.where(g.random(vocab) < 0.5, 0, -1)
+    steps[:, vocab // 2] = top
+    x = np.ldexp(steps.astype(np.float64), -149).astype(np.float32)
+    x[:, 1::4] = np.where(x[:, 1::4] == 0, np.float32(-0.0), x[:, 1::4])
+    x[6, 5:9] = -1.0
+    y = torch.zeros((rows, -(-vocab // 8) * 8))
+    y[:, :vocab] = torch.from_numpy(x)
+    y = y.to(DEV)[:, :vocab]
+    assert np.array_equal(y.cpu().numpy().view(np.int32), x.view(np.int32))
+    for workspace in (True, False):
+        check(y, (np.arange(rows) + g.random(rows)) / rows, workspace)
+        check(y, (np.arange(rows) + g.random(rows))[::-1] / rows, workspace, top_p=g.uniform(0.3, 0.99, rows))
+        check(y, g.random(rows), workspace, top_k=g.integers(vocab // 3, vocab, rows))
