@@ -414,10 +414,14 @@ __global__ __launch_bounds__(256) void compact_kernel(KvIndex ix, KvStackArgs c,
                 const int e = e0 + lane, i = e / per, j = e % per;
                 const int pg_i = __shfl(from, i & 63, 64), off_i = __shfl(off, i & 63, 64);
                 const float scale_i = __shfl(scale, i & 63, 64);
-                if (e >= (hi - lo) * per) continue;
+                const bool there = e < (hi - lo) * per;
                 uint4 w = make_uint4(0, 0, 0, 0);
-                if (pg_i != kNoPage) w = follow16(reinterpret_cast<const uint4*>(base_of(pg_i) + off_i * d)[j], scale_i, now);
-                reinterpret_cast<uint4*>(dst + (kept + i) * d)[j] = w;
+                if (there && pg_i != kNoPage) w = reinterpret_cast<const uint4*>(base_of(pg_i) + off_i * d)[j];
+                // (a token's old place is another one's new place: all lanes have read before one writes)
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                if (there && pg_i != kNoPage) w = follow16(w, scale_i, now);
+                if (there) reinterpret_cast<uint4*>(dst + (kept + i) * d)[j] = w;
             }
         } else {
             for (int g = 0; g < ps; g += 16) {
