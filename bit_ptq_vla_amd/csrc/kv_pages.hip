@@ -348,10 +348,13 @@ __device__ __forceinline__ uint4 follow16(uint4 w, float was, float now) {
 //
 // Bound by the chain page table, scales, codes, stores at five waves to a SIMD, and by
 // what shares the moved codes' cache lines: 64 paths of 8 of 32 nodes in 16 layers of 8
-// heads of 128 (29 MB of moved codes; some 60 MB are read and 48 written, with the tokens
-// whose page's scale rises) take 38 us, one path of 5 of 16 in 32 layers of 32 heads 8.
-// A wave for a head's k and v takes 35 and 8, a wave for 64 dimensions of v 60 and 7:
-// each wave repeats the chain.
+// heads of 128 (29 MB of moved codes, node 0's among them, which stays where it is; some
+// 60 MB are read and 46 written, since v's move by whole granules, 16 bytes to a row of a
+// page) take 36 us where no page's scale rises, 39 where scales do and kept tokens follow
+// them; one path of 5 of 16 in 32 layers of 32 heads 8.  Granules of v whose tokens are all
+// kept under the same scale are left alone (written back: 48 MB, 38 us).  A wave for a
+// head's k and v takes 35 and 8, a wave for 64 dimensions of v 60 and 7 (both with those
+// granules written): each wave repeats the chain.
 __global__ __launch_bounds__(256) void compact_kernel(KvIndex ix, KvStackArgs c, const int32_t* path, int64_t path_ld,
                                                       const int32_t* count, int32_t* len_out, int groups) {
     __shared__ int16_t node[kMaxTreeNodes];
@@ -427,7 +430,7 @@ __global__ __launch_bounds__(256) void compact_kernel(KvIndex ix, KvStackArgs c,
             for (int g = 0; g < ps; g += 16) {
                 // places g .. g + 15 of the page: kept ones, then tokens, then others
                 const int k1 = kept - g < 0 ? 0 : kept - g > 16 ? 16 : kept - g;
-                const int i1 = kept + hi - lo - g;
+                const int i1 = kept + hi - lo - g > 16 ? 16 : kept + hi - lo - g;
                 if (i1 <= 0 || (i1 <= k1 && was == now)) continue;
                 for (int j = lane; j < d; j += 64) {
                     uint4* x = reinterpret_cast<uint4*>(dst + j * ps + g);

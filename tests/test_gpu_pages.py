@@ -247,3 +247,33 @@ def test_compact_with_zero_scales_and_captured():
         assert out.tolist() == [32]
         for name in ("k_scale", "v_scale", "k", "v"):
             assert np.array_equal(getattr(c.cache, name).cpu().numpy(), c.host[name]), name
+
+
+@pytest.mark.parametrize("page,cached,nodes,path", [
+    (64, 48, 16, [0, 3, 9, 15]), (64, 47, 40, [0, 1, 2, 16, 17, 30, 39]), (32, 16, 8, [3, 7]), (64, 1, 63, [0, 62]),
+    (32, 31, 70, list(range(0, 70, 3))), (16, 15, 33, [0, 32])])
+@pytest.mark.parametrize("equal", [True, False])
+def test_granules_of_kept_tokens(page, cached, nodes, path, equal):
+    """Granules of a page whose tokens are all kept: under one scale for all pages, where
+    nothing of them changes, and under scales of their own."""
+    cols = -(-(cached + nodes) // page)
+    c = Cache(cols + 1, page, 2, 64, seed=cached + page, spread=3.0)
+    if equal:
+        c.host["k_scale"][:] = 0.03
+        c.host["v_scale"][:] = 0.02
+        c.upload()
+    table = c.table(1, cols)
+    batch = q.KvBatch(i32(table), i32([0, nodes]), i32([cached + nodes]), max_q=nodes, max_kv=cols * page)
+    wide = np.full((1, nodes), -1)
+    wide[0, :len(path)] = path
+    before = {n: x.copy() for n, x in c.host.items()}
+    got = q.qlin_kv_compact(q.KvStack([c.cache]), batch, i32(wide), i32([len(path)]))
+    torch.cuda.synchronize()
+    assert got.tolist() == oracle.kv_compact([c.host], table, [0, nodes], [cached + nodes], wide, [len(path)])
+    for name in ("k_scale", "v_scale", "k", "v"):
+        assert np.array_equal(getattr(c.cache, name).cpu().numpy(), c.host[name]), name
+    if equal:
+        first = table[0, 0]
+        kept = min(cached, page)
+        assert np.array_equal(c.host["k"][first][:, :kept], before["k"][first][:, :kept])
+        assert np.array_equal(c.host["v"][first][:, :, :kept], before["v"][first][:, :, :kept])
