@@ -143,7 +143,7 @@ hipError_t launch_tree_accept(const KvIndex& ix, const int32_t* parents, const i
 
 // A token from each row of logits (the arrays of settings may be null).
 constexpr int64_t kMaxVocab = 1 << 18;
-constexpr int kSampleBins = 46 * 32;
+constexpr int kSampleBins = 64 * 32;
 struct SampleArgs {
     const void* logits;
     int64_t ld;

@@ -9,10 +9,17 @@
 // two, and its mass is 2^44 2^((a - rint(a)) / 32), an integer: bins do not depend on
 // the row's maximum, so one pass over the row fills them without knowing it, and
 // integer sums have no order: any split of a row over threads and blocks, and any
-// order of their atomics, gives the same token.  The 46 octaves below the largest bin
-// count (what lies lower weighs less than 2^-45 of it).  a - rint(a) is one fused
-// product in float64, exact but for its last rounding, and the mass is evaluated in
-// float64 to 2^-46 of itself.
+// order of their atomics, gives the same token.  The 64 octaves below the largest bin
+// count (what lies lower weighs less than 2^-63 of it, all of it together less than
+// 2^-45).  a - rint(a) is one fused product in float64, exact but for its last
+// rounding, and the mass is evaluated in float64 to 2^-46 of itself.
+//
+// How far sums are off, in units of 2^-44 of the largest weight, of which a row's mass
+// has 2^44 at least: bins come to the largest one's units with 20 bits behind the
+// point, listed elements with 9, so that what 2048 bins or 512 elements cut off is one
+// unit; a target, a bin's share of it and the mass behind a filter are rounded to one
+// each.  With a weight's own rounding, 2^-44 of itself, a filter and the token are
+// decided as exact weights decide them unless top_p or u lies within 2^-40 of a border.
 //
 // Each filter, and the token itself, is one question: the first element of the
 // order at which the running count, or mass, passes a target.  The bins' running
@@ -44,12 +51,14 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
 constexpr int kSlots = 2048;             // of the ring of bins
-constexpr int kBins = kSampleBins;       // 46 octaves
+constexpr int kBins = kSampleBins;       // 64 octaves: every slot of the ring
 constexpr int kSub = 2048;               // bins of a histogram over keys
-constexpr int kList = 1536;              // elements that are listed at once
+constexpr int kList = 1408;              // elements that are listed at once (two blocks fill a CU's LDS)
 constexpr int kNear = 512;               // of them, that are all ranked
 constexpr int kFew = 64;                 // of them, that answer one question
+constexpr int kFine = 9;                 // bits of listed elements' masses behind a unit (kNear of them stay below 2^63)
 constexpr uint64_t kOne = 1ull << 44;
+static_assert(kBins == kSlots, "the window is the ring");
 
 // The thread's number, new to the compiler at every use: it would otherwise compute what
 // follows from it for all the phases of a row at once, and spill 70 registers.
@@ -323,10 +332,10 @@ struct Sampler {
     }
 
     // Running sums of mass and count [kThreads * PER], from f(i, mass, count) to g(i, ..).
-    template <int PER, typename F, typename G>
-    static __device__ __forceinline__ void run_up(uint64_t* parts64, uint32_t* parts32, F f, G g) {
+    template <int PER, typename C, typename F, typename G>
+    static __device__ __forceinline__ void run_up(uint64_t* parts64, C* parts, F f, G g) {
         uint64_t m[PER], mass = 0;
-        uint32_t c[PER], count = 0;
+        C c[PER], count = 0;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
             f(PER * thread() + j, m[j], c[j]);
@@ -334,7 +343,7 @@ struct Sampler {
             count += c[j];
         }
         uint64_t before = block_scan(mass, parts64) - mass;
-        uint32_t ahead = block_scan(count, parts32) - count;
+        C ahead = block_scan(count, parts) - count;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
             before += m[j];
@@ -377,9 +386,17 @@ struct Sampler {
         return hi;
     }
 
-    // m in units of a bin i below the largest, in those of the largest, and back.
-    static __device__ __forceinline__ uint64_t to_top(uint64_t m, int i, const Shared& s) {
-        return i == 0 ? m : __umul64hi(m, s.down[i & 31]) << 1 >> (i >> 5);      // m below 2^63
+    // m (below 2^63) in units of a bin i below the largest, in those of the largest: whole
+    // ones, and 2^-20 of them; and back.
+    struct Mass {
+        uint64_t whole;
+        uint32_t part;
+    };
+    static __device__ __forceinline__ Mass to_top(uint64_t m, int i, const Shared& s) {
+        const uint64_t down = s.down[i & 31], lo = m * down, hi = __umul64hi(m, down) << 1 | lo >> 63;
+        const int k = i >> 5;
+        const uint64_t rest = k ? hi << (64 - k) | lo << 1 >> k : lo << 1;
+        return {hi >> k, static_cast<uint32_t>(rest >> 44)};
     }
     static __device__ __forceinline__ uint64_t from_top(uint64_t m, int i, uint64_t most, const Shared& s) {
         if (i == 0) return m;
@@ -753,7 +770,7 @@ struct Sampler {
     struct Token {
         uint32_t key;
         int index;
-        uint64_t mass;             // of all that was kept
+        double mass;               // of all that was kept
     };
 
     // The list's n <= kNear elements, each at its rank, and the token.  All that the
@@ -766,7 +783,7 @@ struct Sampler {
         const uint32_t width = n > 1 ? 1u << (32 - __builtin_clz(n - 1)) : 1, share = (n * width + kThreads - 1) / kThreads;
         const uint32_t e = t & (width - 1), from = t / width * share, to = from + share < n ? from + share : n;
         uint64_t mine = e < n ? s.list.order[e] : 0, m = 0;
-        if (t < n) m = to_top(s.list.mass[t], depth_of(sc, logit_of(~static_cast<uint32_t>(mine >> 32))), s);
+        if (t < n) m = to_top(s.list.mass[t] << kFine, depth_of(sc, logit_of(~static_cast<uint32_t>(mine >> 32))), s).whole;
         if (t < 8) s.list.order[n + t] = ~0ull;
         s.count[t] = 0;
         __syncthreads();
@@ -797,16 +814,18 @@ struct Sampler {
         auto upto = [&](uint32_t kept) { return kept < n ? s.list.sorted.ahead[kept] : all; };
         uint32_t kept = __syncthreads_count(t < n && ~static_cast<uint32_t>(mine >> 32) >= least);
         kept = set.top_k < kept ? set.top_k : kept;
-        uint64_t mass = whole ? whole : upto(kept);
+        uint64_t mass = upto(kept);
         if (set.top_p < 1.f) {
-            kept = __syncthreads_count(t < kept && ahead <= last_kept(set.top_p, mass));
+            const uint64_t last = whole ? last_kept(set.top_p, whole) << kFine | ((1u << kFine) - 1) : last_kept(set.top_p, mass);
+            kept = __syncthreads_count(t < kept && ahead <= last);
             mass = upto(kept);
         }
         bool exact;
         const uint64_t goal = part_of(units_of(set.u), mass, &exact);
         const uint32_t at = __syncthreads_count(t < kept && behind <= goal);
         mine = s.list.sorted.order[at];
-        return {~static_cast<uint32_t>(mine >> 32), static_cast<int>(static_cast<uint32_t>(mine)), mass};
+        return {~static_cast<uint32_t>(mine >> 32), static_cast<int>(static_cast<uint32_t>(mine)),
+                static_cast<double>(mass) * (1.0 / (1 << kFine))};
     }
 
     static __device__ __forceinline__ void store_token(const SampleArgs& a, int r, const Scale& sc, const Token& token) {
@@ -814,7 +833,7 @@ struct Sampler {
         a.token[r] = token.index;
         if (!a.logprob) return;
         const float v = logit_of(token.key);
-        const double share = static_cast<double>(mass_of(sc, v)) / static_cast<double>(token.mass);
+        const double share = static_cast<double>(mass_of(sc, v)) / token.mass;
         const double y = log(share) - depth_of(sc, v) * (0.6931471805599453 / 32);
         a.logprob[r] = static_cast<float>(y < 0.0 ? y : 0.0);
     }
@@ -857,15 +876,13 @@ struct Sampler {
             for (int e = 0; e < N; ++e) atomicAdd(&s.count[slot[e]], 1u);
         });
         __syncthreads();
-        run_up<kSlots / kThreads>(
+        run_up<kBins / kThreads>(
             s.part64, s.part32,
             [&](int i, uint64_t& m, uint32_t& c) {
                 m = 0;
-                c = i < kBins ? s.count[i] : 0;
+                c = s.count[i];
             },
-            [&](int i, uint64_t, uint32_t c) {
-                if (i < kBins) s.run_count[i] = c;
-            });
+            [&](int i, uint64_t, uint32_t c) { s.run_count[i] = c; });
         if (s.run_count[kBins - 1] < top_k) return false;
         const int reach = first_past<kBins>(s.run_count, top_k - 1, s);
         if (s.run_count[reach] > kNear) return false;
@@ -916,26 +933,26 @@ struct Sampler {
                     store_largest(a, r, static_cast<uint64_t>(kKeyNone) << 32);
                     return;
                 }
-                run_up<kSlots / kThreads>(
-                    s.part64, s.part32,
-                    [&](int i, uint64_t& m, uint32_t& c) {
-                        m = 0;
-                        c = 0;
-                        if (i >= kBins) return;
+                // (a bin's count above the part of its mass behind the point, whose sums stay below 2^31)
+                run_up<kBins / kThreads>(
+                    s.part64, s.part64,
+                    [&](int i, uint64_t& m, uint64_t& c) {
                         const uint64_t raw = s.mass[slot_of(sc.top - i)];
-                        m = to_top(raw, i, s);
+                        const Mass x = to_top(raw, i, s);
+                        uint32_t n;
                         if (counting) {
-                            c = s.count[slot_of(sc.top - i)];
+                            n = s.count[slot_of(sc.top - i)];
                         } else {
                             // masses are within 1.1% of 2^44
-                            const float n = static_cast<float>(raw) * 0x1p-44f;
-                            c = static_cast<uint32_t>(rintf(n) + floorf(n * (1.f / 45)));
+                            const float f = static_cast<float>(raw) * 0x1p-44f;
+                            n = static_cast<uint32_t>(rintf(f) + floorf(f * (1.f / 45)));
                         }
+                        m = x.whole;
+                        c = static_cast<uint64_t>(n) << 32 | x.part;
                     },
-                    [&](int i, uint64_t m, uint32_t c) {
-                        if (i >= kBins) return;
-                        s.run_mass[i] = m;
-                        s.run_count[i] = c;
+                    [&](int i, uint64_t m, uint64_t c) {
+                        s.run_mass[i] = m + (static_cast<uint32_t>(c) >> 20);
+                        s.run_count[i] = static_cast<uint32_t>(c >> 32);
                     });
                 mass = uniform(s.run_mass[kBins - 1]);
                 all = uniform(s.run_count[kBins - 1]);
@@ -961,7 +978,7 @@ struct Sampler {
                         uint64_t m;
                         uint32_t n;
                         sum_of(row, sc, {least, keys_of(sc, top_key, least_bin, s).hi}, s, m, n);
-                        mass = (least_bin ? uniform(s.run_mass[least_bin - 1]) : 0) + uniform(to_top(m, least_bin, s));
+                        mass = (least_bin ? uniform(s.run_mass[least_bin - 1]) : 0) + uniform(to_top(m, least_bin, s).whole);
                         all = (least_bin ? uniform(s.run_count[least_bin - 1]) : 0) + n;
                     }
                 }
@@ -1026,10 +1043,10 @@ struct Sampler {
                 if (step == 2) token.index = nth_of(row, range.hi, nth, s);
             }
             if (step == 2) {
-                token.mass = mass;
+                token.mass = static_cast<double>(mass);
                 break;
             }
-            mass = before + uniform(to_top(passed + upto, bin, s));
+            mass = before + uniform(to_top(passed + upto, bin, s).whole);
             ++step;
             range.lo = 0;
         }
@@ -1151,7 +1168,7 @@ __global__ __launch_bounds__(kThreads, 4) void sample_join_kernel(SampleArgs a, 
         }
         __syncthreads();
         // (loads that every thread makes: those of all bins are out together)
-        constexpr int kEach = (kBins + kThreads - 1) / kThreads;
+        constexpr int kEach = kBins / kThreads;
         uint64_t m[kEach] = {};
         uint32_t c[kEach] = {};
 #pragma unroll 4
@@ -1159,7 +1176,7 @@ __global__ __launch_bounds__(kThreads, 4) void sample_join_kernel(SampleArgs a, 
             const int below = s.offset[p];
 #pragma unroll
             for (int j = 0; j < kEach; ++j) {
-                const int i = t + kThreads * j, at = i < kBins ? i - below : -1;
+                const int at = t + kThreads * j - below;
                 const uint64_t pm = in[p].mass[at < 0 ? 0 : at];
                 m[j] += at < 0 ? 0 : pm;
                 if (counting) c[j] += at < 0 ? 0 : in[p].count[at];
@@ -1168,7 +1185,6 @@ __global__ __launch_bounds__(kThreads, 4) void sample_join_kernel(SampleArgs a, 
 #pragma unroll
         for (int j = 0; j < kEach; ++j) {
             const int i = t + kThreads * j;
-            if (i >= kBins) continue;
             s.mass[slot_of(sc.top - i)] = m[j];
             s.count[slot_of(sc.top - i)] = c[j];
         }

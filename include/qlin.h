@@ -627,9 +627,10 @@ qlin_status qlin_kv_attention_tree(const void* q, qlin_dtype dtype, int64_t toke
  *   token    out int32 [rows];  logprob  out float [rows] or NULL.
  *   A NaN among the logits counts as -infinity, which is never taken; a row of
  *   nothing else gives token -1 and a NaN.  Several +infinities are equal.
- *   Weights are rounded to 2^-44 of the largest and summed as integers: a token is
- *   that of exact weights unless u or top_p lies within about 2^-40 of a border, and
- *   the same row gives the same token in any call.
+ *   Weights are rounded to 2^-44 of themselves, those below 2^-63 of the largest left
+ *   out, and sums are off by a few 2^-44 of the largest: a token is that of exact
+ *   weights unless u or top_p lies within 2^-40 of the mass from a border, or a weight
+ *   within 2^-40 of itself from min_p.  The same row gives the same token in any call.
  *   workspace  device memory, 16-byte aligned, contents overwritten, of at least
  *            qlin_sample_workspace_bytes(rows, vocab) bytes (else
  *            QLIN_ERR_WORKSPACE), or NULL with workspace_bytes 0: a row is then not

@@ -244,3 +244,51 @@ def test_zeros_among_denormals(vocab, top):
         check(y, (np.arange(rows) + g.random(rows)) / rows, workspace)
         check(y, (np.arange(rows) + g.random(rows))[::-1] / rows, workspace, top_p=g.uniform(0.3, 0.99, rows))
         check(y, g.random(rows), workspace, top_k=g.integers(vocab // 3, vocab, rows))
+
+
+def row_at_a_border(n, share):
+    """A leader and n elements, one to each 32nd part of an octave from ten octaves below it:
+    float32 logits, and a u (or top-p) that asks for 1 + share of the leader's weight."""
+    x = -(np.arange(n) + 320.3) * np.log(2) / 32
+    x = np.concatenate([[0.0], x]).astype(np.float32)
+    w = lambda v: np.exp(np.asarray(v, np.longdouble))  # noqa: E731
+    u = np.float32(1 / float(w(x).sum()))
+    for at in (70, 330):                              # two elements' last bits bring the sum there
+        ulps = np.arange(-4000, 4001)
+        v = (x[at].view(np.int32) + ulps.astype(np.int32)).view(np.float32)
+        total = w(np.delete(x, at)).sum() + w(v)
+        x[at] = v[np.argmin(np.abs(total * np.longdouble(u) - (1 + share)))]
+    return x, u
+
+
+@pytest.mark.parametrize("workspace", [True, False])
+@pytest.mark.parametrize("n,share", [(480, 2.0 ** -37), (480, -2.0 ** -37), (1400, 2.0 ** -36.5), (1400, -2.0 ** -37), (1700, 2.0 ** -37)])
+def test_many_light_elements_at_a_border(n, share, workspace):
+    """What a leader's weight and many far lighter ones sum to, one to a bin: listed at once,
+    and in bins."""
+    x, u = row_at_a_border(n, share)
+    for vocab in (len(x), 16385):                     # (a row that is split, too)
+        y = torch.full((1, -(-vocab // 8) * 8), -np.inf)
+        y[0, vocab - len(x):vocab] = torch.from_numpy(x)
+        y = y.to(DEV)[:, :vocab]
+        check(y, [u], workspace)
+        check(y, [0.9999], workspace, top_p=[u])
+        check(y, [u], workspace, min_p=[1e-30])
+        check(y, [u], workspace, top_k=[vocab - 1])
+
+
+@pytest.mark.parametrize("workspace", [True, False])
+@pytest.mark.parametrize("low", [-31.0, -32.3, -33.0, -40.0])
+def test_a_wide_tail(low, workspace):
+    """2^18 elements that weigh 2^-45 to 2^-58 of the largest each."""
+    vocab = 2 ** 18
+    x = torch.full((2, vocab), low, device=DEV)
+    x[:, 0] = 0.0
+    x[1, 1] = -1e-9
+    if low > -40:
+        check(x, [0.5, 0.5], workspace)
+        check(x, [0.25, 0.75], workspace, top_p=[0.9, 0.5])
+    check(x, [0.25, 0.25], workspace, top_k=[vocab - 5, 2])
+    token, _ = run(x[:1], [1.0], workspace=workspace)
+    # u = 1 - 2^-48: 2^-40 of the mass from the last one, at most
+    assert vocab - 1 - token[0] <= 2.0 ** -40 / np.exp(low) + 1
