@@ -532,7 +532,9 @@ class TreeDecoder:
     that step() can be captured into a graph.
 
     Every sequence has `nodes` nodes a step, the first of them the last token
-    taken (`last`), and room for `tokens` tokens.
+    taken (`last`), and room for `tokens` tokens.  One whose nodes find no room
+    (its row of the table is full, or pages are lacking) takes no token in that
+    step and stays as it is.
     """
 
     def __init__(self, dev, layers: int, batch: int, nodes: int, tokens: int, vocab: int, page_size: int = 16,
@@ -545,7 +547,7 @@ class TreeDecoder:
 
         if vocab % 8:
             raise ValueError("the vocabulary is a multiple of 8")
-        self.q, self.batch, self.nodes, self.vocab, self.hidden = q, batch, nodes, vocab, hidden
+        self.q, self.batch, self.nodes, self.tokens, self.vocab, self.hidden = q, batch, nodes, tokens, vocab, hidden
         cols = -(-(tokens + nodes) // page_size)
         m = batch * nodes
         tdt = {"f16": torch.float16, "bf16": torch.bfloat16}[dtype]
@@ -561,9 +563,10 @@ class TreeDecoder:
         w = synth.device_normal(seed, f"tree_decoder/head/{vocab}x{hidden}", (vocab, hidden), dev, std=hidden ** -0.5)
         self.head = q.qlin_quantize_weights(w, bits=8)
         self.gamma = torch.ones(hidden, device=dev)
-        self.len, self.grown, self.kept = (torch.zeros(batch, **i32) for _ in range(3))
+        self.len, self.got, self.grown, self.kept = (torch.zeros(batch, **i32) for _ in range(4))
+        self.fits = torch.zeros(batch, dtype=torch.bool, device=dev)
         self.want = torch.zeros(batch, **i32)
-        self.last = torch.zeros(batch, **i32)
+        self.last, self.new = torch.zeros(batch, **i32), torch.zeros(batch, **i32)
         self.moved = torch.empty((batch, 2), **i32)
         self.max_kv = cols * page_size
         self.starts = torch.arange(0, m + 1, nodes, **i32)
@@ -579,14 +582,17 @@ class TreeDecoder:
         self.token, self.logprob = torch.empty(m, **i32), torch.empty(m, dtype=torch.float32, device=dev)
         self.sample_ws = q.sample_workspace(m, vocab, dev)
         self.path = (torch.empty((batch, nodes), **i32), torch.empty(batch, **i32), self.last)
+        self.none = torch.full((), -1, **i32)
 
     def prompt(self, tokens, lengths):
         """The cached tokens of each sequence: rows of tokens (int32, on the
-        device) of the given lengths, the last token taken behind them not
-        included."""
+        device) of the given lengths (at most `tokens` each), the last token
+        taken behind them not included."""
         import torch
 
         q = self.q
+        if len(lengths) != self.batch or not all(0 <= n <= self.tokens for n in lengths) or sum(lengths) != tokens.numel():
+            raise ValueError(f"the prompt holds {self.batch} lengths of 0 .. {self.tokens} tokens, as many tokens in all as given")
         new = torch.tensor(lengths, dtype=torch.int32, device=tokens.device)
         q.qlin_kv_resize(self.pool, self.stack, self.table, self.len, new, len_out=self.grown, moved=self.moved)
         starts = torch.cat([new.new_zeros(1), new.cumsum(0).to(torch.int32)])
@@ -601,12 +607,16 @@ class TreeDecoder:
         """One step: parents int32 [batch * nodes]; draft int32 [batch * nodes],
         whose entries at the first nodes are the last tokens taken; u float32
         [batch * nodes].  Returns (path, count, token): self.last becomes the
-        token sampled behind each path, self.len counts its tokens."""
+        token sampled behind each path, self.len counts its tokens.  A sequence
+        that stays as it is has count 0, a path of -1 and its last token."""
         import torch
 
         q = self.q
         torch.add(self.len, self.nodes, out=self.want)
-        q.qlin_kv_resize(self.pool, self.stack, self.table, self.len, self.want, len_out=self.grown, moved=self.moved)
+        q.qlin_kv_resize(self.pool, self.stack, self.table, self.len, self.want, len_out=self.got, moved=self.moved)
+        # a sequence that did not get its new length has none in this step: its nodes lie nowhere
+        torch.eq(self.got, self.want, out=self.fits)
+        torch.mul(self.got, self.fits, out=self.grown)
         q.qlin_tree_plan(parents, self.kv, mask=self.mask, positions=self.positions)
         torch.index_select(self.embed, 0, draft, out=self.residual)
         x = self.zero
@@ -615,7 +625,12 @@ class TreeDecoder:
         q.qlin_add_rmsnorm_quant(x, self.gamma, self.residual, bits=8, out=self.codes)
         q.qlin_gemm_w8a8(*self.codes, *self.head, self.hidden, out=self.logits, workspace=self.head_ws)
         q.qlin_sample(self.logits, u, out=(self.token, self.logprob), workspace=self.sample_ws, **sampling)
-        q.qlin_tree_accept(parents, draft, self.token, self.kv, out=self.path)
-        q.qlin_kv_compact(self.stack, self.kv, self.path[0], self.path[1], kv_len_out=self.kept)
-        q.qlin_kv_resize(self.pool, self.stack, self.table, self.grown, self.kept, len_out=self.len, moved=self.moved)
+        path, count, last = self.path
+        q.qlin_tree_accept(parents, draft, self.token, self.kv, out=(path, count, self.new))
+        q.qlin_kv_compact(self.stack, self.kv, path, count, kv_len_out=self.kept)
+        torch.where(self.fits[:, None], path, self.none, out=path)
+        torch.mul(count, self.fits, out=count)
+        torch.where(self.fits, self.new, last, out=last)
+        torch.where(self.fits, self.kept, self.len, out=self.kept)
+        q.qlin_kv_resize(self.pool, self.stack, self.table, self.got, self.kept, len_out=self.len, moved=self.moved)
         return self.path

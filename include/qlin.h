@@ -562,9 +562,14 @@ qlin_status qlin_kv_attention(const void* q, qlin_dtype dtype, int64_t tokens, i
  * node of its sequence; any other value makes it a root.  Node 0 is the last token
  * already taken, the others are drafted.  All nodes lie in the cache in their
  * order, behind the cached tokens; a node's rotary position is the number of cached
- * tokens plus its depth.  One step: qlin_tree_plan, then in each layer
- * qlin_rope_append_kv (with these positions) and qlin_kv_attention_tree, a token
- * sampled behind every node (qlin_sample), qlin_tree_accept, qlin_kv_compact.
+ * tokens plus its depth.  One step: qlin_kv_resize to the lengths with all nodes,
+ * qlin_tree_plan, then in each layer qlin_rope_append_kv (with these positions) and
+ * qlin_kv_attention_tree, a token sampled behind every node (qlin_sample),
+ * qlin_tree_accept, qlin_kv_compact, qlin_kv_resize to the lengths that this leaves.
+ * A sequence that does not get its new length (len_out is another one: pages are
+ * lacking, or its row of the table ends) has kv_len 0 in that step: with more new
+ * tokens than its length it has no place in the cache, nothing is written for it, its
+ * attention is zeros, and its length, path and token stay the caller's own.
  *
  * qlin_tree_plan -- parents int32 [tokens] to
  *   mask      out uint32 [tokens][mask_ld]: bit j % 32 of word j / 32 of node i's row

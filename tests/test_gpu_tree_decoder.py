@@ -171,3 +171,72 @@ def test_layer_with_a_chain_is_the_layer_without_a_tree():
     torch.cuda.synchronize()
     assert torch.equal(a.stack.caches[0].k, b.stack.caches[0].k) and torch.equal(a.layers[0].qr[:n], b.layers[0].qr[:n])
     assert torch.allclose(a.layers[0].ctx[:n].float(), b.layers[0].ctx[:n].float(), rtol=2.0 ** -10, atol=1e-3)
+
+
+def held_tokens(d, b):
+    """What the caches hold of sequence b's tokens: codes times scales, exactly as stored."""
+    n, out = int(d.len[b]), []
+    pages = d.table[b, :-(-n // 16)].long()
+    for c in d.stack.caches:
+        out += [c.k[pages].transpose(1, 2).flatten(0, 1)[:n].clone(), c.k_scale[pages].clone(),
+                c.v[pages].permute(0, 3, 1, 2).flatten(0, 1)[:n].clone(), c.v_scale[pages].clone()]
+    return out
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_sequences_without_room_stay_as_they_are(captured):
+    """Steps up to and past the end of the first row's pages, and without free pages: the
+    sequences that do not get them take no token and keep what they hold, the others go on."""
+    d = TreeDecoder(torch.device(DEV), layers=2, batch=3, nodes=7, tokens=60, vocab=1000, dtype="f16")
+    g = np.random.default_rng(12)
+    d.prompt(i32(g.integers(0, d.vocab, 93)), [60, 32, 1])
+    d.last.copy_(i32(g.integers(0, d.vocab, 3)))
+    n = d.batch * d.nodes
+    args = (torch.zeros(n, dtype=torch.int32, device=DEV), torch.zeros(n, dtype=torch.int32, device=DEV), torch.zeros(n, device=DEV))
+    step = lambda: d.step(*args)  # noqa: E731
+    if captured:
+        for layer in d.layers:
+            layer.workspace(n)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            d.step(*args)
+        step = lambda: graph.replay() or d.path  # noqa: E731
+    room = d.table.shape[1] * 16
+    stayed = went = 0
+    for t in range(30):
+        parents, draft, u = inputs(d, g)
+        for x, y in zip(args, (i32(parents), i32(draft), torch.from_numpy(u).to(DEV))):
+            x.copy_(y)
+        none_free = t >= 26
+        if none_free:                                  # (as if other rows held them)
+            d.pool.free_bits.zero_()
+        lens, last, table = d.len.tolist(), d.last.tolist(), d.table.clone()
+        before = [held_tokens(d, b) for b in range(d.batch)]
+        path, count, token = step()
+        torch.cuda.synchronize()
+        for b in range(d.batch):
+            fits = lens[b] + d.nodes <= room and not (none_free and -(-(lens[b] + d.nodes) // 16) > -(-lens[b] // 16))
+            took = int(count[b])
+            assert (took > 0) == fits, (t, b)
+            assert int(d.len[b]) == lens[b] + took
+            pages = -(-lens[b] // 16)
+            if fits:
+                went += 1
+                assert path[b, :1].tolist() == [0] and torch.all(path[b, took:] == -1)
+            else:
+                stayed += 1
+                assert torch.all(path[b] == -1) and int(token[b]) == last[b]
+                assert torch.equal(d.table[b], table[b])
+                assert all(torch.equal(x, y) for x, y in zip(held_tokens(d, b), before[b])), (t, b)
+            assert torch.equal(d.table[b, :pages], table[b, :pages]) and torch.all(d.table[b, -(-int(d.len[b]) // 16):] == -1)
+    assert stayed > 8 and went > 40
+
+
+def test_prompts_past_the_room_are_refused():
+    d = TreeDecoder(torch.device(DEV), layers=1, batch=2, nodes=3, tokens=20, vocab=1000)
+    tokens = i32(np.arange(30))
+    for lengths in ([21, 9], [30], [10, 10], [31, -1], [10, 10, 10]):
+        with pytest.raises(ValueError, match="prompt"):
+            d.prompt(tokens, lengths)
+    d.prompt(tokens, [20, 10])
+    assert d.len.tolist() == [20, 10]
