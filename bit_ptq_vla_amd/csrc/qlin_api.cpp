@@ -323,7 +323,8 @@ qlin::KvStackArgs stack_args(const qlin_kv_cache* c, int32_t layers, int32_t at)
     return a;
 }
 
-// Checks and launch of the two attention entry points (tree: with a mask).
+// Checks and launch of the two attention entry points (tree: with a mask, null where no
+// sequence has a new token).
 int64_t attention_bytes(int32_t heads_q, const qlin_kv_cache* cache, const qlin_kv_batch* batch, bool tree) {
     if (kv_check(cache, batch, 0, heads_q) != QLIN_OK) return -1;
     const qlin::KvAttnPlan plan = (tree ? qlin::plan_kv_attention_tree : qlin::plan_kv_attention)(
@@ -332,9 +333,9 @@ int64_t attention_bytes(int32_t heads_q, const qlin_kv_cache* cache, const qlin_
 }
 
 qlin_status attention(const void* q, qlin_dtype dtype, int64_t tokens, int64_t ldq, int32_t heads_q,
-                      const qlin_kv_cache* cache, const qlin_kv_batch* batch, const uint32_t* mask, int64_t mask_ld,
-                      float sm_scale, float softcap, void* out, int64_t ldo, void* workspace, int64_t workspace_bytes,
-                      void* stream) {
+                      const qlin_kv_cache* cache, const qlin_kv_batch* batch, bool tree, const uint32_t* mask,
+                      int64_t mask_ld, float sm_scale, float softcap, void* out, int64_t ldo, void* workspace,
+                      int64_t workspace_bytes, void* stream) {
     qlin_status st = kv_check(cache, batch, tokens, heads_q);
     if (st != QLIN_OK) return st;
     if (tokens > 0 && (!q || !out)) return QLIN_ERR_NULL;
@@ -347,7 +348,7 @@ qlin_status attention(const void* q, qlin_dtype dtype, int64_t tokens, int64_t l
     if (ldq % 8 != 0 || ldq < wide || ldo % 8 != 0 || ldo < wide || workspace_bytes < 0) return QLIN_ERR_SHAPE;
     if (!workspace && workspace_bytes > 0) return QLIN_ERR_NULL;
     if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return QLIN_ERR_ALIGN;
-    const qlin::KvAttnPlan plan = (mask ? qlin::plan_kv_attention_tree : qlin::plan_kv_attention)(
+    const qlin::KvAttnPlan plan = (tree ? qlin::plan_kv_attention_tree : qlin::plan_kv_attention)(
         batch->batch, batch->max_q, batch->max_kv, heads_q, cache->heads, cache->head_dim, workspace != nullptr);
     if (plan.blocks > kMaxAttnBlocks) return QLIN_ERR_SHAPE;
     if (workspace && workspace_bytes < plan.ws_bytes) return QLIN_ERR_WORKSPACE;
@@ -356,13 +357,13 @@ qlin_status attention(const void* q, qlin_dtype dtype, int64_t tokens, int64_t l
     const Span outs[2] = {{out, tokens > 0 ? ((tokens - 1) * ldo + wide) * 2 : 0}, {workspace, workspace_bytes}};
     Span ins[10] = {{q, tokens > 0 ? ((tokens - 1) * ldq + wide) * 2 : 0}, {cache->k, codes}, {cache->v, codes},
                    {cache->k_scale, scales}, {cache->v_scale, scales},
-                   {mask, tokens > 0 ? ((tokens - 1) * mask_ld + (batch->max_q + 31) / 32) * 4 : 0}};
+                   {mask, tree && tokens > 0 ? ((tokens - 1) * mask_ld + (static_cast<int64_t>(batch->max_q) + 31) / 32) * 4 : 0}};
     kv_index_spans(cache, batch, ins + 6);
     if (any_overlap(outs, 2, ins, 10)) return QLIN_ERR_ALIAS;
     if (tokens == 0 || batch->batch == 0 || batch->max_q == 0) return QLIN_OK;
     st = check_device();
     if (st != QLIN_OK) return st;
-    if (mask)
+    if (tree)
         return map_err(qlin::launch_kv_attention_tree(plan, q, dtype, ldq, heads_q, kv_index(cache, batch, tokens),
                                                       cache->k, cache->v, cache->k_scale, cache->v_scale, cache->heads,
                                                       cache->head_dim, sm_scale, softcap, mask, mask_ld, out, ldo,
@@ -767,7 +768,7 @@ int64_t qlin_kv_attention_workspace_bytes(int32_t heads_q, const qlin_kv_cache* 
 qlin_status qlin_kv_attention(const void* q, qlin_dtype dtype, int64_t tokens, int64_t ldq, int32_t heads_q,
                               const qlin_kv_cache* cache, const qlin_kv_batch* batch, float sm_scale, float softcap,
                               void* out, int64_t ldo, void* workspace, int64_t workspace_bytes, void* stream) {
-    return attention(q, dtype, tokens, ldq, heads_q, cache, batch, nullptr, 0, sm_scale, softcap, out, ldo, workspace,
+    return attention(q, dtype, tokens, ldq, heads_q, cache, batch, false, nullptr, 0, sm_scale, softcap, out, ldo, workspace,
                      workspace_bytes, stream);
 }
 
@@ -781,13 +782,13 @@ qlin_status qlin_kv_attention_tree(const void* q, qlin_dtype dtype, int64_t toke
                                    const qlin_kv_cache* cache, const qlin_kv_batch* batch, const uint32_t* mask,
                                    int64_t mask_ld, float sm_scale, float softcap, void* out, int64_t ldo,
                                    void* workspace, int64_t workspace_bytes, void* stream) {
-    if (!batch || !mask) return QLIN_ERR_NULL;
+    if (!batch || (tokens > 0 && batch->max_q > 0 && !mask)) return QLIN_ERR_NULL;
     if (batch->prefix_len) return QLIN_ERR_UNSUPPORTED;
     if (batch->max_q > qlin::kMaxTreeNodes || mask_ld < (static_cast<int64_t>(batch->max_q) + 31) / 32 ||
         mask_ld > 0x7FFFFFFF)
         return QLIN_ERR_SHAPE;
     if (!aligned4(mask)) return QLIN_ERR_ALIGN;
-    return attention(q, dtype, tokens, ldq, heads_q, cache, batch, mask, mask_ld, sm_scale, softcap, out, ldo,
+    return attention(q, dtype, tokens, ldq, heads_q, cache, batch, true, mask, mask_ld, sm_scale, softcap, out, ldo,
                      workspace, workspace_bytes, stream);
 }
 
@@ -809,7 +810,7 @@ qlin_status qlin_tree_plan(const int32_t* parents, int64_t tokens, const qlin_kv
                            int64_t mask_ld, int32_t* positions, void* stream) {
     qlin_status st = tree_check(batch, tokens);
     if (st != QLIN_OK) return st;
-    if (tokens > 0 && (!parents || !mask || !positions)) return QLIN_ERR_NULL;
+    if (tokens > 0 && (!parents || (batch->max_q > 0 && !mask) || !positions)) return QLIN_ERR_NULL;
     const int64_t words = (static_cast<int64_t>(batch->max_q) + 31) / 32;
     if (mask_ld < words || mask_ld > 0x7FFFFFFF) return QLIN_ERR_SHAPE;
     if (!aligned4(parents) || !aligned4(mask) || !aligned4(positions)) return QLIN_ERR_ALIGN;
@@ -830,7 +831,7 @@ qlin_status qlin_tree_accept(const int32_t* parents, const int32_t* draft, const
     if (st != QLIN_OK) return st;
     if (tokens > 0 && (!parents || !draft || !sampled)) return QLIN_ERR_NULL;
     const int64_t n = batch->batch;
-    if (n > 0 && (!path || !count || !token)) return QLIN_ERR_NULL;
+    if (n > 0 && ((batch->max_q > 0 && !path) || !count || !token)) return QLIN_ERR_NULL;
     if (path_ld < batch->max_q || path_ld > 0x7FFFFFFF) return QLIN_ERR_SHAPE;
     if (!aligned4(parents) || !aligned4(draft) || !aligned4(sampled) || !aligned4(path) || !aligned4(count) ||
         !aligned4(token))
@@ -967,7 +968,7 @@ qlin_status qlin_kv_compact(const qlin_kv_cache* caches, int32_t layers, const q
     st = kv_check(&caches[0], batch, 0, caches[0].heads);
     if (st != QLIN_OK) return st;
     const int64_t n = batch->batch;
-    if (n > 0 && (!path || !count)) return QLIN_ERR_NULL;
+    if (n > 0 && ((batch->max_q > 0 && !path) || !count)) return QLIN_ERR_NULL;
     if (batch->max_q > qlin::kMaxTreeNodes || path_ld < batch->max_q || path_ld > 0x7FFFFFFF) return QLIN_ERR_SHAPE;
     const int64_t wide = layers < qlin::kMaxStackLayers ? layers : qlin::kMaxStackLayers;
     if (n * wide * caches[0].heads > kMaxAttnBlocks) return QLIN_ERR_SHAPE;

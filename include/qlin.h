@@ -585,7 +585,8 @@ qlin_status qlin_kv_attention(const void* q, qlin_dtype dtype, int64_t tokens, i
  *   count     out int32 [batch]: nodes of the path (0 without new tokens).
  *   token     out int32 [batch]: the token sampled behind its last node, -1 without.
  * Of batch, q_start, kv_len, batch, max_q and max_kv are read.  Index arrays are
- * 4-byte aligned.  One launch each; rows of no sequence stay as they are.
+ * 4-byte aligned.  One launch each; rows of no sequence stay as they are.  Arrays
+ * that hold nothing (no tokens, or max_q 0), here and below, may be NULL.
  */
 #define QLIN_MAX_TREE_NODES 1024
 qlin_status qlin_tree_plan(const int32_t* parents, int64_t tokens, const qlin_kv_batch* batch, uint32_t* mask,

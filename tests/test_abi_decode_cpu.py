@@ -306,3 +306,16 @@ def test_decode_validation_under_asan_and_ubsan(tmp_path):
     out = r.stdout + r.stderr
     assert r.returncode == 0, out[-4000:]
     assert " passed" in r.stdout and "ERROR: AddressSanitizer" not in out and "runtime error:" not in out
+
+
+# ---- calls in which no sequence has a new token: arrays that hold nothing may be null
+
+def test_calls_without_new_tokens_take_empty_arrays(lib):
+    none = batch(max_q=0)
+    assert tree(lib, tokens=0, x=None, out=None, mask=None) == q.QLIN_OK
+    assert tree(lib, tokens=0, x=None, out=None, mask=None, b=none, ldm=0) == q.QLIN_OK
+    assert tree(lib, b=none, mask=None, ldm=0) == q.QLIN_OK
+    assert plan(lib, b=none, mask=None, ld=0) == q.QLIN_OK
+    # what would be read or written is still asked for
+    assert tree(lib, mask=None) == plan(lib, mask=None) == accept(lib, path=None) == compact(lib, path=None) == q.QLIN_ERR_NULL
+    assert tree(lib, b=none, mask=None, ldm=-1) == plan(lib, b=none, mask=None, ld=-1) == q.QLIN_ERR_SHAPE

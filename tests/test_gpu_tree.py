@@ -242,3 +242,29 @@ def test_captured_and_on_another_stream():
         again = q.qlin_kv_attention_tree(x, c.cache, batch, 8, mask)
     side.synchronize()
     assert torch.equal(again, want)
+
+
+@pytest.mark.parametrize("tokens", [0, 3])
+def test_steps_without_new_tokens(tokens):
+    """A batch none of whose sequences has a new token: nothing is written but counts and lengths."""
+    c = Cache(6, 16, 2, 64)
+    kv = [20, 0, 33]
+    batch = q.KvBatch(i32(c.table(3, 2)), i32([0, 0, 0, 0]), i32(kv), max_q=0, max_kv=32)
+    parents = i32(np.zeros(tokens))
+    mask, positions = q.qlin_tree_plan(parents, batch, positions=torch.full((tokens,), 7, dtype=torch.int32, device=DEV))
+    assert mask.shape == (tokens, 0) and positions.tolist() == [7] * tokens
+    x = queries(tokens, 4 * 64, "f16", "none").to(DEV) if tokens else torch.empty((0, 256), dtype=torch.float16, device=DEV)
+    out = torch.full_like(x, 5.0)
+    q.qlin_kv_attention_tree(x, c.cache, batch, 4, mask, out=out)
+    path, count, token = q.qlin_tree_accept(parents, parents, parents, batch)
+    assert path.shape == (3, 0) and count.tolist() == [0] * 3 and token.tolist() == [-1] * 3
+    assert q.qlin_kv_compact(q.KvStack([c.cache]), batch, path, count).tolist() == [20, 0, 32]
+    torch.cuda.synchronize()
+    assert torch.all(out == 5.0)
+    for name in ("k_scale", "v_scale", "k", "v"):
+        assert np.array_equal(getattr(c.cache, name).cpu().numpy(), c.host[name]), name
+    # the same with room for one, and no token at all
+    if tokens == 0:
+        one = q.KvBatch(batch.page_table, batch.q_start, batch.kv_len, max_q=1, max_kv=32)
+        mask, _ = q.qlin_tree_plan(parents, one)
+        assert q.qlin_kv_attention_tree(x, c.cache, one, 4, mask).shape == (0, 256)
