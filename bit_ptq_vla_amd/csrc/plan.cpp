@@ -170,17 +170,25 @@ int64_t composite_calib_work_bytes(int64_t n, int64_t k, int b) {
     return (chunks * k + k + k * b) * 8;
 }
 
+// Few long rows are split over blocks, in parts of a multiple of kSamplePartLogits (what
+// a block takes at a time), while that gives no more blocks than CUs.  A second launch
+// joins them, which four parts pay for, three from 81920 logits on, two from 131072.
+// Measured, us for a block to a row / for parts, top-p and a temperature:
+//   4 parts: fp16, 1 row 49153 logits 37 / 35, 64000 32 / 30; 64 rows 64000 35 / 35, 128256 58 / 50, 257152 99 / 77
+//   more:    fp16, 1 row in 8 128256 50 / 40, in 16 257152 88 / 62; fp32 59 / 44, 105 / 67
+//   3 parts: fp16, 1 row 48000 33 / 34; 85 rows 81920 42 / 42, 96000 50 / 48, 257152 98 / 84; fp32 49 / 51, 56 / 55, 141 / 121
+//   2 parts: fp16, 1 row 32000 21 / 23; 128 rows 64000 36 / 38, 128256 59 / 58, 257152 98 / 88; fp32 43 / 47, 79 / 78, 144 / 129
+// (8192 logits to a part: 32000 in 4 21 / 23, 257152 in 32 88 / 67.)
 SamplePlan plan_sample(int64_t rows, int64_t vocab, bool allow_split) {
-    SamplePlan p{1, static_cast<int>(vocab), 0};
-    const int64_t step = 4096, most = (vocab + 2 * step - 1) / (2 * step);
+    const SamplePlan whole{1, static_cast<int>(vocab), 0};
+    const int64_t most = (vocab + kSamplePartLogits - 1) / kSamplePartLogits;
     int64_t parts = allow_split && rows > 0 ? device_cus() / rows : 1;
     parts = parts < most ? parts : most;
-    parts = parts < kMaxSampleParts ? parts : kMaxSampleParts;
-    if (parts < 2) return p;
-    p.size = static_cast<int>(((vocab + parts - 1) / parts + step - 1) / step * step);
-    p.parts = static_cast<int>((vocab + p.size - 1) / p.size);
-    p.ws_bytes = p.parts > 1 ? rows * p.parts * kSamplePartBytes : 0;
-    return p;
+    if (parts < 2) return whole;
+    const int64_t size = ((vocab + parts - 1) / parts + kSamplePartLogits - 1) / kSamplePartLogits * kSamplePartLogits;
+    parts = (vocab + size - 1) / size;
+    if (vocab < (parts == 2 ? 131072 : parts == 3 ? 81920 : 0)) return whole;
+    return {static_cast<int>(parts), static_cast<int>(size), rows * parts * kSamplePartBytes};
 }
 
 // The rest of a plan: `heads` (sequence, kv head) pairs of row_tiles tiles each, and

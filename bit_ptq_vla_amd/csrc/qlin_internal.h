@@ -157,7 +157,8 @@ struct SampleArgs {
     float* logprob;
 };
 constexpr int64_t kSamplePartBytes = 16 + kSampleBins * 12;
-constexpr int kMaxSampleParts = 64;
+constexpr int kSamplePartLogits = 16384;     // a part's are a multiple of these
+constexpr int kMaxSampleParts = kMaxVocab / kSamplePartLogits;
 struct SamplePlan {
     int parts, size;          // blocks to a row, and the logits that each takes
     int64_t ws_bytes;

@@ -640,7 +640,7 @@ qlin_status qlin_kv_attention_tree(const void* q, qlin_dtype dtype, int64_t toke
  *   workspace  device memory, 16-byte aligned, contents overwritten, of at least
  *            qlin_sample_workspace_bytes(rows, vocab) bytes (else
  *            QLIN_ERR_WORKSPACE), or NULL with workspace_bytes 0: a row is then not
- *            split over blocks, which is slower for few rows.  Calls (and replays of
+ *            split over blocks, which is slower for few long rows.  Calls (and replays of
  *            captured calls) that can run at the same time need different ones.
  * Preconditions: rows 0 .. 2^21; vocab 1 .. 2^18; ld >= vocab.  Outputs overlap no
  * input.  The arrays of settings are 4-byte aligned.

@@ -319,3 +319,16 @@ def test_calls_without_new_tokens_take_empty_arrays(lib):
     # what would be read or written is still asked for
     assert tree(lib, mask=None) == plan(lib, mask=None) == accept(lib, path=None) == compact(lib, path=None) == q.QLIN_ERR_NULL
     assert tree(lib, b=none, mask=None, ldm=-1) == plan(lib, b=none, mask=None, ld=-1) == q.QLIN_ERR_SHAPE
+
+
+def test_short_rows_of_logits_take_no_workspace(lib):
+    size = lib.qlin_sample_workspace_bytes
+    assert all(size(rows, vocab) == 0 for rows in (1, 16, 128) for vocab in (1, 32000, 49152))
+    assert size(1, 49153) > 0 and size(64, 49153) > 0 and size(65, 49153) == 0
+    assert size(85, 81919) == 0 and size(85, 81920) > 0
+    assert size(128, (1 << 17) - 1) == 0 and size(128, 1 << 17) > 0 and size(129, 1 << 18) == 0
+    for rows in range(1, 129):
+        for vocab in (49153, 65536, 65537, 81920, 98304, 98305, 131071, 131072, 200000, 1 << 18):
+            part = 16 + 2048 * 12
+            parts = size(rows, vocab) // rows // part
+            assert size(rows, vocab) == rows * parts * part and parts * rows <= 256 and parts <= 16 and parts != 1

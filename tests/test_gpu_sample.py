@@ -267,7 +267,7 @@ def test_many_light_elements_at_a_border(n, share, workspace):
     """What a leader's weight and many far lighter ones sum to, one to a bin: listed at once,
     and in bins."""
     x, u = row_at_a_border(n, share)
-    for vocab in (len(x), 16385):                     # (a row that is split, too)
+    for vocab in (len(x), 50001):                     # (a row that is split, too)
         y = torch.full((1, -(-vocab // 8) * 8), -np.inf)
         y[0, vocab - len(x):vocab] = torch.from_numpy(x)
         y = y.to(DEV)[:, :vocab]
@@ -292,3 +292,56 @@ def test_a_wide_tail(low, workspace):
     token, _ = run(x[:1], [1.0], workspace=workspace)
     # u = 1 - 2^-48: 2^-40 of the mass from the last one, at most
     assert vocab - 1 - token[0] <= 2.0 ** -40 / np.exp(low) + 1
+
+
+@pytest.mark.parametrize("rows,vocab", [(1, 49153), (2, 50001), (64, 49999), (65, 49999), (85, 81927), (3, 65544), (128, 131072), (17, 131079), (1, 2 ** 18)])
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+def test_split_rows(rows, vocab, dtype):
+    """Rows that are split over blocks, and those next to them that are not: the same tokens,
+    and the oracle's."""
+    x, g = draw(rows, vocab, dtype, rows + vocab)
+    u = g.random(rows).astype(np.float32)
+    s = dict(temperature=g.uniform(0.5, 1.3, rows), top_k=g.integers(1, 400, rows), top_p=g.uniform(0.6, 1.1, rows),
+             min_p=np.where(g.random(rows) < 0.5, 0.0, g.uniform(0.0, 0.05, rows)))
+    s["temperature"][::5] = 0.0
+    s["top_k"][::3] = 0
+    few = slice(0, 4)
+    for names in ((), ("temperature",), ("temperature", "top_p"), ("top_k",), tuple(s)):
+        now = {n: s[n] for n in names}
+        split, whole = run(x, u, **now), run(x, u, workspace=False, **now)
+        assert np.array_equal(split[0], whole[0]) and np.array_equal(split[1], whole[1], equal_nan=True)
+        check(x[few], u[few], **{n: v[few] for n, v in now.items()})
+
+
+def test_split_rows_with_masks_flat_parts_and_captured():
+    inf, nan = float("inf"), float("nan")
+    rows, vocab = 6, 70000
+    x, g = draw(rows, vocab, "f32", 31)
+    x = copy(x)
+    x[0, :40000] = -inf                                # parts without an element
+    x[1, 30000:] = 0.5                                 # equal logits over parts
+    x[2, 5:] = nan
+    x[3] = -inf
+    x[4, ::2] = -1e30                                  # parts whose largest lies far below
+    x[4, 20000:] = -1e30
+    x[5, 100] = x[5, 69999] = inf
+    u = np.array([0.7, 0.6, 0.9, 0.5, 0.999, 0.6], np.float32)
+    assert q.sample_workspace(rows, vocab, DEV) is not None
+    for s in ({}, dict(top_p=np.full(rows, 0.8)), dict(top_k=[60000] * rows, temperature=np.full(rows, 0.7)), dict(temperature=np.zeros(rows))):
+        check(x, u, **s)
+        check(x, u, workspace=False, **s)
+    du, work = dev(u), q.sample_workspace(rows, vocab, DEV)
+    out = (torch.empty(rows, dtype=torch.int32, device=DEV), torch.empty(rows, device=DEV))
+    y = copy(x)
+    graph = torch.cuda.CUDAGraph()
+    q.qlin_sample(y, du, out=out, workspace=work)
+    with torch.cuda.graph(graph):
+        q.qlin_sample(y, du, out=out, workspace=work)
+    for k in range(3):
+        y.copy_(x.roll(k, 0))
+        want = run(y, u)
+        work.fill_(255)
+        out[0].fill_(-7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(out[0].cpu().numpy(), want[0]) and np.array_equal(out[1].cpu().numpy(), want[1], equal_nan=True)
