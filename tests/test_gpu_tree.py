@@ -268,3 +268,22 @@ def test_steps_without_new_tokens(tokens):
         one = q.KvBatch(batch.page_table, batch.q_start, batch.kv_len, max_q=1, max_kv=32)
         mask, _ = q.qlin_tree_plan(parents, one)
         assert q.qlin_kv_attention_tree(x, c.cache, one, 4, mask).shape == (0, 256)
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: f"{c[0]}-{c[1]}-{c[2]}-{c[3]}-p{c[4]}-cap{c[5]}-{len(c[6])}")
+def test_chain_and_causal_attention(case):
+    """A chain's mask row is the causal one: where blocks of 16 rows take both calls the products
+    and sums come in one order, and the outputs are the same bits; elsewhere both are within the
+    derived tolerance of the oracle, and so of each other within its double."""
+    dtype, hq, hkv, d, page, cap, seqs = case
+    c, table, start, kv, _, x, batch = setup(case)
+    chain = np.concatenate([np.arange(n) - 1 for n, _ in seqs])
+    mask, _ = q.qlin_tree_plan(i32(chain), batch)
+    tree = q.qlin_kv_attention_tree(x, c.cache, batch, hq, mask, softcap=cap)
+    causal = q.qlin_kv_attention(x, c.cache, batch, hq, softcap=cap)
+    torch.cuda.synchronize()
+    if case in CASES[:11]:
+        assert torch.equal(tree, causal)
+    sees = make_sees(chain, start, max(1, batch.max_q))
+    for out in (tree, causal):
+        check(out, x, c, table, start, kv, hq, sees, d ** -0.5, cap, dtype)
