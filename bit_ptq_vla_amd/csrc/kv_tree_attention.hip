@@ -12,7 +12,10 @@ namespace {
 // waves take the range's 64-key steps in turn and join through LDS, 16 rows at a time.
 // A wave holds all of the rows, so that a step's codes are read and expanded to fp16
 // once for NQ products with 16 queries each: expanding them (20 vector instructions to
-// 16 codes) costs as much as the softmax of 16 rows.
+// 16 codes) costs as much as the softmax of 16 rows.  As in that attention, a weight times
+// its page's v scale is rounded to fp16 before the product with v's codes, for the matrix
+// units' rate: by 2^-11 of itself, or 2^-25 of the largest in its row; the sum of the
+// weights takes them unrounded, in fp32.
 //
 // Bound by latency where there is little (16 nodes over 816 keys of 32 heads, 7 MB: 11
 // us, a join among them), by the vector units' issue where there is much: 64 trees of up

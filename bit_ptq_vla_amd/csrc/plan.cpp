@@ -179,6 +179,8 @@ int64_t composite_calib_work_bytes(int64_t n, int64_t k, int b) {
 //   3 parts: fp16, 1 row 48000 33 / 34; 85 rows 81920 42 / 42, 96000 50 / 48, 257152 98 / 84; fp32 49 / 51, 56 / 55, 141 / 121
 //   2 parts: fp16, 1 row 32000 21 / 23; 128 rows 64000 36 / 38, 128256 59 / 58, 257152 98 / 88; fp32 43 / 47, 79 / 78, 144 / 129
 // (8192 logits to a part: 32000 in 4 21 / 23, 257152 in 32 88 / 67.)
+// Two blocks to a CU, 130 rows in 3: 131072 56 / 61, 257152 98 / 95, fp32 78 / 81, 143 / 133;
+// 192 rows in 2: 59 / 67, 100 / 106, fp32 82 / 89, 149 / 148.
 SamplePlan plan_sample(int64_t rows, int64_t vocab, bool allow_split) {
     const SamplePlan whole{1, static_cast<int>(vocab), 0};
     const int64_t most = (vocab + kSamplePartLogits - 1) / kSamplePartLogits;

@@ -114,7 +114,7 @@ hipError_t launch_rope_table(float* table, int64_t positions, int rot, double ba
 // joined by a second kernel).
 struct KvAttnPlan {
     bool many;                // 256 query rows (128 of a 256-wide head) to a block; else
-    int tile;                 // 16 of them (of a tree 16, 32 or 64)
+    int tile;                 // 16 of them (of a tree 16 or 32)
     int lds_bytes;            // of the 16-row blocks
     int row_tiles, splits, split_keys;
     int even;                 // blocks that share a tree's work evenly (many), or 0

@@ -34,11 +34,12 @@
 // A block takes a row, or a part of one where rows are few (the parts' bins then
 // meet in a second launch).
 //
-// Bound by the pass that fills the bins, about 25 vector instructions and an LDS atomic
-// (two with a top-k) to a logit, and behind it by a chain of scans and barriers, 10 to 20
-// us: 1024 rows of 32003 bf16 logits with mixed filters (66 MB) take 48 us, 256 of
-// 257152 fp32 logits without any (263 MB, read again for the last bin) 130, one of 32000
-// 26.
+// Bound by waiting: the pass that fills the bins takes about 25 vector instructions and
+// an LDS atomic (two with a top-k) to a logit, and a chain of scans and barriers follows,
+// 10 to 20 us.  1024 rows of 32003 bf16 logits with mixed filters (66 MB) take 51 us,
+// vector units 28% busy, waves waiting 59% of their time; 256 of 257152 fp32 logits
+// without any (263 MB, read again for the last bin) 133, two waves to a SIMD, 34% and 57%,
+// 5.9 conflict cycles to an LDS instruction; one of 32000 21.
 
 #include "device_common.h"
 #include "qlin_internal.h"
